@@ -17,8 +17,8 @@
  *
  * Conventions shared by every entry point
  * ---------------------------------------
- *  - All tensor pointers are DEVICE pointers to dense fp32 arrays owned by the
- *    caller; each must be 16-byte aligned.  Outputs are fully overwritten (no
+ *  - All tensor pointers are DEVICE pointers to dense arrays, fp32 unless a
+ *    call says otherwise, owned by the caller; each must be 16-byte aligned.  Outputs are fully overwritten (no
  *    zeroing needed, prior contents never read).  The library keeps no pointer
  *    after a call returns.
  *  - Layout is token-major: x[T][S][H], element (t,k,i) at (t*S+k)*H+i, so one
@@ -354,6 +354,137 @@ int mhc_site_pre_zq8_check(const float* x, const float* fn_w, const float* scale
                            int iters, float eps, float norm_eps, const float* pre,
                            const float* post, const float* comb, const float* y, const float* z,
                            const signed char* q, const float* d);
+
+/*
+ * 8-bit blocks: activation checkpoints, and the operands of the 8-bit product.
+ *
+ * An encoded matrix of `rows` x `cols` is
+ *   codes  [rows][P]      e4m3 (4 exponent bits of bias 7, 3 mantissa bits, no
+ *                         infinity), P = cols rounded up to 128, zero past cols
+ *   scales [rows][P/128]  one byte per block of 128 consecutive columns: e + 127,
+ *                         the block's values being code * 2^e
+ * or, in its SQUARE form, the same codes with one scale per 128 x 128 square:
+ *   scales [ceil(rows/128)][P/128].
+ * Of a block with largest finite magnitude a, e is the least integer >= -126
+ * with a <= 448 * 2^e (0 where a = 0), and code = x * 2^-e rounded to nearest,
+ * ties to even; an infinity or a NaN encodes as NaN.  A power of two moves only
+ * exponents, so every code has the relative rounding of e4m3 itself, and decoded
+ * values are exact in fp32 (but that an entry above 248 * 2^120 = 3.296e38
+ * rounds to 2^128, which fp32 holds as an infinity).  The calls take scale bytes as encode writes them
+ * (1 .. 247).
+ *
+ * mhc_f8_encode: x [rows][cols] (MHC_F32 or MHC_BF16) into codes / scales and, in
+ *   the same pass, its transpose into codes_t [cols][Pt], scales_t
+ *   [cols][Pt/128], Pt = rows rounded up to 128 (blocks along the rows of x; the
+ *   form a product needs that sums over rows).  Either pair may be NULL, not
+ *   both.  With square != 0 both use one scale per square (scales_t
+ *   [P/128][Pt/128]), so codes_t is the exact transpose of codes: the form for
+ *   weights.
+ * mhc_f8_repack: the transpose of an encoded (not square) matrix, decoded and
+ *   encoded again along the other axis: what mhc_f8_encode of the decoded
+ *   matrix writes to codes_t, scales_t.
+ * mhc_f8_decode: the values, fp32 [rows][cols].
+ * mhc_f8_matmul: out[m][n] = sum_k A[m][k] * B[n][k], fp32 sums, out [M][N] of
+ *   out_type MHC_F32 or MHC_BF16 (rounded to nearest even).  a, a_scales: M rows
+ *   of K codes; b, b_scales: N rows, in the square form if b_square != 0.  K is
+ *   a multiple of 128 (the padded width of both; K = 0 gives zeros).  Products
+ *   are exact and the k blocks are summed in an order fixed by the shape; an
+ *   operand value under 2^-126 may count as zero.
+ * Training uses: forward z W^T: b = W.  Input gradient df W: a = df,
+ *   b = codes_t of W.  Weight gradient df^T z: a = codes_t of df, b = codes_t of
+ *   z (from mhc_f8_repack of the kept codes).
+ *
+ * cols % 4 == 0 and N % 4 == 0 (MHC_EALIGN), K % 128 == 0 (MHC_EALIGN); at most
+ * 2^28 columns, 2^28 blocks in all, M * N < 2^31 and K <= 2^28
+ * (MHC_EUNSUPPORTED); rows = 0 or M = 0 does nothing.  Pointers are 16-byte
+ * aligned; outputs must not overlap inputs or each other.  No scratch.
+ */
+enum { MHC_F32 = 0, MHC_BF16 = 1 };
+
+int mhc_f8_encode(const void* x, int x_type, int rows, int cols, int square,
+                  unsigned char* codes, unsigned char* scales, unsigned char* codes_t,
+                  unsigned char* scales_t, void* stream);
+int mhc_f8_repack(const unsigned char* codes, const unsigned char* scales, int rows, int cols,
+                  unsigned char* codes_t, unsigned char* scales_t, void* stream);
+int mhc_f8_decode(const unsigned char* codes, const unsigned char* scales, int rows, int cols,
+                  float* out, void* stream);
+int mhc_f8_matmul(const unsigned char* a, const unsigned char* a_scales, const unsigned char* b,
+                  const unsigned char* b_scales, int b_square, int M, int N, int K, void* out,
+                  int out_type, void* stream);
+
+/*
+ * mhc_site_post_bwd -- the gradient of mhc_site_post.  With g = dL/dx_out:
+ *   dx[t,j,i]    = sum_k comb[t,j,k] * g[t,k,i]
+ *   df[t,i]      = sum_k post[t,k] * g[t,k,i]
+ *   dpost[t,k]   = sum_i g[t,k,i] * f[t,i]
+ *   dcomb[t,j,k] = sum_i x[t,j,i] * g[t,k,i]
+ *
+ * Arguments:
+ *   g         [T][S][H]  gradient of the site's output state (read only)
+ *   x         [T][S][H]  the site's input state: fp32 with x_scales NULL, or the
+ *   x_scales             codes and scales of its 8-bit checkpoint (mhc_f8_encode
+ *                        of the matrix [T*S][H])
+ *   f         [T][H]     the branch output, fp32 with f_scales NULL, or its
+ *   f_scales             8-bit checkpoint
+ *   post [T][S], comb [T][S][S]  the gates of the forward pass (read only)
+ *   dx [T][S][H], df [T][H], dpost [T][S], dcomb [T][S][S]   out
+ * dx is the gradient through the post mix alone: pass it to mhc_site_pre_bwd as
+ * dx_in, which adds the part that came through the pre half.
+ */
+int mhc_site_post_bwd(const float* g, const void* x, const unsigned char* x_scales,
+                      const void* f, const unsigned char* f_scales, const float* post,
+                      const float* comb, int T, int streams, int hidden, float* dx, float* df,
+                      float* dpost, float* dcomb, void* stream);
+
+/*
+ * mhc_site_pre_bwd -- the gradient of mhc_site_pre, recomputed from its input x
+ * (the gates and every Sinkhorn round; nothing else of the forward pass is
+ * kept).  With an 8-bit checkpoint of x it is the gradient at the decoded x.
+ *
+ * Arguments:
+ *   x, x_scales          as mhc_site_post_bwd
+ *   fn_w, scale, base, T, streams, hidden, iters, eps   as mhc_site_pre;
+ *                        iters at most 120 (MHC_EUNSUPPORTED above)
+ *   dy    [T][H]         gradient of y (read only)
+ *   dpre  [T][S]         further gradient of pre, beside the one through y, or NULL
+ *   dpost [T][S], dcomb [T][S][S]   gradients of post and comb (read only)
+ *   dx_in [T][S][H]      added to dx, or NULL (read only; may be dx itself)
+ *   dx    [T][S][H]      out
+ *   dfn_w [R][S*H], dscale [3], dbase [R]   out: sums over the T tokens, zeros
+ *                        for T = 0
+ *   work, work_bytes     device scratch of the caller, at least
+ *                        mhc_site_pre_bwd_work_bytes bytes (MHC_EINVAL if less);
+ *                        in use until the call's work is done
+ * Sums over tokens are added in an order fixed by the shape: equal inputs give
+ * equal bits.  (2+S)*S*S*H < 2^33.
+ *
+ * mhc_site_pre_bwd_work_bytes: 0 for T < 1 or a shape the call rejects.
+ */
+size_t mhc_site_pre_bwd_work_bytes(int T, int streams, int hidden);
+int mhc_site_pre_bwd(const void* x, const unsigned char* x_scales, const float* fn_w,
+                     const float* scale, const float* base, int T, int streams, int hidden,
+                     int iters, float eps, const float* dy, const float* dpre,
+                     const float* dpost, const float* dcomb, const float* dx_in, float* dx,
+                     float* dfn_w, float* dscale, float* dbase, void* work, size_t work_bytes,
+                     void* stream);
+
+/* The argument checks of the calls above alone (no HIP call). */
+int mhc_f8_encode_check(const void* x, int x_type, int rows, int cols, int square,
+                        const unsigned char* codes, const unsigned char* scales,
+                        const unsigned char* codes_t, const unsigned char* scales_t);
+int mhc_f8_matmul_check(const unsigned char* a, const unsigned char* a_scales,
+                        const unsigned char* b, const unsigned char* b_scales, int b_square,
+                        int M, int N, int K, const void* out, int out_type);
+int mhc_site_post_bwd_check(const float* g, const void* x, const unsigned char* x_scales,
+                            const void* f, const unsigned char* f_scales, const float* post,
+                            const float* comb, int T, int streams, int hidden, const float* dx,
+                            const float* df, const float* dpost, const float* dcomb);
+int mhc_site_pre_bwd_check(const void* x, const unsigned char* x_scales, const float* fn_w,
+                           const float* scale, const float* base, int T, int streams, int hidden,
+                           int iters, float eps, const float* dy, const float* dpre,
+                           const float* dpost, const float* dcomb, const float* dx_in,
+                           const float* dx, const float* dfn_w, const float* dscale,
+                           const float* dbase, const void* work, size_t work_bytes);
 
 /* Static text for a return code (never NULL). */
 const char* mhc_status_string(int status);

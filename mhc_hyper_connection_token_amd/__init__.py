@@ -22,6 +22,9 @@ __all__ = ["site_pre", "site_post", "site_pre_zq8", "site_pre_check", "site_post
            "head", "head_check", "bandwidth_probe", "packed_weight_bytes", "pack_weight",
            "site_pre_scratch_bytes",
            "Workspace",
+           "f8_encode", "f8_repack", "f8_decode", "f8_matmul", "f8_encode_check",
+           "f8_matmul_check", "site_post_bwd", "site_post_bwd_check", "site_pre_bwd",
+           "site_pre_bwd_check", "site_pre_bwd_work_bytes",
            "workspace_bytes", "load_library", "MhcError", "LIB_PATH", "EXPORTED_SYMBOLS",
            "STATUS"]
 
@@ -37,7 +40,11 @@ EXPORTED_SYMBOLS = ("mhc_site_pre", "mhc_site_post", "mhc_site_pre_exact", "mhc_
                     "mhc_status_string", "mhc_probe_sink_floats", "mhc_bandwidth_probe",
                     "mhc_packed_weight_bytes", "mhc_pack_weight", "mhc_site_pre_packed",
                     "mhc_site_post_pre_packed", "mhc_site_pre_scratch_bytes",
-                    "mhc_site_pre_static")
+                    "mhc_site_pre_static",
+                    "mhc_f8_encode", "mhc_f8_repack", "mhc_f8_decode", "mhc_f8_matmul",
+                    "mhc_f8_encode_check", "mhc_f8_matmul_check", "mhc_site_post_bwd",
+                    "mhc_site_post_bwd_check", "mhc_site_pre_bwd", "mhc_site_pre_bwd_check",
+                    "mhc_site_pre_bwd_work_bytes")
 
 STATUS = {0: "MHC_OK", 1: "MHC_EINVAL", 2: "MHC_EALIGN", 3: "MHC_EUNSUPPORTED",
           4: "MHC_EHIP", 5: "MHC_EOVERLAP", 6: "MHC_ECAPTURE"}
@@ -126,6 +133,28 @@ def load_library() -> ctypes.CDLL:
     lib.mhc_probe_sink_floats.restype = sz
     lib.mhc_bandwidth_probe.argtypes = [vp, vp, sz, i, vp]
     lib.mhc_bandwidth_probe.restype = i
+    lib.mhc_f8_encode.argtypes = [vp, i, i, i, i, vp, vp, vp, vp, vp]
+    lib.mhc_f8_encode.restype = i
+    lib.mhc_f8_encode_check.argtypes = [vp, i, i, i, i, vp, vp, vp, vp]
+    lib.mhc_f8_encode_check.restype = i
+    lib.mhc_f8_repack.argtypes = [vp, vp, i, i, vp, vp, vp]
+    lib.mhc_f8_repack.restype = i
+    lib.mhc_f8_decode.argtypes = [vp, vp, i, i, vp, vp]
+    lib.mhc_f8_decode.restype = i
+    lib.mhc_f8_matmul.argtypes = [vp, vp, vp, vp, i, i, i, i, vp, i, vp]
+    lib.mhc_f8_matmul.restype = i
+    lib.mhc_f8_matmul_check.argtypes = [vp, vp, vp, vp, i, i, i, i, vp, i]
+    lib.mhc_f8_matmul_check.restype = i
+    lib.mhc_site_post_bwd.argtypes = [vp] * 7 + [i, i, i] + [vp] * 5
+    lib.mhc_site_post_bwd.restype = i
+    lib.mhc_site_post_bwd_check.argtypes = [vp] * 7 + [i, i, i] + [vp] * 4
+    lib.mhc_site_post_bwd_check.restype = i
+    lib.mhc_site_pre_bwd.argtypes = [vp] * 5 + [i, i, i, i, fl] + [vp] * 10 + [sz, vp]
+    lib.mhc_site_pre_bwd.restype = i
+    lib.mhc_site_pre_bwd_check.argtypes = [vp] * 5 + [i, i, i, i, fl] + [vp] * 10 + [sz]
+    lib.mhc_site_pre_bwd_check.restype = i
+    lib.mhc_site_pre_bwd_work_bytes.argtypes = [i, i, i]
+    lib.mhc_site_pre_bwd_work_bytes.restype = sz
     if lib.mhc_workspace_struct_bytes() != ctypes.sizeof(_WsStruct):
         raise RuntimeError("mhc_workspace layout of the library and the binding differ")
     _lib = lib
@@ -433,6 +462,258 @@ def head(x, fn_w, scale, base, eps: float, *, out=None, stream=None):
     if rc != 0:
         raise MhcError("mhc_head", rc, _status_text(lib, rc))
     return out
+
+
+F8_BLOCK = 128
+
+
+def _blocks(n: int) -> int:
+    return (n + F8_BLOCK - 1) // F8_BLOCK
+
+
+def _gpu(t, name, dtype, shape=None):
+    """Device address of a contiguous GPU tensor of this dtype (and shape)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} GPU tensor")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _call(name, device, stream, *args, others=()):
+    """One library call on `device` (the operands' own, made current where it is
+    not), on `stream` or that device's current stream."""
+    import torch
+    for t in others:
+        if t is not None and t.device != device:
+            raise ValueError(f"operands are on {device} and {t.device}")
+    lib = load_library()
+    if device.index is None or device.index == torch.cuda.current_device():
+        rc = getattr(lib, name)(*args, _stream_handle(stream))
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(lib, name)(*args, _stream_handle(stream))
+    if rc != 0:
+        raise MhcError(name, rc, _status_text(lib, rc))
+
+
+def _kept(x, name, rows, H):
+    """Addresses (data, scales or None) and tensors of an activation [..., H] that is
+    a float32 tensor or the (codes, scales) pair of its 8-bit checkpoint."""
+    import torch
+    if isinstance(x, (tuple, list)):
+        codes, scales = x
+        kb = _blocks(H)
+        pc = _gpu(codes, f"{name} codes", torch.float8_e4m3fn, (*rows, kb * F8_BLOCK))
+        return pc, _gpu(scales, f"{name} scales", torch.uint8, (*rows, kb)), (codes, scales)
+    return _gpu(x, name, torch.float32, (*rows, H)), None, (x,)
+
+
+def f8_encode(x, *, transposed=False, square: bool = False, out=None, stream=None):
+    """8-bit blocks of x [..., cols] (float32 or bfloat16; include/mhc.h, "8-bit blocks").
+    Returns (codes [..., P] float8_e4m3fn, scales [..., P/128] uint8), P = cols rounded up
+    to 128.  transposed=True adds (codes_t [cols, Pt], scales_t), the encoded transpose of
+    the matrix x (leading dimensions together its rows), from the same pass;
+    transposed="only" returns that pair alone.  square=True (x [rows, cols]) uses one scale
+    per 128 x 128 square, for weights: scales [ceil(rows/128), P/128].
+    `out` may supply the tuple that the call returns."""
+    import torch
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("x must be float32 or bfloat16")
+    if x.dim() < 2 or (square and x.dim() != 2):
+        raise ValueError("x must be [rows, cols]" if square else "x must be [..., rows, cols]")
+    if transposed not in (False, True, "only"):
+        raise ValueError('transposed must be False, True or "only"')
+    px = _gpu(x, "x", x.dtype)
+    lead, cols = tuple(x.shape[:-1]), x.shape[-1]
+    rows = 1
+    for d in lead:
+        rows *= d
+    kb, rb = _blocks(cols), _blocks(rows)
+    shapes = []
+    if transposed != "only":
+        shapes += [(*lead, kb * F8_BLOCK), (rb, kb) if square else (*lead, kb)]
+    if transposed:
+        shapes += [(cols, rb * F8_BLOCK), (kb, rb) if square else (cols, rb)]
+    kinds = (torch.float8_e4m3fn, torch.uint8)
+    if out is None:
+        out = tuple(torch.empty(s, device=x.device, dtype=kinds[k & 1])
+                    for k, s in enumerate(shapes))
+    elif len(out) != len(shapes):
+        raise ValueError(f"out must hold {len(shapes)} tensors")
+    ptrs = [_gpu(o, f"out[{k}]", kinds[k & 1], s) for k, (o, s) in enumerate(zip(out, shapes))]
+    if not transposed:
+        ptrs += [None, None]
+    elif transposed == "only":
+        ptrs = [None, None] + ptrs
+    _call("mhc_f8_encode", x.device, stream, px, int(x.dtype == torch.bfloat16), rows, cols,
+          int(square), *ptrs, others=out)
+    return out
+
+
+def f8_repack(codes, scales, cols: int, *, out=None, stream=None):
+    """The encoded transpose (codes_t [cols, Pt], scales_t [cols, Pt/128]) of an encoded
+    matrix codes [rows, P], scales [rows, P/128] of `cols` columns: a kept activation in the
+    form a weight gradient's product needs.  `out` may supply that pair."""
+    import torch
+    kb = _blocks(cols)
+    if codes.dim() != 2:
+        raise ValueError("codes must be [rows, P]")
+    rows = codes.shape[0]
+    rb = _blocks(rows)
+    pc = _gpu(codes, "codes", torch.float8_e4m3fn, (rows, kb * F8_BLOCK))
+    ps = _gpu(scales, "scales", torch.uint8, (rows, kb))
+    if out is None:
+        out = (torch.empty((cols, rb * F8_BLOCK), device=codes.device,
+                           dtype=torch.float8_e4m3fn),
+               torch.empty((cols, rb), device=codes.device, dtype=torch.uint8))
+    _call("mhc_f8_repack", codes.device, stream, pc, ps, rows, cols,
+          _gpu(out[0], "out[0]", torch.float8_e4m3fn, (cols, rb * F8_BLOCK)),
+          _gpu(out[1], "out[1]", torch.uint8, (cols, rb)), others=(scales, *out))
+    return out
+
+
+def f8_decode(codes, scales, cols: int, *, out=None, stream=None):
+    """The float32 values [..., cols] of 8-bit blocks codes [..., P], scales [..., P/128]."""
+    import torch
+    kb = _blocks(cols)
+    lead = tuple(codes.shape[:-1])
+    pc = _gpu(codes, "codes", torch.float8_e4m3fn, (*lead, kb * F8_BLOCK))
+    ps = _gpu(scales, "scales", torch.uint8, (*lead, kb))
+    if out is None:
+        out = torch.empty((*lead, cols), device=codes.device, dtype=torch.float32)
+    rows = 1
+    for d in lead:
+        rows *= d
+    _call("mhc_f8_decode", codes.device, stream, pc, ps, rows, cols,
+          _gpu(out, "out", torch.float32, (*lead, cols)), others=(scales, out))
+    return out
+
+
+def f8_matmul(a, a_scales, b, b_scales, *, dtype=None, out=None, stream=None):
+    """a [M, K] times b [N, K] transposed, both 8-bit blocks: [M, N] float32 (default) or
+    bfloat16.  K is the padded width of both (a multiple of 128).  b_scales is [N, K/128],
+    or [ceil(N/128), K/128] for the square form of a weight."""
+    import torch
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
+        raise ValueError("a must be [M, K] and b [N, K]")
+    (M, K), N = a.shape, b.shape[0]
+    kb = K // F8_BLOCK
+    dtype = out.dtype if out is not None else dtype if dtype is not None else torch.float32
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("the product is float32 or bfloat16")
+    square = b_scales.dim() == 2 and b_scales.shape[0] != N
+    pa = _gpu(a, "a", torch.float8_e4m3fn)
+    pb = _gpu(b, "b", torch.float8_e4m3fn)
+    pas = _gpu(a_scales, "a_scales", torch.uint8, (M, kb))
+    pbs = _gpu(b_scales, "b_scales", torch.uint8, (_blocks(N) if square else N, kb))
+    if out is None:
+        out = torch.empty((M, N), device=a.device, dtype=dtype)
+    _call("mhc_f8_matmul", a.device, stream, pa, pas, pb, pbs, int(square), M, N, K,
+          _gpu(out, "out", dtype, (M, N)), int(dtype == torch.bfloat16),
+          others=(a_scales, b, b_scales, out))
+    return out
+
+
+def f8_encode_check(x_ptr, x_type, rows, cols, square, codes_ptr, scales_ptr, codes_t_ptr,
+                    scales_t_ptr) -> int:
+    """The library's host-side argument check of mhc_f8_encode on raw addresses."""
+    return load_library().mhc_f8_encode_check(x_ptr, x_type, rows, cols, square, codes_ptr,
+                                              scales_ptr, codes_t_ptr, scales_t_ptr)
+
+
+def f8_matmul_check(a_ptr, a_scales_ptr, b_ptr, b_scales_ptr, b_square, M, N, K, out_ptr,
+                    out_type) -> int:
+    """The library's host-side argument check of mhc_f8_matmul on raw addresses."""
+    return load_library().mhc_f8_matmul_check(a_ptr, a_scales_ptr, b_ptr, b_scales_ptr, b_square,
+                                              M, N, K, out_ptr, out_type)
+
+
+def site_post_bwd(g, x, f, post, comb, *, out=None, stream=None):
+    """Gradient of site_post: from g [T,S,H] = dL/dx', the forward's x [T,S,H], f [T,H],
+    post [T,S] and comb [T,S,S].  x and f are float32 tensors or the (codes, scales) pairs
+    that f8_encode(x), f8_encode(f) returned.  Returns (dx [T,S,H], df [T,H], dpost [T,S],
+    dcomb [T,S,S]); `out` may supply that tuple."""
+    import torch
+    if g.dim() != 3:
+        raise ValueError("g must be [T, S, H]")
+    T, S, H = g.shape
+    f32 = torch.float32
+    pg = _gpu(g, "g", f32)
+    px, pxs, tx = _kept(x, "x", (T, S), H)
+    pf, pfs, tf = _kept(f, "f", (T,), H)
+    shapes = ((T, S, H), (T, H), (T, S), (T, S, S))
+    if out is None:
+        out = tuple(torch.empty(s, device=g.device, dtype=f32) for s in shapes)
+    _call("mhc_site_post_bwd", g.device, stream, pg, px, pxs, pf, pfs,
+          _gpu(post, "post", f32, (T, S)), _gpu(comb, "comb", f32, (T, S, S)), T, S, H,
+          *(_gpu(o, n, f32, s) for o, n, s in zip(out, ("dx", "df", "dpost", "dcomb"), shapes)),
+          others=(*tx, *tf, post, comb, *out))
+    return out
+
+
+def site_post_bwd_check(g_ptr, x_ptr, x_scales_ptr, f_ptr, f_scales_ptr, post_ptr, comb_ptr, T,
+                        S, H, dx_ptr, df_ptr, dpost_ptr, dcomb_ptr) -> int:
+    """The library's host-side argument check of mhc_site_post_bwd on raw addresses."""
+    return load_library().mhc_site_post_bwd_check(g_ptr, x_ptr, x_scales_ptr, f_ptr, f_scales_ptr,
+                                                  post_ptr, comb_ptr, T, S, H, dx_ptr, df_ptr,
+                                                  dpost_ptr, dcomb_ptr)
+
+
+def site_pre_bwd_work_bytes(T: int, streams: int, hidden: int) -> int:
+    """Bytes of device scratch a site_pre_bwd call of this shape needs."""
+    return int(load_library().mhc_site_pre_bwd_work_bytes(T, streams, hidden))
+
+
+def site_pre_bwd(x, fn_w, scale, base, iters: int, eps: float, dy, dpost, dcomb, *, dpre=None,
+                 dx_in=None, out=None, work=None, stream=None):
+    """Gradient of site_pre, recomputed from its input x [T,S,H] (a float32 tensor or the
+    (codes, scales) pair that f8_encode(x) returned): dy [T,H], dpost [T,S], dcomb [T,S,S]
+    are the gradients of its outputs, dpre [T,S] a further one of pre, and dx_in [T,S,H]
+    is added to dx (site_post_bwd's dx; it may be out's dx itself).  Returns (dx [T,S,H],
+    dfn_w, dscale, dbase); `out` may supply that tuple.  `work` is a uint8 tensor of at
+    least site_pre_bwd_work_bytes bytes (allocated per call when not given)."""
+    import torch
+    if dy.dim() != 2 or dcomb.dim() != 3:
+        raise ValueError("dy must be [T, H] and dcomb [T, S, S]")
+    (T, H), S = dy.shape, dcomb.shape[1]
+    R = (2 + S) * S
+    f32 = torch.float32
+    px, pxs, tx = _kept(x, "x", (T, S), H)
+    shapes = ((T, S, H), (R, S * H), (3,), (R,))
+    if out is None:
+        out = tuple(torch.empty(s, device=dy.device, dtype=f32) for s in shapes)
+    po = [_gpu(o, n, f32, s) for o, n, s in zip(out, ("dx", "dfn_w", "dscale", "dbase"), shapes)]
+    if work is None:
+        work = torch.empty(site_pre_bwd_work_bytes(T, S, H), device=dy.device, dtype=torch.uint8)
+        if isinstance(stream, torch.cuda.Stream):
+            work.record_stream(stream)
+        elif stream is not None:
+            work.record_stream(torch.cuda.ExternalStream(int(stream), device=dy.device))
+    _call("mhc_site_pre_bwd", dy.device, stream, px, pxs,
+          _gpu(fn_w, "fn_w", f32, (R, S * H)), _gpu(scale, "scale", f32, (3,)),
+          _gpu(base, "base", f32, (R,)), T, S, H, int(iters), float(eps), _gpu(dy, "dy", f32),
+          None if dpre is None else _gpu(dpre, "dpre", f32, (T, S)),
+          _gpu(dpost, "dpost", f32, (T, S)), _gpu(dcomb, "dcomb", f32, (T, S, S)),
+          None if dx_in is None else _gpu(dx_in, "dx_in", f32, (T, S, H)), *po,
+          _gpu(work, "work", torch.uint8), work.numel(),
+          others=(*tx, fn_w, scale, base, dpre, dpost, dcomb, dx_in, *out, work))
+    return out
+
+
+def site_pre_bwd_check(x_ptr, x_scales_ptr, fn_w_ptr, scale_ptr, base_ptr, T, S, H, iters, eps,
+                       dy_ptr, dpre_ptr, dpost_ptr, dcomb_ptr, dx_in_ptr, dx_ptr, dfn_w_ptr,
+                       dscale_ptr, dbase_ptr, work_ptr, work_bytes) -> int:
+    """The library's host-side argument check of mhc_site_pre_bwd on raw addresses."""
+    return load_library().mhc_site_pre_bwd_check(
+        x_ptr, x_scales_ptr, fn_w_ptr, scale_ptr, base_ptr, T, S, H, iters, float(eps), dy_ptr,
+        dpre_ptr, dpost_ptr, dcomb_ptr, dx_in_ptr, dx_ptr, dfn_w_ptr, dscale_ptr, dbase_ptr,
+        work_ptr, work_bytes)
 
 
 def bandwidth_probe(src, dst, copy: bool, *, stream=None):

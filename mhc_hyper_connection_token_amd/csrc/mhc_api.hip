@@ -5,38 +5,20 @@
 #include <mutex>
 
 #include "mhc.h"
+#include "mhc_checks.h"
 #include "mhc_kernels.h"
+
+using mhc::check_ptr;
+using mhc::check_shape;
+using mhc::overlaps;
+using mhc::Span;
+using mhc::span;
 
 namespace {
 
-constexpr long kMaxElems = 1L << 31;  // T*S*H must stay below this (int indexing)
-constexpr int kMaxTokens = 1 << 23;   // bounds the flattened launch grids
 constexpr int kFusedMinTokens = 256;  // below this the split-K path fills the chip better
 constexpr int kSoloPlanMaxWide = 64;  // S > 4: up to this T the solo K-split with 16-token tiles
 constexpr int kExactChunk = 8192;     // tokens per pass of mhc_site_pre_exact
-
-int check_ptr(const void* p) {
-  if (!p) return MHC_EINVAL;
-  if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return MHC_EALIGN;
-  return MHC_OK;
-}
-
-struct Span {
-  uintptr_t lo, hi;
-};
-Span span(const void* p, size_t bytes) {
-  uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Span{a, a + bytes};
-}
-bool overlaps(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
-
-int check_shape(int T, int S, int H) {
-  if (T < 0 || S < 1 || H < 1) return MHC_EINVAL;
-  if (S > 8) return MHC_EUNSUPPORTED;
-  if (H % 4 != 0) return MHC_EALIGN;
-  if ((long)T * S * H >= kMaxElems || T >= kMaxTokens) return MHC_EUNSUPPORTED;
-  return MHC_OK;
-}
 
 // Library-owned scratch, one current buffer per device (split-K partials,
 // packed weight).

@@ -103,4 +103,59 @@ hipError_t launch_probe(const float* src, float* dst, long nq, bool copy, hipStr
 hipError_t launch_post(const float* x, const float* f, const float* post, const float* comb,
                        int T, int S, int H, float* x_out, hipStream_t st);
 
+// 8-bit blocks (mhc_f8.h).  Either of codes / codes_t may be null, not both.
+hipError_t launch_f8_encode(const void* x, bool bf16, int rows, int cols, bool square,
+                            unsigned char* codes, unsigned char* scales, unsigned char* codes_t,
+                            unsigned char* scales_t, hipStream_t st);
+// The row form of the transpose of an encoded [rows][cols] matrix.
+hipError_t launch_f8_repack(const unsigned char* codes, const unsigned char* scales, int rows,
+                            int cols, unsigned char* codes_t, unsigned char* scales_t,
+                            hipStream_t st);
+hipError_t launch_f8_decode(const unsigned char* codes, const unsigned char* scales, int rows,
+                            int cols, float* out, hipStream_t st);
+// out[M][N] (fp32 or bf16) = A[M][K] * B[N][K]^T; square: B has one scale per
+// 128 x 128 square.
+hipError_t launch_f8_matmul(const unsigned char* a, const unsigned char* as,
+                            const unsigned char* b, const unsigned char* bs, bool square, int M,
+                            int N, int K, void* out, bool bf16, hipStream_t st);
+
+// Gradient of the post mix; x and f are 8-bit blocks where their scales are given.
+struct PostBwd {
+  const float* g;
+  const void* x;
+  const unsigned char* x_scales;
+  const void* f;
+  const unsigned char* f_scales;
+  const float* post;
+  const float* comb;
+  float* dx;
+  float* df;
+  float* dpost;
+  float* dcomb;
+};
+hipError_t launch_post_bwd(const PostBwd& p, int T, int S, int H, hipStream_t st);
+
+// Gradient of the pre chain; x as above, dpre and dx_in may be null.  work holds
+// pre_bwd_work_bytes of scratch.
+struct PreBwd {
+  const void* x;
+  const unsigned char* x_scales;
+  const float* fn_w;
+  const float* scale;
+  const float* base;
+  const float* dy;
+  const float* dpre;
+  const float* dpost;
+  const float* dcomb;
+  const float* dx_in;
+  float* dx;
+  float* dfn_w;
+  float* dscale;
+  float* dbase;
+};
+size_t pre_bwd_work_bytes(int T, int S, int H);
+int pre_bwd_max_iters();
+hipError_t launch_pre_bwd(const PreBwd& p, int T, int S, int H, int iters, float eps, void* work,
+                          hipStream_t st);
+
 }  // namespace mhc
