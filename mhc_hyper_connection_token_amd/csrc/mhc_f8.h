@@ -17,6 +17,9 @@ constexpr int kF8Block = 128;
 typedef int intx4 __attribute__((ext_vector_type(4)));
 typedef int intx8 __attribute__((ext_vector_type(8)));
 typedef float floatx2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef unsigned uintx2 __attribute__((ext_vector_type(2)));
 
 // |v| as bits, 0 where v is infinite or NaN: such entries do not set a scale.
@@ -53,6 +56,15 @@ __device__ __forceinline__ float4 f8_unpack(unsigned q, float scale) {
   const floatx2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)q, false);
   const floatx2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)q, true);
   return make_float4(lo[0] * scale, lo[1] * scale, hi[0] * scale, hi[1] * scale);
+}
+
+// Eight codes (two dwords) to bf16, times the block scale.
+__device__ __forceinline__ bf16x8 f8_to_bf16(int lo, int hi, float scale) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
 // Maximum over the 32 lanes of a half-wave; every lane ends with it.
