@@ -472,30 +472,35 @@ def _blocks(n: int) -> int:
 
 
 def _gpu(t, name, dtype, shape=None):
-    """Device address of a contiguous GPU tensor of this dtype (and shape)."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} GPU tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t.data_ptr()
+    """Device address of a contiguous GPU tensor of this dtype (and shape, a tuple)."""
+    try:
+        if t.is_cuda and t.dtype == dtype and t.is_contiguous() and (
+                shape is None or t.shape == shape):
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    raise ValueError(f"{name} must be a contiguous {dtype} GPU tensor")
 
 
-def _call(name, device, stream, *args, others=()):
-    """One library call on `device` (the operands' own, made current where it is
-    not), on `stream` or that device's current stream."""
+def _call(name, device, stream, args, others):
+    """One library call on `device` (an index; the operands' own, made current where it
+    is not), on `stream` or that device's current stream."""
     import torch
     for t in others:
-        if t is not None and t.device != device:
-            raise ValueError(f"operands are on {device} and {t.device}")
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"operands are on GPUs {device} and {t.get_device()}")
     lib = load_library()
-    if device.index is None or device.index == torch.cuda.current_device():
-        rc = getattr(lib, name)(*args, _stream_handle(stream))
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if device == torch.cuda.current_device():
+        rc = getattr(lib, name)(*args, stream)
     else:
         with torch.cuda.device(device):
-            rc = getattr(lib, name)(*args, _stream_handle(stream))
+            rc = getattr(lib, name)(*args, stream)
     if rc != 0:
         raise MhcError(name, rc, _status_text(lib, rc))
 
@@ -551,8 +556,8 @@ def f8_encode(x, *, transposed=False, square: bool = False, out=None, stream=Non
         ptrs += [None, None]
     elif transposed == "only":
         ptrs = [None, None] + ptrs
-    _call("mhc_f8_encode", x.device, stream, px, int(x.dtype == torch.bfloat16), rows, cols,
-          int(square), *ptrs, others=out)
+    _call("mhc_f8_encode", x.get_device(), stream,
+          (px, int(x.dtype == torch.bfloat16), rows, cols, int(square), *ptrs), out)
     return out
 
 
@@ -572,9 +577,11 @@ def f8_repack(codes, scales, cols: int, *, out=None, stream=None):
         out = (torch.empty((cols, rb * F8_BLOCK), device=codes.device,
                            dtype=torch.float8_e4m3fn),
                torch.empty((cols, rb), device=codes.device, dtype=torch.uint8))
-    _call("mhc_f8_repack", codes.device, stream, pc, ps, rows, cols,
-          _gpu(out[0], "out[0]", torch.float8_e4m3fn, (cols, rb * F8_BLOCK)),
-          _gpu(out[1], "out[1]", torch.uint8, (cols, rb)), others=(scales, *out))
+    _call("mhc_f8_repack", codes.get_device(), stream,
+          (pc, ps, rows, cols,
+           _gpu(out[0], "out[0]", torch.float8_e4m3fn, (cols, rb * F8_BLOCK)),
+           _gpu(out[1], "out[1]", torch.uint8, (cols, rb))),
+          (scales, *out))
     return out
 
 
@@ -590,8 +597,8 @@ def f8_decode(codes, scales, cols: int, *, out=None, stream=None):
     rows = 1
     for d in lead:
         rows *= d
-    _call("mhc_f8_decode", codes.device, stream, pc, ps, rows, cols,
-          _gpu(out, "out", torch.float32, (*lead, cols)), others=(scales, out))
+    _call("mhc_f8_decode", codes.get_device(), stream,
+          (pc, ps, rows, cols, _gpu(out, "out", torch.float32, (*lead, cols))), (scales, out))
     return out
 
 
@@ -614,9 +621,10 @@ def f8_matmul(a, a_scales, b, b_scales, *, dtype=None, out=None, stream=None):
     pbs = _gpu(b_scales, "b_scales", torch.uint8, (_blocks(N) if square else N, kb))
     if out is None:
         out = torch.empty((M, N), device=a.device, dtype=dtype)
-    _call("mhc_f8_matmul", a.device, stream, pa, pas, pb, pbs, int(square), M, N, K,
-          _gpu(out, "out", dtype, (M, N)), int(dtype == torch.bfloat16),
-          others=(a_scales, b, b_scales, out))
+    _call("mhc_f8_matmul", a.get_device(), stream,
+          (pa, pas, pb, pbs, int(square), M, N, K, _gpu(out, "out", dtype, (M, N)),
+           int(dtype == torch.bfloat16)),
+          (a_scales, b, b_scales, out))
     return out
 
 
@@ -650,10 +658,12 @@ def site_post_bwd(g, x, f, post, comb, *, out=None, stream=None):
     shapes = ((T, S, H), (T, H), (T, S), (T, S, S))
     if out is None:
         out = tuple(torch.empty(s, device=g.device, dtype=f32) for s in shapes)
-    _call("mhc_site_post_bwd", g.device, stream, pg, px, pxs, pf, pfs,
-          _gpu(post, "post", f32, (T, S)), _gpu(comb, "comb", f32, (T, S, S)), T, S, H,
-          *(_gpu(o, n, f32, s) for o, n, s in zip(out, ("dx", "df", "dpost", "dcomb"), shapes)),
-          others=(*tx, *tf, post, comb, *out))
+    _call("mhc_site_post_bwd", g.get_device(), stream,
+          (pg, px, pxs, pf, pfs, _gpu(post, "post", f32, (T, S)),
+           _gpu(comb, "comb", f32, (T, S, S)), T, S, H,
+           *(_gpu(o, n, f32, s) for o, n, s in zip(out, ("dx", "df", "dpost", "dcomb"),
+                                                   shapes))),
+          (*tx, *tf, post, comb, *out))
     return out
 
 
@@ -695,14 +705,14 @@ def site_pre_bwd(x, fn_w, scale, base, iters: int, eps: float, dy, dpost, dcomb,
             work.record_stream(stream)
         elif stream is not None:
             work.record_stream(torch.cuda.ExternalStream(int(stream), device=dy.device))
-    _call("mhc_site_pre_bwd", dy.device, stream, px, pxs,
-          _gpu(fn_w, "fn_w", f32, (R, S * H)), _gpu(scale, "scale", f32, (3,)),
-          _gpu(base, "base", f32, (R,)), T, S, H, int(iters), float(eps), _gpu(dy, "dy", f32),
-          None if dpre is None else _gpu(dpre, "dpre", f32, (T, S)),
-          _gpu(dpost, "dpost", f32, (T, S)), _gpu(dcomb, "dcomb", f32, (T, S, S)),
-          None if dx_in is None else _gpu(dx_in, "dx_in", f32, (T, S, H)), *po,
-          _gpu(work, "work", torch.uint8), work.numel(),
-          others=(*tx, fn_w, scale, base, dpre, dpost, dcomb, dx_in, *out, work))
+    _call("mhc_site_pre_bwd", dy.get_device(), stream,
+          (px, pxs, _gpu(fn_w, "fn_w", f32, (R, S * H)), _gpu(scale, "scale", f32, (3,)),
+           _gpu(base, "base", f32, (R,)), T, S, H, int(iters), float(eps),
+           _gpu(dy, "dy", f32), None if dpre is None else _gpu(dpre, "dpre", f32, (T, S)),
+           _gpu(dpost, "dpost", f32, (T, S)), _gpu(dcomb, "dcomb", f32, (T, S, S)),
+           None if dx_in is None else _gpu(dx_in, "dx_in", f32, (T, S, H)), *po,
+           _gpu(work, "work", torch.uint8), work.numel()),
+          (*tx, fn_w, scale, base, dpre, dpost, dcomb, dx_in, *out, work))
     return out
 
 

@@ -14,6 +14,11 @@ namespace mhc {
 
 namespace {
 constexpr int kRowsUnroll = 4;  // blocks per half-wave, all loads in flight at once
+// Rows of a tile that a thread holds: 8 gives 4 waves per SIMD (at 16 the registers
+// leave 2: 16.0 against 12.3 us for 1001 x 7168 bf16 both ways; at 4 a block's 1024
+// threads spill).
+constexpr int kTileRows = 8;
+constexpr int kTileThreads = 32 * kF8Block / kTileRows;
 }
 
 template <typename E>
@@ -50,22 +55,23 @@ __global__ __launch_bounds__(256) void f8_encode_rows_kernel(const E* __restrict
   }
 }
 
-// One 128 x 128 tile per block.  Thread (rg, cq): rows 16*rg .. +15, columns
-// 4*cq .. +3.  E = unsigned char reads codes with their row scales (xs).
+// One 128 x 128 tile per block.  Thread (rg, cq): rows kTileRows*rg and on,
+// columns 4*cq .. +3.  E = unsigned char reads codes with their row scales (xs).
 // codes / codes_t: either may be null; with SQUARE one scale serves the tile.
 template <typename E, bool SQUARE>
-__global__ __launch_bounds__(256) void f8_encode_tile_kernel(
+__global__ __launch_bounds__(kTileThreads) void f8_encode_tile_kernel(
     const E* __restrict__ x, const unsigned char* __restrict__ xs, int rows, int cols, int KB,
     int RB, unsigned char* __restrict__ codes, unsigned char* __restrict__ scales,
     unsigned char* __restrict__ codes_t, unsigned char* __restrict__ scales_t) {
-  __shared__ unsigned cmax[8][kF8Block];
-  __shared__ uint4 turn[kF8Block * 8];
+  constexpr int NR = kTileRows, NG = kF8Block / NR, NW = NR / 4;
+  __shared__ unsigned cmax[NG][kF8Block];
+  __shared__ __align__(16) unsigned turn[kF8Block * 32];
   const int tid = threadIdx.x, cq = tid & 31, rg = tid >> 5;
   const int rb = blockIdx.x / KB, kb = blockIdx.x - rb * KB;
-  const int row0 = rb * kF8Block + rg * 16, col = kb * kF8Block + 4 * cq;
-  float4 v[16];
+  const int row0 = rb * kF8Block + rg * NR, col = kb * kF8Block + 4 * cq;
+  float4 v[NR];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < NR; ++i) {
     v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row0 + i < rows && col < cols) {
       if constexpr (sizeof(E) == 1) {
@@ -76,16 +82,16 @@ __global__ __launch_bounds__(256) void f8_encode_tile_kernel(
       }
     }
   }
-  unsigned m[4] = {0u, 0u, 0u, 0u}, row_byte[16];
+  unsigned m[4] = {0u, 0u, 0u, 0u}, row_byte[NR];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < NR; ++i) {
     const unsigned a0 = f8_size(v[i].x), a1 = f8_size(v[i].y);
     const unsigned a2 = f8_size(v[i].z), a3 = f8_size(v[i].w);
     m[0] = max(m[0], a0);
     m[1] = max(m[1], a1);
     m[2] = max(m[2], a2);
     m[3] = max(m[3], a3);
-    row_byte[i] = SQUARE ? 0 : f8_scale_byte(umax_half(max(max(a0, a1), max(a2, a3))));
+    row_byte[i] = SQUARE ? 0 : max(max(a0, a1), max(a2, a3));
   }
   unsigned tile_byte = 0;
   if (SQUARE) {
@@ -94,18 +100,16 @@ __global__ __launch_bounds__(256) void f8_encode_tile_kernel(
     __syncthreads();
     unsigned t = 0;
 #pragma unroll
-    for (int g = 0; g < 8; ++g) t = max(t, cmax[0][g]);
+    for (int g = 0; g < NG; ++g) t = max(t, cmax[0][g]);
     tile_byte = f8_scale_byte(t);
   } else if (codes_t) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) cmax[rg][4 * cq + j] = m[j];
-    __syncthreads();
+    *reinterpret_cast<uint4*>(&cmax[rg][4 * cq]) = make_uint4(m[0], m[1], m[2], m[3]);
   }
   const size_t pitch = (size_t)KB * kF8Block, pitch_t = (size_t)RB * kF8Block;
   if (codes) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const unsigned byte = SQUARE ? tile_byte : row_byte[i];
+    for (int i = 0; i < NR; ++i) {
+      const unsigned byte = SQUARE ? tile_byte : f8_scale_byte(umax_half(row_byte[i]));
       if (row0 + i < rows) {
         reinterpret_cast<unsigned*>(codes + (row0 + i) * pitch)[kb * 32 + cq] =
             f8_pack(v[i].x, v[i].y, v[i].z, v[i].w, f8_inverse(byte));
@@ -118,38 +122,43 @@ __global__ __launch_bounds__(256) void f8_encode_tile_kernel(
     if (codes_t) scales_t[(size_t)kb * RB + rb] = (unsigned char)tile_byte;
   }
   if (!codes_t) return;
+  if (!SQUARE) {
+    __syncthreads();
+    uint4 t = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const uint4 c = *reinterpret_cast<const uint4*>(&cmax[g][4 * cq]);
+      t = make_uint4(max(t.x, c.x), max(t.y, c.y), max(t.z, c.z), max(t.w, c.w));
+    }
+    m[0] = t.x, m[1] = t.y, m[2] = t.z, m[3] = t.w;
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    unsigned byte = tile_byte;
-    if (!SQUARE) {
-      unsigned t = 0;
-#pragma unroll
-      for (int g = 0; g < 8; ++g) t = max(t, cmax[g][4 * cq + j]);
-      byte = f8_scale_byte(t);
-      if (rg == 0 && col + j < cols) scales_t[(size_t)(col + j) * RB + rb] = (unsigned char)byte;
-    }
+    const unsigned byte = SQUARE ? tile_byte : f8_scale_byte(m[j]);
+    if (!SQUARE && rg == 0 && col + j < cols)
+      scales_t[(size_t)(col + j) * RB + rb] = (unsigned char)byte;
     const float inv = f8_inverse(byte);
-    unsigned w[4];
+    // The 16-byte chunk of a column is put where its number xor the column quad
+    // says, so that neither these writes nor the reads below meet the same banks.
+    const int at = (4 * cq + j) * 32, chunk = rg * NW / 4, part = rg * NW % 4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 *p = v + 4 * i;
+    for (int i = 0; i < NW; ++i) {
+      const float4* p = v + 4 * i;
       const float e0 = j == 0 ? p[0].x : j == 1 ? p[0].y : j == 2 ? p[0].z : p[0].w;
       const float e1 = j == 0 ? p[1].x : j == 1 ? p[1].y : j == 2 ? p[1].z : p[1].w;
       const float e2 = j == 0 ? p[2].x : j == 1 ? p[2].y : j == 2 ? p[2].z : p[2].w;
       const float e3 = j == 0 ? p[3].x : j == 1 ? p[3].y : j == 2 ? p[3].z : p[3].w;
-      w[i] = f8_pack(e0, e1, e2, e3, inv);
+      turn[at + (chunk ^ (cq & 7)) * 4 + part + i] = f8_pack(e0, e1, e2, e3, inv);
     }
-    // chunk rg of column 4*cq + j, its place rotated by the column quad so that
-    // neither this write nor the read below meets the same banks
-    turn[(4 * cq + j) * 8 + (rg ^ (cq & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int idx = k * 256 + tid, c = idx >> 3, ch = idx & 7;
+  for (int k = 0; k < 1024 / kTileThreads; ++k) {
+    const int idx = k * kTileThreads + tid, c = idx >> 3, ch = idx & 7;
     if (kb * kF8Block + c < cols)
       *reinterpret_cast<uint4*>(codes_t + (size_t)(kb * kF8Block + c) * pitch_t + rb * kF8Block +
-                                ch * 16) = turn[c * 8 + (ch ^ ((c >> 2) & 7))];
+                                ch * 16) =
+          *reinterpret_cast<const uint4*>(&turn[c * 32 + (ch ^ ((c >> 2) & 7)) * 4]);
   }
 }
 
@@ -194,10 +203,10 @@ void encode(const E* x, const unsigned char* xs, int rows, int cols, bool square
   const int RB = (int)(((long)rows + kF8Block - 1) / kF8Block);
   const dim3 tiles((unsigned)RB * KB);
   if (square)
-    hipLaunchKernelGGL((f8_encode_tile_kernel<E, true>), tiles, dim3(256), 0, st, x, xs, rows,
+    hipLaunchKernelGGL((f8_encode_tile_kernel<E, true>), tiles, dim3(kTileThreads), 0, st, x, xs, rows,
                        cols, KB, RB, codes, scales, codes_t, scales_t);
   else
-    hipLaunchKernelGGL((f8_encode_tile_kernel<E, false>), tiles, dim3(256), 0, st, x, xs, rows,
+    hipLaunchKernelGGL((f8_encode_tile_kernel<E, false>), tiles, dim3(kTileThreads), 0, st, x, xs, rows,
                        cols, KB, RB, codes, scales, codes_t, scales_t);
 }
 }  // namespace
@@ -231,7 +240,7 @@ hipError_t launch_f8_repack(const unsigned char* codes, const unsigned char* sca
   const int KB = (cols + kF8Block - 1) / kF8Block;
   const int RB = (int)(((long)rows + kF8Block - 1) / kF8Block);
   hipLaunchKernelGGL((f8_encode_tile_kernel<unsigned char, false>), dim3((unsigned)RB * KB),
-                     dim3(256), 0, st, codes, scales, rows, cols, KB, RB,
+                     dim3(kTileThreads), 0, st, codes, scales, rows, cols, KB, RB,
                      static_cast<unsigned char*>(nullptr), static_cast<unsigned char*>(nullptr),
                      codes_t, scales_t);
   return hipGetLastError();

@@ -46,45 +46,51 @@ __device__ __forceinline__ void load_to_lds(const unsigned char* src, unsigned c
 }  // namespace
 
 // ---------------------------------------------------------------- few rows
-// At most 16*MT rows of A: a block takes 16 columns n, its W waves take the k
+// At most 16*MT rows of A: a block takes 16*NF columns n, its W waves take the k
 // blocks in turn and their sums are added in wave order through LDS.  The
 // weight is read once, straight to registers, U blocks of it in flight per wave.
-template <int MT, int W, int U, typename O>
+template <int MT, int NF, int W, int U, typename O>
 __global__ __launch_bounds__(64 * W) void f8_matmul_narrow_kernel(
     const unsigned char* __restrict__ a, const unsigned char* __restrict__ as,
     const unsigned char* __restrict__ b, const unsigned char* __restrict__ bs, int bshift, int M,
     int N, int KB, O* __restrict__ out) {
-  __shared__ floatx4 part[W][MT][64];
+  __shared__ floatx4 part[W][MT * NF][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = blockIdx.x * 16 * NF;
   // rows past the end read the last row; their results are not stored
-  const int n = min(n0 + r, N - 1);
   const size_t pitch = (size_t)KB * kF8Block;
-  const unsigned char* brow = b + n * pitch + 16 * g;
-  const unsigned char* bsrow = bs + (size_t)(n >> bshift) * KB;
-  const unsigned char* arow[MT];
-  const unsigned char* asrow[MT];
+  const unsigned char *brow[NF], *bsrow[NF], *arow[MT], *asrow[MT];
+#pragma unroll
+  for (int j = 0; j < NF; ++j) {
+    const int n = min(n0 + 16 * j + r, N - 1);
+    brow[j] = b + n * pitch + 16 * g;
+    bsrow[j] = bs + (size_t)(n >> bshift) * KB;
+  }
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int m = min(16 * i + r, M - 1);
     arow[i] = a + m * pitch + 16 * g;
     asrow[i] = as + (size_t)m * KB;
   }
-  floatx4 acc[MT];
+  floatx4 acc[MT][NF];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NF; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
   for (int kb = wave; kb < KB; kb += W * U) {
-    intx4 bv[U][2], av[U][MT][2];
-    unsigned bsv[U], asv[U][MT];
+    intx4 bv[U][NF][2], av[U][MT][2];
+    unsigned bsv[U][NF], asv[U][MT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       // a block past the end reads the row's last one, its weight codes as zeros
       const int k = min(kb + W * u, KB - 1);
       const size_t at = (size_t)k * kF8Block;
-      bv[u][0] = __builtin_nontemporal_load(reinterpret_cast<const intx4*>(brow + at));
-      bv[u][1] = __builtin_nontemporal_load(reinterpret_cast<const intx4*>(brow + at + 64));
-      if (kb + W * u >= KB) bv[u][0] = bv[u][1] = intx4{0, 0, 0, 0};
-      bsv[u] = bsrow[k];
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        bv[u][j][0] = *reinterpret_cast<const intx4*>(brow[j] + at);
+        bv[u][j][1] = *reinterpret_cast<const intx4*>(brow[j] + at + 64);
+        bsv[u][j] = bsrow[j][k];
+      }
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         av[u][i][0] = *reinterpret_cast<const intx4*>(arow[i] + at);
@@ -94,52 +100,78 @@ __global__ __launch_bounds__(64 * W) void f8_matmul_narrow_kernel(
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const float sb = f8_scale(bsv[u]);
+      if (kb + W * u >= KB)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) bv[u][j][0] = bv[u][j][1] = intx4{0, 0, 0, 0};
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        const intx4 bq = bv[u][h >> 1];
-        const bf16x8 bx = f8_to_bf16(bq[2 * (h & 1)], bq[2 * (h & 1) + 1], sb);
+        bf16x8 ax[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-          const intx4 aq = av[u][i][h >> 1];
-          const bf16x8 ax =
-              f8_to_bf16(aq[2 * (h & 1)], aq[2 * (h & 1) + 1], f8_scale(asv[u][i]));
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bx, ax, acc[i], 0, 0, 0);
+          const intx4 q = av[u][i][h >> 1];
+          ax[i] = f8_to_bf16(q[2 * (h & 1)], q[2 * (h & 1) + 1], f8_scale(asv[u][i]));
+        }
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+          const intx4 q = bv[u][j][h >> 1];
+          const bf16x8 bx =
+              f8_to_bf16(q[2 * (h & 1)], q[2 * (h & 1) + 1], f8_scale(bsv[u][j]));
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bx, ax[i], acc[i][j], 0, 0, 0);
         }
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
-  __syncthreads();
-  for (int i = threadIdx.x; i < MT * 64; i += 64 * W) {
-    const int l = i & 63, mt = i >> 6;
-    floatx4 s = part[0][mt][l];
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int w = 1; w < W; ++w) s += part[w][mt][l];
-    const int m = 16 * mt + (l & 15), nq = n0 + 4 * (l >> 4);
+    for (int j = 0; j < NF; ++j) part[wave][i * NF + j][lane] = acc[i][j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < MT * NF * 64; i += 64 * W) {
+    const int l = i & 63, f = i >> 6;
+    floatx4 s = part[0][f][l];
+#pragma unroll
+    for (int w = 1; w < W; ++w) s += part[w][f][l];
+    const int m = 16 * (f / NF) + (l & 15), nq = n0 + 16 * (f % NF) + 4 * (l >> 4);
     if (m < M && nq < N) store_quad(out + (size_t)m * N + nq, s[0], s[1], s[2], s[3]);
   }
 }
 
 // ---------------------------------------------------------------- tiles
+namespace {
+constexpr int kPanel = 32;  // k blocks whose scales are held in LDS
+}
 // A block takes BM rows m and BN columns n; WM x WN waves, each with FM x FN
-// products of v_mfma_f32_32x32x16_bf16.  The codes of one k block (128 bytes a
-// row) are staged in LDS by direct loads, two stages in turn: the loads of the
-// next block run under the products of this one, and one barrier a block keeps
-// both sides in step.  Within a row's 128 bytes the 16-byte chunk c lies at place
-// c ^ (row & 7), so that eight rows read at one chunk meet all banks; the place
-// is chosen on the global side, since the direct load writes lanes in order.
-template <int FM, int FN, int WM, int WN, typename O>
-__global__ __launch_bounds__(64 * WM * WN, (WM * WN + 3) / 4) void f8_matmul_tile_kernel(
+// products of v_mfma_f32_32x32x16_bf16, which at 32 x 32 run at twice the rate of
+// the 16 x 16 ones.  The codes of one k block (128 bytes a row) are staged in LDS
+// by direct loads, NS stages in turn: while one block is multiplied the loads of
+// the NS - 1 after it are under way, and one barrier a block keeps the waves in
+// step.  A lane's 16 bytes are read a chunk ahead of their use and converted next
+// to it; converted on the way into LDS instead (once, not by every wave) the
+// bytes in LDS double, and 333 x 7168 x 7168 took 79 us against 55.
+// Within a row's 128 bytes the 16-byte chunk c lies at place c ^ (row / 2 % 8), so
+// that sixteen rows read at one chunk meet all 64 banks; the place is chosen on
+// the global side, since a direct load writes its lanes in order.
+// What bounds it: with neither loads nor conversions the products alone take
+// 442 us at 4096 x 16384 x 4096 (1240 TFLOP/s; the library's bf16 product of these
+// sizes 420), with them 540: the conversions cost 50, the staging 50.
+template <int FM, int FN, int WM, int WN, int NS, typename O>
+__global__ __launch_bounds__(64 * WM * WN, 2) void f8_matmul_tile_kernel(
     const unsigned char* __restrict__ a, const unsigned char* __restrict__ as,
     const unsigned char* __restrict__ b, const unsigned char* __restrict__ bs, int bshift, int M,
     int N, int KB, int MT, int NT, O* __restrict__ out) {
   constexpr int W = WM * WN, BM = 32 * FM * WM, BN = 32 * FN * WN;
   constexpr int LOADS = (BM + BN) / 8 / W;  // wave loads (8 rows of 128 bytes) a stage
   static_assert(LOADS * 8 * W == BM + BN && BM % 8 == 0, "whole wave loads");
-  __shared__ __align__(16) unsigned char stage[2][(BM + BN) * kF8Block];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // one variable a stage: the compiler then knows which loads a read depends on
+  __shared__ __align__(16) unsigned char stage0[(BM + BN) * kF8Block];
+  __shared__ __align__(16) unsigned char stage1[(BM + BN) * kF8Block];
+  __shared__ __align__(16) unsigned char stage2[NS > 2 ? (BM + BN) * kF8Block : 16];
+  __shared__ __align__(16) unsigned char stage3[NS > 3 ? (BM + BN) * kF8Block : 16];
+  __shared__ unsigned char panel[kPanel][BM + BN];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, h = lane >> 5;
   const int wm = wave % WM, wn = wave / WM;
 
@@ -161,19 +193,10 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN + 3) / 4) void f8_matmul_til
 #pragma unroll
   for (int i = 0; i < LOADS; ++i) {
     const int row = 8 * (i * W + wave) + (lane >> 3);
-    const int chunk = (lane & 7) ^ (row & 7);
+    const int chunk = (lane & 7) ^ ((row >> 1) & 7);
     src[i] = (row < BM ? a + min(m0 + row, M - 1) * pitch
                        : b + min(n0 + row - BM, N - 1) * pitch) + chunk * 16;
   }
-  const unsigned char* asrow[FM];
-  const unsigned char* bsrow[FN];
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-    asrow[i] = as + (size_t)min(m0 + (wm * FM + i) * 32 + r, M - 1) * KB;
-#pragma unroll
-  for (int j = 0; j < FN; ++j)
-    bsrow[j] = bs + (size_t)(min(n0 + (wn * FN + j) * 32 + r, N - 1) >> bshift) * KB;
-
   floatx16 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -182,60 +205,118 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN + 3) / 4) void f8_matmul_til
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
 
-  unsigned sa[FM], sb[FN];
-  auto fetch = [&](int kb, int buf) {
+  auto stage_of = [&](int i) -> unsigned char* {
+    return i == 0 ? stage0 : i == 1 ? stage1 : i == 2 ? stage2 : stage3;
+  };
+  // part p of three of this wave's loads of k block kb, into stage `to`
+  auto fetch = [&](int kb, int to, int p) {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i)
-      load_to_lds(src[i] + (size_t)kb * kF8Block, &stage[buf][8 * (i * W + wave) * kF8Block]);
+      if (i * 3 / LOADS == p)
+        load_to_lds(src[i] + (size_t)kb * kF8Block,
+                    stage_of(to) + 8 * (i * W + wave) * kF8Block);
   };
-  auto scales = [&](int kb) {
+  // The scale bytes of the next kPanel blocks, turned so that a lane reads its row's
+  // beside its neighbours': straight from memory every lane would meet a line of
+  // its own, for each row of products and each block.
+  auto load_panel = [&](int kb) {
+    for (int row = threadIdx.x; row < BM + BN; row += 64 * W) {
+      const unsigned char* p =
+          row < BM ? as + (size_t)min(m0 + row, M - 1) * KB
+                   : bs + (size_t)(min(n0 + row - BM, N - 1) >> bshift) * KB;
+      const int count = min(kPanel, KB - kb);
+      int i = 0;
+      if (KB % 4 == 0)
+        for (; i + 4 <= count; i += 4) {
+          const unsigned v = *reinterpret_cast<const unsigned*>(p + kb + i);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) sa[i] = asrow[i][kb];
+          for (int e = 0; e < 4; ++e) panel[i + e][row] = (unsigned char)(v >> (8 * e));
+        }
+      for (; i < count; ++i) panel[i][row] = p[kb + i];
+    }
+  };
+  float fa[FM], fb[FN];
+  // Block kb has landed (this wave's part; the barrier adds the others') while the
+  // NS - 2 blocks after it may be on their way, and every wave has taken what it
+  // needs of the block before it and of the panel.
+  auto turn = [&](int kb) {
+    if (NS > 2 && kb + NS - 2 < KB)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LOADS * (NS - 2)) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (kb % kPanel == 0) {
+      load_panel(kb);
+      __syncthreads();
+    }
 #pragma unroll
-    for (int j = 0; j < FN; ++j) sb[j] = bsrow[j][kb];
+    for (int i = 0; i < FM; ++i)
+      fa[i] = f8_scale(panel[kb % kPanel][(wm * FM + i) * 32 + r]);
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      fb[j] = f8_scale(panel[kb % kPanel][BM + (wn * FN + j) * 32 + r]);
+  };
+  intx4 av[2][FM], bv[2][FN];
+  auto read = [&](int from, int c, int to) {
+    const unsigned char* arow = stage_of(from) + (wm * FM * 32 + r) * kF8Block;
+    const unsigned char* brow = stage_of(from) + (BM + wn * FN * 32 + r) * kF8Block;
+    const int place = ((2 * c + h) ^ ((r >> 1) & 7)) * 16;
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      bv[to][j] = *reinterpret_cast<const intx4*>(brow + j * 32 * kF8Block + place);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+      av[to][i] = *reinterpret_cast<const intx4*>(arow + i * 32 * kF8Block + place);
   };
   if (KB > 0) {
-    fetch(0, 0);
-    scales(0);
+#pragma unroll
+    for (int k = 0; k < NS - 1; ++k)
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+        if (k < KB) fetch(k, k, p);
+    turn(0);
+    read(0, 0, 0);
+    if (NS - 1 < KB) fetch(NS - 1, NS - 1, 0);
   }
-  for (int kb = 0; kb < KB; ++kb) {
-    // stage kb has landed (this wave's part; the barrier adds the others'), and
-    // every wave is done with the other buffer
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    float fa[FM], fb[FN];
+  for (int k0 = 0; k0 < KB; k0 += NS) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i) fa[i] = f8_scale(sa[i]);
+    for (int here = 0; here < NS; ++here) {
+      const int kb = k0 + here, free = (here + NS - 1) % NS;
+      if (kb >= KB) break;
 #pragma unroll
-    for (int j = 0; j < FN; ++j) fb[j] = f8_scale(sb[j]);
-    if (kb + 1 < KB) {
-      fetch(kb + 1, (kb + 1) & 1);
-      scales(kb + 1);
-    }
-    const unsigned char* arow = &stage[kb & 1][(wm * FM * 32 + r) * kF8Block];
-    const unsigned char* brow = &stage[kb & 1][(BM + wn * FN * 32 + r) * kF8Block];
+      for (int c = 0; c < 4; ++c) {
+        float ga[FM], gb[FN];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int place = ((2 * c + h) ^ (r & 7)) * 16;
-      intx4 av[FM], bv[FN];
+        for (int i = 0; i < FM; ++i) ga[i] = fa[i];
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
-        av[i] = *reinterpret_cast<const intx4*>(arow + i * 32 * kF8Block + place);
+        for (int j = 0; j < FN; ++j) gb[j] = fb[j];
+        // The next chunk is read while this one is multiplied; with the last chunk in
+        // registers the stage is done with, the next one is turned to, and the loads
+        // of a later block into the free stage begin, a third at a time.
+        if (c < 3) {
+          read(here, c + 1, (c + 1) & 1);
+          if (c < 2 && kb + NS - 1 < KB) fetch(kb + NS - 1, free, c + 1);
+        } else if (kb + 1 < KB) {
+          turn(kb + 1);
+          read((here + 1) % NS, 0, 0);
+          if (kb + NS < KB) fetch(kb + NS, here, 0);
+        }
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
-        bv[j] = *reinterpret_cast<const intx4*>(brow + j * 32 * kF8Block + place);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        bf16x8 ax[FM], bx[FN];
-#pragma unroll
-        for (int j = 0; j < FN; ++j) bx[j] = f8_to_bf16(bv[j][2 * s], bv[j][2 * s + 1], fb[j]);
-#pragma unroll
-        for (int i = 0; i < FM; ++i) ax[i] = f8_to_bf16(av[i][2 * s], av[i][2 * s + 1], fa[i]);
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
+        for (int s = 0; s < 2; ++s) {
+          bf16x8 ax[FM], bx[FN];
 #pragma unroll
           for (int j = 0; j < FN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bx[j], ax[i], acc[i][j], 0, 0, 0);
+            bx[j] = f8_to_bf16(bv[c & 1][j][2 * s], bv[c & 1][j][2 * s + 1], gb[j]);
+#pragma unroll
+          for (int i = 0; i < FM; ++i) {
+            ax[i] = f8_to_bf16(av[c & 1][i][2 * s], av[c & 1][i][2 * s + 1], ga[i]);
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+              acc[i][j] =
+                  __builtin_amdgcn_mfma_f32_32x32x16_bf16(bx[j], ax[i], acc[i][j], 0, 0, 0);
+          }
+        }
       }
     }
   }
@@ -266,17 +347,17 @@ struct Args {
   hipStream_t st;
 };
 
-template <int MT, int W, int U, typename O>
+template <int MT, int NF, int W, int U, typename O>
 void narrow(const Args<O>& p) {
-  hipLaunchKernelGGL((f8_matmul_narrow_kernel<MT, W, U, O>), dim3((p.N + 15) / 16),
+  hipLaunchKernelGGL((f8_matmul_narrow_kernel<MT, NF, W, U, O>), dim3((p.N + 16 * NF - 1) / (16 * NF)),
                      dim3(64 * W), 0, p.st, p.a, p.as, p.b, p.bs, p.bshift, p.M, p.N, p.KB,
                      p.out);
 }
-template <int FM, int FN, int WM, int WN, typename O>
+template <int FM, int FN, int WM, int WN, int NS, typename O>
 void tile(const Args<O>& p) {
   const int MT = (p.M + 32 * FM * WM - 1) / (32 * FM * WM);
   const int NT = (p.N + 32 * FN * WN - 1) / (32 * FN * WN);
-  hipLaunchKernelGGL((f8_matmul_tile_kernel<FM, FN, WM, WN, O>), dim3((unsigned)(MT * NT)),
+  hipLaunchKernelGGL((f8_matmul_tile_kernel<FM, FN, WM, WN, NS, O>), dim3((unsigned)(MT * NT)),
                      dim3(64 * WM * WN), 0, p.st, p.a, p.as, p.b, p.bs, p.bshift, p.M, p.N, p.KB,
                      MT, NT, p.out);
 }
@@ -286,14 +367,28 @@ long tiles_of(long M, long N, long bm, long bn) {
 
 template <typename O>
 void matmul(const Args<O>& p) {
+  // Few rows: the weight streams through.  Wide and at most 32 blocks deep, 64
+  // columns a block with the whole depth in flight (M = 8, N = 16384, K = 4096:
+  // 13.9 us, against 17.1 at 16 columns and 16 waves); else 16 columns a block, for
+  // as many blocks as there are (M = 1, N = K = 4096: 5.6 against 11 us;
+  // N = K = 16384: 48 against 56).  From 33 rows of a wide weight the tiles are
+  // faster (M = 64, N = 16384: 22.9 against 24.7 us).
+  const bool wide = p.N >= 8192 && p.KB <= 32;
   if (p.M <= 16) {
-    narrow<1, 8, 4>(p);
+    wide ? narrow<1, 4, 8, 4>(p) : narrow<1, 1, 16, 2>(p);
+  } else if (p.M <= 32) {
+    wide ? narrow<2, 4, 8, 4>(p) : narrow<2, 1, 16, 2>(p);
+  } else if (p.M <= 64 && p.N < 8192) {
+    narrow<4, 1, 16, 2>(p);
+  // The largest tiles that give most compute units one: 256 x 256 (7168 x 4096 x 1024:
+  // 69 us, 128 x 128 68, but at 4096 x 16384 x 4096 540 against 580), 128 x 128
+  // (1024 x 4096 x 4096: 41 us, 64 x 64 62), 64 x 64 three to a unit.
   } else if (tiles_of(p.M, p.N, 256, 256) >= 192) {
-    tile<4, 2, 2, 4>(p);
+    tile<4, 2, 2, 4, 2>(p);
   } else if (tiles_of(p.M, p.N, 128, 128) >= 192) {
-    tile<2, 2, 2, 2>(p);
+    tile<2, 1, 2, 4, 2>(p);
   } else {
-    tile<1, 1, 2, 2>(p);
+    tile<1, 1, 2, 2, 3>(p);
   }
 }
 }  // namespace
