@@ -456,7 +456,7 @@ int mhc_site_post_bwd(const float* g, const void* x, const unsigned char* x_scal
  *                        mhc_site_pre_bwd_work_bytes bytes (MHC_EINVAL if less);
  *                        in use until the call's work is done
  * Sums over tokens are added in an order fixed by the shape: equal inputs give
- * equal bits.  (2+S)*S*S*H < 2^33.
+ * equal bits.  streams * hidden <= 2^24 (MHC_EUNSUPPORTED above).
  *
  * mhc_site_pre_bwd_work_bytes: 0 for T < 1 or a shape the call rejects.
  */

@@ -21,9 +21,22 @@ namespace mhc {
 
 namespace {
 
-constexpr int rows_of(int S) { return (2 + S) * S; }
-constexpr int row_tiles(int S) { return (rows_of(S) + 15) / 16; }
+constexpr int kColumns = 2;             // neighbouring columns a lane of the stream owns
+constexpr int kOutside = 0x7ffffff0;  // an offset past every buffer
+constexpr int kNonTemporal = 2;       // the cache policy bits of a buffer access
+constexpr int kMaxChunk = 1024;  // tokens of a range of the stream (their gates in LDS)
 
+__host__ __device__ constexpr int padded(int T) { return (T + 31) / 32 * 32; }
+constexpr int rows_of(int S) { return (2 + S) * S; }
+constexpr int steps_of(int S) { return (rows_of(S) + 15) / 16; }  // of 16 rows
+constexpr int tiles_of(int S) { return (rows_of(S) + 31) / 32; }  // of 32 rows
+
+// Two neighbouring floats of a buffer.
+template <int POLICY>
+__device__ __forceinline__ floatx2 load_two(__amdgpu_buffer_rsrc_t buf, int offset) {
+  return __builtin_bit_cast(floatx2,
+                            __builtin_amdgcn_raw_buffer_load_b64(buf, offset, 0, POLICY));
+}
 __device__ __forceinline__ float fma4(float4 a, float4 b, float acc) {
   acc = fmaf(a.x, b.x, acc);
   acc = fmaf(a.y, b.y, acc);
@@ -234,25 +247,37 @@ __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
 }
 
 // ---------------------------------------------------------------- gates
-// u [T][16*NRT] (zero past R), side [T][S + 1] = the pre gates and alpha,
-// red [R + 3][T] = dz and, per scale, the sum of dz * m.
-// hist (LDS): the matrix before every pass, 64 entries each.
+// One wave per four tokens (one where S > 4): the gates from the dots, then back.
+//   side [S + 1][TP]   the pre gates and alpha (TP: T rounded up to 32)
+//   red [R + 3][T]     dz and, per scale, the sum of dz * m
+//   ua, ut             u in planes as the stream's operands (below), zero past R
+//                      and past T
+// hist (LDS): the matrix before every pass, 64 entries each.  The way back needs
+// from it the entries and the reciprocal sums, which do not depend on the
+// gradient: they are fetched one round ahead, so that a pass of the dependent
+// chain is a product, two lane exchanges, a difference and a product.
 template <int S>
 __global__ __launch_bounds__(64) void pre_bwd_gates_kernel(
     const float* __restrict__ part, int G, int T, int n, const float* __restrict__ scale,
     const float* __restrict__ base, int iters, float eps, const float* __restrict__ dpre,
-    const float* __restrict__ dpost, const float* __restrict__ dcomb, float* __restrict__ u_out,
-    float* __restrict__ side, float* __restrict__ red) {
+    const float* __restrict__ dpost, const float* __restrict__ dcomb,
+    unsigned short* __restrict__ ua, unsigned short* __restrict__ ut, float* __restrict__ side,
+    float* __restrict__ red) {
   constexpr int L = S <= 4 ? 4 : 8, NU = L == 4 ? 4 : 1;
-  constexpr int R = rows_of(S), NRT = row_tiles(S), V = R + 1 + S;
+  constexpr int R = rows_of(S), KS = steps_of(S), NRT = tiles_of(S), V = R + 1 + S;
   __shared__ float raw[NU][V], dzs[NU][R];
   extern __shared__ float hist[];
   const int lane = threadIdx.x, t0 = blockIdx.x * NU;
+  const size_t TP = padded(T);
   for (int i = lane; i < NU * V; i += 64) {
     const int k = i / V, v = i - k * V;
+    const float* p = part + (size_t)min(t0 + k, T - 1) * V + v;
+    const size_t step = (size_t)T * V;
     float s = 0.f;
-    if (t0 + k < T)
-      for (int gi = 0; gi < G; ++gi) s += part[((size_t)gi * T + t0 + k) * V + v];
+    int gi = 0;
+    for (; gi + 4 <= G; gi += 4, p += 4 * step)
+      s += (p[0] + p[step]) + (p[2 * step] + p[3 * step]);
+    for (; gi < G; ++gi, p += step) s += p[0];
     raw[k][v] = s;
   }
   __syncthreads();
@@ -264,7 +289,7 @@ __global__ __launch_bounds__(64) void pre_bwd_gates_kernel(
       if (gt < S) {
         const float p = sigmoid_exact_ends(fmaf(scale[0], m, base[gt]));
         const float d = raw[k][R + 1 + gt] + (dpre ? dpre[t * S + gt] : 0.f);
-        side[t * (S + 1) + gt] = p;
+        side[gt * TP + t] = p;
         dzs[k][gt] = d * p * (1.0f - p);
       } else {
         const float p = sigmoid_exact_ends(fmaf(scale[1], m, base[gt]));
@@ -291,26 +316,36 @@ __global__ __launch_bounds__(64) void pre_bwd_gates_kernel(
       hist[(2 * it + 1) * 64 + lane] = c;
       c *= __builtin_amdgcn_rcpf(col_sum<L>(c) + pad);
     }
+    // c: after the round; mid, old: before its column and its row pass
+    float mid = hist[(2 * iters - 1) * 64 + lane], old = hist[(2 * iters - 2) * 64 + lane];
+    float rmid = __builtin_amdgcn_rcpf(col_sum<L>(mid) + pad);
+    float rold = __builtin_amdgcn_rcpf(row_sum<L>(old) + pad);
     for (int it = iters - 1; it >= 0; --it) {
-      float before = hist[(2 * it + 1) * 64 + lane];
-      d = (d - col_sum<L>(d * c)) * __builtin_amdgcn_rcpf(col_sum<L>(before) + pad);
+      const int before = it > 0 ? it - 1 : 0;
+      const float mid2 = hist[(2 * before + 1) * 64 + lane], old2 = hist[(2 * before) * 64 + lane];
+      d = (d - col_sum<L>(d * c)) * rmid;
       d = valid ? d : 0.f;
-      c = before;
-      before = hist[(2 * it) * 64 + lane];
-      d = (d - row_sum<L>(d * c)) * __builtin_amdgcn_rcpf(row_sum<L>(before) + pad);
+      d = (d - row_sum<L>(d * mid)) * rold;
       d = valid ? d : 0.f;
-      c = before;
+      c = old;
+      mid = mid2;
+      old = old2;
+      rmid = __builtin_amdgcn_rcpf(col_sum<L>(mid) + pad);
+      rold = __builtin_amdgcn_rcpf(row_sum<L>(old) + pad);
     }
     if (valid) dzs[tu][r] = d * c;
   }
   __syncthreads();
-  for (int k = 0; k < NU && t0 + k < T; ++k) {
+  for (int k = 0; k < NU; ++k) {
     const size_t t = t0 + k;
+    const bool live = t < (size_t)T;
     const float rinv = rms_inverse(raw[k][R], n, eps);
     float gm[3] = {0.f, 0.f, 0.f};
-    for (int r = lane; r < 16 * NRT; r += 64) {
+    // token t as row i of ua's steps and as entry (h, e) of ut's step s
+    const int i = (int)(t & 31), s = i >> 4, h = (i >> 2) & 1, e = ((i >> 3) & 1) * 4 + (i & 3);
+    for (int r = lane; r < 32 * NRT; r += 64) {
       float uv = 0.f;
-      if (r < R) {
+      if (live && r < R) {
         const int grp = r < S ? 0 : r < 2 * S ? 1 : 2;
         const float dz = dzs[k][r], p = dz * (raw[k][r] * rinv);
         gm[0] += grp == 0 ? p : 0.f;
@@ -319,136 +354,252 @@ __global__ __launch_bounds__(64) void pre_bwd_gates_kernel(
         uv = scale[grp] * dz * rinv;
         red[(size_t)r * T + t] = dz;
       }
-      u_out[t * (16 * NRT) + r] = uv;
+      float p[3];
+      planes(uv, p[0], p[1], p[2]);
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        const unsigned short v = (unsigned short)(__float_as_uint(p[q]) >> 16);
+        if (r < 16 * KS)
+          ua[((((t >> 5) * KS + (r >> 4)) * 3 + q) * 64 + i + 32 * ((r >> 3) & 1)) * 8 +
+             (r & 7)] = v;
+        ut[(((((t >> 5) * NRT + (r >> 5)) * 2 + s) * 3 + q) * 64 + (r & 31) + 32 * h) * 8 + e] = v;
+      }
     }
     float dot = 0.f;
     for (int q = 0; q < 3; ++q) {
       gm[q] = sum_wave(gm[q]);
       dot = fmaf(scale[q], gm[q], dot);
     }
-    if (lane == 0) {
-      side[t * (S + 1) + S] = -dot * rinv * rinv / (float)n;
+    if (lane == 0 && live) {
+      side[S * TP + t] = -dot * rinv * rinv / (float)n;
       for (int q = 0; q < 3; ++q) red[(size_t)(R + q) * T + t] = gm[q];
     }
   }
 }
 
 // ---------------------------------------------------------------- stream
-// A wave owns 64 columns (lane: quad r16 of 16) and walks a range of tokens 16
-// at a time; lane group g holds tokens 4g .. 4g+3 of them, four columns each.
-//   dx: D[token][column] = u W on v_mfma_f32_16x16x4_f32, started from the
-//       vector sum dx_in + pre dy + alpha x; W stays in registers.
-//   dW: D[row][column] += u^T x over four tokens (one per lane group), with x
-//       as it was loaded: both products use the layout of the loads.
+// dx and dW in one pass over dx_in, dy and x, both on v_mfma_f32_32x32x16_bf16.  A
+// wave owns 32 groups of Q neighbouring columns, one group a lane, and walks a
+// range of tokens 32 at a time; lane half h holds the tokens 8a + 4h + b (a, b < 4)
+// of a step.  Product q takes the q-th column of every group, so that each lane
+// moves Q neighbouring floats of 16 tokens and the results land where they are
+// stored from:
+//   dx: D[token][column] += u W over the rows, both in planes (six products; the
+//       three left out are below 2^-24), started from dx_in + pre dy + alpha x
+//   dW: D[row][column] += u^T x over the tokens, x exact in bf16 (fp32: in planes)
+// The weight's planes are the lanes' own columns: each wave makes them once, in
+// LDS.  u comes in operand order from the gates kernel:
+//   ua [group of 32 tokens][step of 16 rows][plane][lane][8]: row i = lane % 32,
+//      k = 8h + e for row 16 step + k of W
+//   ut [group][tile of 32 rows][step of 16 tokens][plane][lane][8]: row lane % 32,
+//      k = (h, e) for token 8 (2 step + e / 4) + 4h + e % 4
+// The next step's loads start as soon as this one's have gone into the sums, and
+// run under the products.
 template <int S, bool F8>
-__global__ __launch_bounds__(256) void pre_bwd_stream_kernel(
+__global__ __launch_bounds__(256, 1) void pre_bwd_stream_kernel(
     const void* __restrict__ x, const unsigned char* __restrict__ xs,
-    const float* __restrict__ w, const float* __restrict__ dy, const float* __restrict__ u,
-    const float* __restrict__ side, const float* dx_in, int T, int H, int KB, int SB, int chunk,
-    float* dx, float* __restrict__ dw_part) {
-  constexpr int R = rows_of(S), NRT = row_tiles(S), KS = (R + 3) / 4, RP = 16 * NRT;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
-  const int ci = blockIdx.x / SB, HQ = H >> 2, n4 = S * HQ;
-  const int cq = ((blockIdx.x - ci * SB) * 4 + wave) * 16 + r16;
-  const bool in = cq < n4;
-  const int cs = in ? cq / HQ : 0, q = in ? cq - cs * HQ : 0;
-  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4* w4 = reinterpret_cast<const float4*>(w);
-  float4 wv[KS];
+    const float* __restrict__ w, const float* __restrict__ dy, const bf16x8* __restrict__ ua,
+    const bf16x8* __restrict__ ut, const float* __restrict__ side, const float* dx_in, int T,
+    int H, int KB, int SB, int chunk, float* dx, float* __restrict__ dw_part) {
+  constexpr int R = rows_of(S), KS = steps_of(S), NRT = tiles_of(S), Q = kColumns;
+  __shared__ bf16x8 wl[4][KS * 3 * Q][64];
+  __shared__ float4 gate[S + 1][kMaxChunk / 4];  // side, for the block's tokens
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ci = blockIdx.x / SB, n = S * H;
+  const int t_begin = ci * chunk, t_end = min(t_begin + chunk, T);
+  const size_t TP = padded(T);
+  const int group = ((blockIdx.x - ci * SB) * 4 + wave) * 32 + r;
+  const bool in = group * Q < n;
+  const int col = in ? group * Q : 0, cs = col / H, hc = col - cs * H;
+  {
+    const float* wc = w + col;
 #pragma unroll
-  for (int s = 0; s < KS; ++s)
-    wv[s] = in && 4 * s + g < R ? w4[(size_t)(4 * s + g) * n4 + cq] : zero;
-  floatx4 dw[NRT][4];
+    for (int ks = 0; ks < KS; ++ks) {
+      floatx2 v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int row = 16 * ks + 8 * h + e;
+        v[e] = row < R ? *reinterpret_cast<const floatx2*>(wc + (size_t)row * n) : floatx2(0.f);
+      }
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        bf16x8 o[3];
+        planes8(make_float4(v[0][q], v[1][q], v[2][q], v[3][q]),
+                make_float4(v[4][q], v[5][q], v[6][q], v[7][q]), o);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) wl[wave][(ks * 3 + p) * Q + q][lane] = o[p];
+      }
+    }
+  }
+  floatx16 dw[NRT][Q];
 #pragma unroll
   for (int i = 0; i < NRT; ++i)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) dw[i][k] = floatx4{0.f, 0.f, 0.f, 0.f};
-  const int t_end = min((ci + 1) * chunk, T);
-  // what one step of 16 tokens reads; the next step's is on its way while this
-  // one is computed
-  struct Step {
-    unsigned code[4], byte[4];
-    float4 x[4], d[4], o[4];
-    float p[4], al[4], ut[4][NRT], ua[KS];
-  };
-  auto load = [&](int t0, Step& n) {
+    for (int q = 0; q < Q; ++q)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const size_t t = min(t0 + 4 * g + i, t_end - 1);
+      for (int v = 0; v < 16; ++v) dw[i][q][v] = 0.f;
+
+  // what a step reads, token 8a + 4h + b at index 4a + b
+  unsigned code[16], byte[16];
+  floatx2 xf[16], d[16], o[16];
+  // A step's rows are buffers of their own (at most 2^31 bytes: n <= 2^24), a lane's
+  // place in them an offset; tokens past the end and columns past n are out of
+  // range, where loads give zero and stores are dropped.
+  const int row_x = F8 ? S * KB * 128 : 4 * n, row_s = S * KB;
+  const int lane_n = in ? 4 * (4 * h * n + col) : kOutside;
+  const int lane_h = in ? 4 * (4 * h * H + hc) : kOutside;
+  const int lane_x = F8 ? (in ? 4 * h * row_x + cs * KB * 128 + hc : kOutside) : lane_n;
+  const int lane_s = in ? 4 * h * row_s + cs * KB + (hc >> 7) : kOutside;
+  auto rows = [&](const void* p, int t0, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(static_cast<const char*>(p)) + (size_t)t0 * bytes, (short)0,
+        p && t0 < t_end ? min(t_end - t0, 32) * bytes : 0, 0x00020000);
+  };
+  auto load = [&](int t0) {
+    const auto bx = rows(x, t0, row_x), bs = rows(xs, t0, row_s), bd = rows(dy, t0, 4 * H),
+               bo = rows(dx_in, t0, 4 * n);
+    int lx = lane_x, ls = lane_s, lh = lane_h, ln = lane_n;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int k = 8 * (i >> 2) + (i & 3);
+      // opaque: the sixteen offsets would be kept in registers across the steps
+      asm volatile("" : "+v"(lx), "+v"(ls), "+v"(lh), "+v"(ln));
       if constexpr (F8) {
-        const size_t row = t * S + cs;
-        n.code[i] = static_cast<const unsigned*>(x)[row * KB * 32 + q];
-        n.byte[i] = xs[row * KB + (q >> 5)];
+        code[i] = __builtin_amdgcn_raw_buffer_load_b16(bx, lx + k * row_x, 0, 0);
+        byte[i] = __builtin_amdgcn_raw_buffer_load_b8(bs, ls + k * row_s, 0, 0);
       } else {
-        n.x[i] = static_cast<const float4*>(x)[(t * S + cs) * HQ + q];
+        xf[i] = load_two<0>(bx, lx + k * row_x);
       }
-      n.d[i] = reinterpret_cast<const float4*>(dy)[t * HQ + q];
-      n.o[i] = dx_in ? reinterpret_cast<const float4*>(dx_in)[t * n4 + (in ? cq : 0)] : zero;
-      n.p[i] = side[t * (S + 1) + cs];
-      n.al[i] = side[t * (S + 1) + S];
-#pragma unroll
-      for (int k = 0; k < NRT; ++k) n.ut[i][k] = u[t * RP + 16 * k + r16];
+      d[i] = load_two<0>(bd, lh + k * 4 * H);
+      o[i] = load_two<kNonTemporal>(bo, ln + k * 4 * n);
     }
-    const size_t ta = min(t0 + r16, t_end - 1);
-#pragma unroll
-    for (int s = 0; s < KS; ++s) n.ua[s] = u[ta * RP + 4 * s + g];
   };
-  Step next;
-  load(ci * chunk, next);
-  for (int t0 = ci * chunk; t0 < t_end; t0 += 16) {
-    Step now = next;
-    if (t0 + 16 < t_end) load(t0 + 16, next);
-    floatx4 acc[4];
+  load(t_begin);
+  for (int i = threadIdx.x; i < (S + 1) * (kMaxChunk / 4); i += 256) {
+    const int c = i / (kMaxChunk / 4), k = i - c * (kMaxChunk / 4);
+    if (4 * k < chunk && (size_t)t_begin + 4 * k < TP)
+      gate[c][k] = *reinterpret_cast<const float4*>(side + c * TP + t_begin + 4 * k);
+  }
+  __syncthreads();
+  for (int t0 = t_begin; t0 < t_end; t0 += 32) {
+    float4 pg[4], al[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool live = t0 + 4 * g + i < t_end;
-      if constexpr (F8) now.x[i] = f8_unpack(now.code[i], f8_scale(now.byte[i]));
-      const float4 xv = now.x[i], d = now.d[i], o = now.o[i];
-      acc[0][i] = fmaf(now.al[i], xv.x, fmaf(now.p[i], d.x, o.x));
-      acc[1][i] = fmaf(now.al[i], xv.y, fmaf(now.p[i], d.y, o.y));
-      acc[2][i] = fmaf(now.al[i], xv.z, fmaf(now.p[i], d.z, o.z));
-      acc[3][i] = fmaf(now.al[i], xv.w, fmaf(now.p[i], d.w, o.w));
-      // a token past the end (the last one again) adds nothing to dW
-      if (!live) {
-        now.x[i] = zero;
+    for (int a = 0; a < 4; ++a) {
+      pg[a] = gate[cs][(t0 - t_begin) / 4 + 2 * a + h];
+      al[a] = gate[S][(t0 - t_begin) / 4 + 2 * a + h];
+    }
+    floatx16 acc[Q];
+    constexpr int XP = F8 ? 1 : 3;
+    union Operand {
+      unsigned u[4];
+      bf16x8 v;
+    } xo[2][Q][XP];  // x as the operand of dW's two steps
 #pragma unroll
-        for (int k = 0; k < NRT; ++k) now.ut[i][k] = 0.f;
+    for (int i = 0; i < 16; i += 2) {
+      float p[2], a[2];
+      const float *pf = reinterpret_cast<const float*>(&pg[i >> 2]),
+                  *af = reinterpret_cast<const float*>(&al[i >> 2]);
+      float v[2][Q];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        p[k] = pf[(i + k) & 3];
+        a[k] = af[(i + k) & 3];
+        if constexpr (F8) {
+          const float sc = f8_scale(byte[i + k]);
+          const unsigned b = __builtin_bit_cast(
+              unsigned,
+              __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)code[i + k], sc, false));
+          v[k][0] = __uint_as_float(b << 16);
+          v[k][1] = __uint_as_float(b & 0xffff0000u);
+        } else {
+#pragma unroll
+          for (int q = 0; q < Q; ++q) v[k][q] = xf[i + k][q];
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        float pl[2][3];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          acc[q][i + k] = fmaf(a[k], v[k][q], fmaf(p[k], d[i + k][q], o[i + k][q]));
+          if constexpr (F8)
+            pl[k][0] = v[k][q];
+          else
+            planes(v[k][q], pl[k][0], pl[k][1], pl[k][2]);
+        }
+#pragma unroll
+        for (int m = 0; m < XP; ++m)
+          xo[i >> 3][q][m].u[(i & 7) >> 1] = upper_halves(pl[0][m], pl[1][m]);
       }
     }
+    // u first: loads come back in order, and what is asked for after the next step's
+    // rows would have to wait for them
+    const size_t tg = t0 >> 5;
+    bf16x8 um[NRT][2][3], uk[KS][3];
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      acc[0] = __builtin_amdgcn_mfma_f32_16x16x4f32(now.ua[s], wv[s].x, acc[0], 0, 0, 0);
-      acc[1] = __builtin_amdgcn_mfma_f32_16x16x4f32(now.ua[s], wv[s].y, acc[1], 0, 0, 0);
-      acc[2] = __builtin_amdgcn_mfma_f32_16x16x4f32(now.ua[s], wv[s].z, acc[2], 0, 0, 0);
-      acc[3] = __builtin_amdgcn_mfma_f32_16x16x4f32(now.ua[s], wv[s].w, acc[3], 0, 0, 0);
-    }
+    for (int i = 0; i < NRT; ++i)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int k = 0; k < NRT; ++k) {
-        const float a = now.ut[i][k];
-        dw[k][0] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, now.x[i].x, dw[k][0], 0, 0, 0);
-        dw[k][1] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, now.x[i].y, dw[k][1], 0, 0, 0);
-        dw[k][2] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, now.x[i].z, dw[k][2], 0, 0, 0);
-        dw[k][3] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, now.x[i].w, dw[k][3], 0, 0, 0);
+        for (int p = 0; p < 3; ++p)
+          um[i][s][p] = ut[(((tg * NRT + i) * 2 + s) * 3 + p) * 64 + lane];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int p = 0; p < 3; ++p) uk[ks][p] = ua[((tg * KS + ks) * 3 + p) * 64 + lane];
+    __builtin_amdgcn_sched_barrier(0);
+    load(t0 + 32);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < NRT; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int m = 0; m < (F8 ? 1 : 3 - p); ++m)
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+              dw[i][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(um[i][s][p], xo[s][q][m].v,
+                                                                 dw[i][q], 0, 0, 0);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int m = 0; m < 3; ++m) {
+        bf16x8 wq[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) wq[q] = wl[wave][(ks * 3 + m) * Q + q][lane];
+#pragma unroll
+        for (int p = 0; p < 3 - m; ++p)
+#pragma unroll
+          for (int q = 0; q < Q; ++q)
+            acc[q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(uk[ks][p], wq[q], acc[q], 0, 0, 0);
       }
+    const auto bo = rows(dx, t0, 4 * n);
+    int ln = lane_n;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = t0 + 4 * g + i;
-      if (t < t_end && in)
-        reinterpret_cast<float4*>(dx)[(size_t)t * n4 + cq] =
-            make_float4(acc[0][i], acc[1][i], acc[2][i], acc[3][i]);
+    for (int i = 0; i < 16; ++i) {
+      const int k = 8 * (i >> 2) + (i & 3);
+      asm volatile("" : "+v"(ln));
+      floatx2 v;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) v[q] = acc[q][i];
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uintx2, v), bo,
+                                              ln + k * 4 * n, 0, kNonTemporal);
     }
   }
   if (!in) return;
-  float4* o4 = reinterpret_cast<float4*>(dw_part) + (size_t)ci * R * n4 + cq;
+  float* part = dw_part + (size_t)ci * R * n + col;
 #pragma unroll
   for (int k = 0; k < NRT; ++k)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int r = 16 * k + 4 * g + v;
-      if (r < R)
-        o4[(size_t)r * n4] = make_float4(dw[k][0][v], dw[k][1][v], dw[k][2][v], dw[k][3][v]);
+    for (int i = 0; i < 16; ++i) {
+      const int row = 32 * k + 8 * (i >> 2) + 4 * h + (i & 3);
+      floatx2 v;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) v[q] = dw[k][q][i];
+      if (row < R) *reinterpret_cast<floatx2*>(part + (size_t)row * n) = v;
     }
 }
 
@@ -465,7 +616,15 @@ __global__ __launch_bounds__(256) void pre_bwd_sums_kernel(const float* __restri
   if (row < R + 3) {
     __shared__ float sums[4];
     float s = 0.f;
-    for (int t = threadIdx.x; t < T; t += 256) s += red[(size_t)row * T + t];
+    const float* p = red + (size_t)row * T;
+    int t = threadIdx.x;
+    for (; t + 7 * 256 < T; t += 8 * 256) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = p[t + k * 256];
+      s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    }
+    for (; t < T; t += 256) s += p[t];
     s = sum_wave(s);
     if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
     __syncthreads();
@@ -481,11 +640,17 @@ __global__ __launch_bounds__(256) void pre_bwd_sums_kernel(const float* __restri
   const long i = (long)(row - R - 3) * 256 + threadIdx.x;
   if (i >= quads) return;
   const float4* p = reinterpret_cast<const float4*>(part) + i;
-  float4 s = chunks > 0 ? p[0] : make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = 1; c < chunks; ++c) {
-    const float4 v = p[c * quads];
-    s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float4 v) { s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w); };
+  int c = 0;
+  for (; c + 4 <= chunks; c += 4) {
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = p[(c + k) * quads];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) add(v[k]);
   }
+  for (; c < chunks; ++c) add(p[c * quads]);
   reinterpret_cast<float4*>(dw)[i] = s;
 }
 
@@ -493,11 +658,11 @@ namespace {
 
 // The split of a call's work: token groups of 32*TT tokens times G ranges of the
 // hidden axis for the dots (4 waves, `steps` slices each), `chunks` token ranges
-// of `chunk` for the stream, about 2048 waves each (8 per compute unit) where the
-// shape has that many.
+// of `chunk` for the stream; about 2048 and 1024 waves (8 and 4 per compute unit)
+// where the shape has that many.
 struct Plan {
   int TT, G, HS, steps, SB, chunk, chunks;
-  size_t planes, part, u, side, red, dw, floats;  // offsets and total, in floats
+  size_t planes, part, ua, ut, side, red, dw, floats;  // offsets and total, in floats
 };
 size_t round64(size_t v) { return (v + 63) / 64 * 64; }
 int div_up(int a, int b) { return (a + b - 1) / b; }
@@ -511,21 +676,24 @@ Plan plan(int T, int S, int H, bool f8) {
   const int want = div_up(512, groups);
   p.steps = div_up(p.HS, 4 * want);
   p.G = div_up(p.HS, 4 * p.steps);
-  p.SB = div_up(S * (H / 4), 64);
-  int c = 512 / p.SB;
-  const int cmax = div_up(T, 64);
-  c = c < 1 ? 1 : c > cmax ? cmax : c;
-  p.chunk = div_up(div_up(T, c), 16) * 16;
+  p.SB = div_up(S * H, 128 * kColumns);
+  const int groups32 = padded(T) / 32;
+  int c = 256 / p.SB;
+  c = c < div_up(T, kMaxChunk) ? div_up(T, kMaxChunk) : c > groups32 ? groups32 : c;
+  p.chunk = div_up(groups32, c) * 32;
   p.chunks = div_up(T, p.chunk);
   size_t at = 0;
   p.planes = at;  // 64 lanes of 16 bytes for each step, plane and row tile
   at += (size_t)S * p.HS * 4 * 3 * div_up(R, 32) * 64 * 4;
   p.part = at;
   at += round64((size_t)p.G * T * (R + 1 + S));
-  p.u = at;
-  at += round64((size_t)T * 16 * div_up(R, 16));
+  // three planes of two bytes, 32 tokens by 16 (32) rows a step (tile)
+  p.ua = at;
+  at += (size_t)groups32 * div_up(R, 16) * 3 * 64 * 4;
+  p.ut = at;
+  at += (size_t)groups32 * div_up(R, 32) * 2 * 3 * 64 * 4;
   p.side = at;
-  at += round64((size_t)T * (S + 1));
+  at += round64((size_t)groups32 * 32 * (S + 1));
   p.red = at;
   at += round64((size_t)T * (R + 3));
   p.dw = at;
@@ -554,7 +722,7 @@ void run(const PreBwd& a, int T, int H, int iters, float eps, float* work, hipSt
     return;
   }
   const Plan p = plan(T, S, H, F8);
-  float *part = work + p.part, *u = work + p.u, *side = work + p.side, *red = work + p.red;
+  float *part = work + p.part, *side = work + p.side, *red = work + p.red;
   float* dw = p.chunks > 1 ? work + p.dw : a.dfn_w;
   constexpr int NRT = (R + 31) / 32;
   const long frags = (long)S * p.HS * 4 * NRT * 64;
@@ -569,12 +737,17 @@ void run(const PreBwd& a, int T, int H, int iters, float eps, float* work, hipSt
   } else {
     dots<S, F8, 1>(a, p, T, H, KB, work, st);
   }
-  hipLaunchKernelGGL((pre_bwd_gates_kernel<S>), dim3((unsigned)((T + NU - 1) / NU)), dim3(64),
+  hipLaunchKernelGGL((pre_bwd_gates_kernel<S>), dim3((unsigned)(padded(T) / NU)),
+                     dim3(64),
                      (size_t)iters * 2 * 64 * sizeof(float), st, part, p.G, T, n, a.scale,
-                     a.base, iters, eps, a.dpre, a.dpost, a.dcomb, u, side, red);
-  hipLaunchKernelGGL((pre_bwd_stream_kernel<S, F8>), dim3((unsigned)(p.SB * p.chunks)),
-                     dim3(256), 0, st, a.x, a.x_scales, a.fn_w, a.dy, u, side, a.dx_in, T, H, KB,
-                     p.SB, p.chunk, a.dx, dw);
+                     a.base, iters, eps, a.dpre, a.dpost, a.dcomb,
+                     reinterpret_cast<unsigned short*>(work + p.ua),
+                     reinterpret_cast<unsigned short*>(work + p.ut), side, red);
+  hipLaunchKernelGGL((pre_bwd_stream_kernel<S, F8>),
+                     dim3((unsigned)(p.SB * p.chunks)), dim3(256), 0, st, a.x, a.x_scales, a.fn_w,
+                     a.dy, reinterpret_cast<const bf16x8*>(work + p.ua),
+                     reinterpret_cast<const bf16x8*>(work + p.ut), side, a.dx_in, T, H, KB, p.SB,
+                     p.chunk, a.dx, dw);
   const long quads = p.chunks > 1 ? (long)R * n / 4 : 0;
   hipLaunchKernelGGL(pre_bwd_sums_kernel, dim3((unsigned)(R + 3 + (quads + 255) / 256)),
                      dim3(256), 0, st, red, T, R, dw, p.chunks, quads, a.dfn_w, a.dscale,

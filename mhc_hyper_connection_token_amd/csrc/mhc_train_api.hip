@@ -188,7 +188,7 @@ int mhc_site_post_bwd(const float* g, const void* x, const unsigned char* x_scal
 }
 
 size_t mhc_site_pre_bwd_work_bytes(int T, int streams, int hidden) {
-  if (T < 1 || check_shape(T, streams, hidden)) return 0;
+  if (T < 1 || check_shape(T, streams, hidden) || (long)streams * hidden > (1L << 24)) return 0;
   return mhc::pre_bwd_work_bytes(T, streams, hidden);
 }
 
@@ -202,7 +202,7 @@ int mhc_site_pre_bwd_check(const void* x, const unsigned char* x_scales, const f
   if (rc) return rc;
   if (iters < 1 || !(eps > 0.0f) || !std::isfinite(eps)) return MHC_EINVAL;
   const size_t S = streams, H = hidden, Tz = T, R = (2 + S) * S;
-  if (iters > mhc::pre_bwd_max_iters() || R * S * H >= (1UL << 33)) return MHC_EUNSUPPORTED;
+  if (iters > mhc::pre_bwd_max_iters() || S * H > (1UL << 24)) return MHC_EUNSUPPORTED;
   const void* sums[] = {dfn_w, dscale, dbase};
   if ((rc = check_ptrs(sums, 3))) return rc;
   const Span ds[] = {span(dfn_w, R * S * H * 4), span(dscale, 12), span(dbase, R * 4)};
