@@ -76,61 +76,92 @@ __device__ __forceinline__ void planes8(float4 a, float4 b, bf16x8 out[3]) {
   }
 }
 
-// The dots' order of a slice of 64 hidden columns: step ks = 2j + s of four,
-// lane half h, holds columns 32j + 16h + 8s .. +7.  The 16 codes of chunk 2j + h
-// of a row, one load of a lane, serve steps 2j and 2j + 1.
-__device__ __forceinline__ int dots_column(int ks, int h) {
-  return 32 * (ks >> 1) + 16 * h + 8 * (ks & 1);
+// The dots' order of a slice of 64 hidden columns in two steps of 32: the column of
+// entry 4q (q = 0, 1) of lane group g = lane / 16.  Codes: a lane's 16 bytes at 16g,
+// eight to a step.  fp32: four floats at 4g of every 16, so that the four groups
+// read 64 neighbouring bytes.
+__device__ __forceinline__ int dots_column(bool f8, int step, int g, int q) {
+  return f8 ? 16 * g + 8 * step + 4 * q : 32 * step + 16 * q + 4 * g;
 }
 
 // W [R][S*H] as row operands of the dots: for stream c, slice, step, plane and
-// row tile of 32, 64 lanes of eight bf16 (row = lane % 32), zeros past R and H.
+// row tile of 16, 64 lanes of eight bf16 (row = lane % 16), zeros past R and H.
 __global__ __launch_bounds__(256) void pre_bwd_planes_kernel(const float* __restrict__ w, int R,
                                                              int NRT, int S, int H, int HS,
-                                                             long total,
+                                                             bool f8, long total,
                                                              bf16x8* __restrict__ out) {
   const long i = (long)blockIdx.x * 256 + threadIdx.x;
   if (i >= total) return;
   const int lane = (int)(i & 63);
   const long f = i >> 6;
   const int rt = (int)(f % NRT);
-  const long step = f / NRT;  // (c * HS + slice) * 4 + ks
-  const int ks = (int)(step & 3), cs = (int)(step >> 2), c = cs / HS, slice = cs - c * HS;
-  const int row = 32 * rt + (lane & 31), col = 64 * slice + dots_column(ks, lane >> 5);
-  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float* p = w + ((size_t)row * S + c) * H + col;
-  const float4 a = row < R && col < H ? *reinterpret_cast<const float4*>(p) : zero;
-  const float4 b = row < R && col + 4 < H ? *reinterpret_cast<const float4*>(p + 4) : zero;
-  bf16x8 o[3];
-  planes8(a, b, o);
+  const long part = f / NRT;  // (c * HS + slice) * 2 + step
+  const int step = (int)(part & 1), cs = (int)(part >> 1), c = cs / HS, slice = cs - c * HS;
+  const int row = 16 * rt + (lane & 15);
+  float4 v[2];
 #pragma unroll
-  for (int k = 0; k < 3; ++k) out[((step * 3 + k) * NRT + rt) * 64 + lane] = o[k];
+  for (int q = 0; q < 2; ++q) {
+    const int col = 64 * slice + dots_column(f8, step, lane >> 4, q);
+    v[q] = row < R && col < H
+               ? *reinterpret_cast<const float4*>(w + ((size_t)row * S + c) * H + col)
+               : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  bf16x8 o[3];
+  planes8(v[0], v[1], o);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) out[((part * 3 + k) * NRT + rt) * 64 + lane] = o[k];
+}
+
+// Exchange of the four lane groups with the four registers: register i of group g
+// becomes register g of group i.
+__device__ __forceinline__ void swap32(float& a, float& b) {
+  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void swap16(float& a, float& b) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void turn_groups(float& v0, float& v1, float& v2, float& v3) {
+  swap32(v0, v2);
+  swap32(v1, v3);
+  swap16(v0, v1);
+  swap16(v2, v3);
 }
 
 // ---------------------------------------------------------------- dots
 // part[G][T][R + 1 + S]: the R dots, the sum of squares, the S products with dy.
-// A wave takes 32*TT tokens and `steps` slices of 64 hidden columns in all S
+// A wave takes 16*TT tokens and `steps` slices of 64 hidden columns in all S
 // streams; the four waves of a block take neighbouring ranges and are added up
 // in LDS, the G blocks of a token group by the gates kernel.
-// The dots run on v_mfma_f32_32x32x16_bf16 with W in three planes.  A decoded
+// The dots run on v_mfma_f32_16x16x32_bf16 with W in three planes.  A decoded
 // code is exact in bf16, so three products give fp32 dots; an fp32 x is cut into
-// planes as well and takes six (the three left out are below 2^-24).  Against
-// v_mfma_f32_16x16x4_f32 this is 16/3 (or 16/6) of the rate.
-template <int S, bool F8, int TT>
+// planes as well and takes six (the three left out are below 2^-24).
+// Every load of x and dy gives the four lane groups 64 neighbouring bytes of a
+// token; dy, four floats a lane, is then turned between the groups to meet the
+// codes' order.  60 us at 4096 tokens of 4 x 4096, where x and dy alone are 22:
+// products and conversions take 17, and a wave waits in turn for dy (22), the
+// codes (10), the planes (8) and the scales (6), which two waves a SIMD hardly hide.
+// SPLIT: a block takes one stream, for batches too short to fill the chip otherwise.
+template <int S, bool F8, int TT, bool SPLIT>
 __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
     const void* __restrict__ x, const unsigned char* __restrict__ xs,
     const bf16x8* __restrict__ wp, const float* __restrict__ dy, int T, int H, int KB, int G,
     int HS, int steps, float* __restrict__ part) {
-  constexpr int R = rows_of(S), NRT = (R + 31) / 32, V = R + 1 + S, VP = 32 * NRT + 1 + S;
-  constexpr int UC = S <= 4 ? S : 1;  // unrolled further, the streams' loads spill
-  __shared__ float sums[4][32 * TT][VP];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 31, h = lane >> 5;
+  constexpr int R = rows_of(S), NRT = steps_of(S), V = R + 1 + S, VP = 16 * NRT + 1 + S;
+  constexpr int UC = S <= 4 && !SPLIT ? S : 1;  // unrolled further, the streams' loads spill
+  __shared__ float sums[4][16 * TT][VP];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
   const int tb = blockIdx.x / G, gi = blockIdx.x - tb * G, HQ = H >> 2;
+  const int range = SPLIT ? gi / S : gi;
+  const int c0 = SPLIT ? gi - range * S : 0, c1 = SPLIT ? c0 + 1 : S;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   size_t t[TT];
 #pragma unroll
-  for (int k = 0; k < TT; ++k) t[k] = min((tb * TT + k) * 32 + r, T - 1);
-  floatx16 acc[TT][NRT];
+  for (int k = 0; k < TT; ++k) t[k] = min((tb * TT + k) * 16 + r, T - 1);
+  floatx4 acc[TT][NRT];
   float ss[TT], dp[TT][S];
 #pragma unroll
   for (int k = 0; k < TT; ++k) {
@@ -138,54 +169,53 @@ __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
 #pragma unroll
     for (int c = 0; c < S; ++c) dp[k][c] = 0.f;
 #pragma unroll
-    for (int i = 0; i < NRT; ++i)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[k][i][v] = 0.f;
+    for (int i = 0; i < NRT; ++i) acc[k][i] = floatx4{0.f, 0.f, 0.f, 0.f};
   }
-  const int s0 = (gi * 4 + wave) * steps, s1 = min(s0 + steps, HS);
+  const int s0 = (range * 4 + wave) * steps, s1 = min(s0 + steps, HS);
   for (int sl = s0; sl < s1; ++sl) {
-    float4 d[TT][4][2];
+    float4 d[TT][4];  // columns 4i .. of the lane's: 16g + 4i (codes) or 16i + 4g
 #pragma unroll
-    for (int k = 0; k < TT; ++k)
+    for (int k = 0; k < TT; ++k) {
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        const int q = 16 * sl + dots_column(ks, h) / 4;
-        const float4* p = reinterpret_cast<const float4*>(dy) + t[k] * HQ;
-        d[k][ks][0] = q < HQ ? p[q] : zero;
-        d[k][ks][1] = q + 1 < HQ ? p[q + 1] : zero;
+      for (int i = 0; i < 4; ++i) {
+        const int q = 16 * sl + 4 * i + g;
+        d[k][i] = q < HQ ? reinterpret_cast<const float4*>(dy)[t[k] * HQ + q] : zero;
       }
-#pragma unroll UC
-    for (int c = 0; c < S; ++c) {
-      float dc[TT];
-#pragma unroll
-      for (int k = 0; k < TT; ++k) dc[k] = 0.f;
-      const bf16x8* wc = wp + (size_t)(c * HS + sl) * 4 * 3 * NRT * 64 + lane;
-      intx4 code[TT][2];
-      float scale[TT];
       if constexpr (F8) {
+        turn_groups(d[k][0].x, d[k][1].x, d[k][2].x, d[k][3].x);
+        turn_groups(d[k][0].y, d[k][1].y, d[k][2].y, d[k][3].y);
+        turn_groups(d[k][0].z, d[k][1].z, d[k][2].z, d[k][3].z);
+        turn_groups(d[k][0].w, d[k][1].w, d[k][2].w, d[k][3].w);
+      }
+    }
+#pragma unroll UC
+    for (int c = c0; c < c1; ++c) {
+      float dc[TT];
+      const bf16x8* wc = wp + (size_t)(c * HS + sl) * 2 * 3 * NRT * 64 + lane;
+      intx4 code[TT];
+      float scale[TT];
 #pragma unroll
-        for (int k = 0; k < TT; ++k) {
+      for (int k = 0; k < TT; ++k) {
+        dc[k] = 0.f;
+        if constexpr (F8) {
           const size_t row = t[k] * S + c;
-          const intx4* p = static_cast<const intx4*>(x) + row * KB * 8 + 4 * sl + h;
-          code[k][0] = p[0];
-          code[k][1] = p[2];
+          code[k] = static_cast<const intx4*>(x)[row * KB * 8 + 4 * sl + g];
           scale[k] = f8_scale(xs[row * KB + (sl >> 1)]);
         }
       }
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
+      for (int step = 0; step < 2; ++step) {
         bf16x8 wv[3][NRT];
 #pragma unroll
         for (int p = 0; p < 3; ++p)
 #pragma unroll
-          for (int i = 0; i < NRT; ++i) wv[p][i] = wc[((ks * 3 + p) * NRT + i) * 64];
+          for (int i = 0; i < NRT; ++i) wv[p][i] = wc[((step * 3 + p) * NRT + i) * 64];
 #pragma unroll
         for (int k = 0; k < TT; ++k) {
           float4 xa, xb;
           bf16x8 xp[3];
           if constexpr (F8) {
-            const intx4 q = code[k][ks >> 1];
-            xp[0] = f8_to_bf16(q[2 * (ks & 1)], q[2 * (ks & 1) + 1], scale[k]);
+            xp[0] = f8_to_bf16(code[k][2 * step], code[k][2 * step + 1], scale[k]);
             union {
               bf16x8 v;
               unsigned u[4];
@@ -196,21 +226,21 @@ __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
             xb = make_float4(__uint_as_float(o.u[2] << 16), __uint_as_float(o.u[2] & 0xffff0000u),
                              __uint_as_float(o.u[3] << 16), __uint_as_float(o.u[3] & 0xffff0000u));
           } else {
-            const int q = 16 * sl + dots_column(ks, h) / 4;
+            const int q = 16 * sl + 8 * step + g;
             const float4* p = static_cast<const float4*>(x) + (t[k] * S + c) * HQ;
             xa = q < HQ ? p[q] : zero;
-            xb = q + 1 < HQ ? p[q + 1] : zero;
+            xb = q + 4 < HQ ? p[q + 4] : zero;
             planes8(xa, xb, xp);
           }
           ss[k] = fma4(xb, xb, fma4(xa, xa, ss[k]));
-          dc[k] = fma4(d[k][ks][1], xb, fma4(d[k][ks][0], xa, dc[k]));
+          dc[k] = fma4(d[k][2 * step + 1], xb, fma4(d[k][2 * step], xa, dc[k]));
 #pragma unroll
           for (int i = 0; i < NRT; ++i) {
 #pragma unroll
             for (int p = 0; p < 3; ++p)
 #pragma unroll
               for (int m = 0; m < (F8 ? 1 : 3 - p); ++m)
-                acc[k][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wv[p][i], xp[m], acc[k][i],
+                acc[k][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[p][i], xp[m], acc[k][i],
                                                                     0, 0, 0);
           }
         }
@@ -223,23 +253,23 @@ __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
   }
 #pragma unroll
   for (int k = 0; k < TT; ++k) {
-    float* mine = sums[wave][32 * k + r];
+    float* mine = sums[wave][16 * k + r];
 #pragma unroll
     for (int i = 0; i < NRT; ++i)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) mine[32 * i + 8 * (v >> 2) + 4 * h + (v & 3)] = acc[k][i][v];
-    const float s = swap32_sum(ss[k]);
-    if (h == 0) mine[32 * NRT] = s;
+      for (int v = 0; v < 4; ++v) mine[16 * i + 4 * g + v] = acc[k][i][v];
+    const float s = swap32_sum(swap16_sum(ss[k]));
+    if (g == 0) mine[16 * NRT] = s;
 #pragma unroll
     for (int c = 0; c < S; ++c) {
-      const float v = swap32_sum(dp[k][c]);
-      if (h == 0) mine[32 * NRT + 1 + c] = v;
+      const float v = swap32_sum(swap16_sum(dp[k][c]));
+      if (g == 0) mine[16 * NRT + 1 + c] = v;
     }
   }
   __syncthreads();
-  const int first = tb * 32 * TT;
-  for (int i = threadIdx.x; i < 32 * TT * V; i += 256) {
-    const int k = i / V, v = i - k * V, at = v < R ? v : v - R + 32 * NRT;
+  const int first = tb * 16 * TT;
+  for (int i = threadIdx.x; i < 16 * TT * V; i += 256) {
+    const int k = i / V, v = i - k * V, at = v < R ? v : v - R + 16 * NRT;
     if (first + k < T)
       part[((size_t)gi * T + first + k) * V + v] =
           (sums[0][k][at] + sums[1][k][at]) + (sums[2][k][at] + sums[3][k][at]);
@@ -275,9 +305,14 @@ __global__ __launch_bounds__(64) void pre_bwd_gates_kernel(
     const size_t step = (size_t)T * V;
     float s = 0.f;
     int gi = 0;
-    for (; gi + 4 <= G; gi += 4, p += 4 * step)
-      s += (p[0] + p[step]) + (p[2 * step] + p[3 * step]);
-    for (; gi < G; ++gi, p += step) s += p[0];
+    for (; gi + 8 <= G; gi += 8, p += 8 * step) {
+      float w[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) w[q] = p[q * step];
+      s += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+    }
+    for (; gi + 2 <= G; gi += 2, p += 2 * step) s += p[0] + p[step];
+    if (gi < G) s += p[0];
     raw[k][v] = s;
   }
   __syncthreads();
@@ -656,12 +691,13 @@ __global__ __launch_bounds__(256) void pre_bwd_sums_kernel(const float* __restri
 
 namespace {
 
-// The split of a call's work: token groups of 32*TT tokens times G ranges of the
+// The split of a call's work: token groups of 16*TT tokens times G ranges of the
 // hidden axis for the dots (4 waves, `steps` slices each), `chunks` token ranges
 // of `chunk` for the stream; about 2048 and 1024 waves (8 and 4 per compute unit)
 // where the shape has that many.
 struct Plan {
   int TT, G, HS, steps, SB, chunk, chunks;
+  bool split;
   size_t planes, part, ua, ut, side, red, dw, floats;  // offsets and total, in floats
 };
 size_t round64(size_t v) { return (v + 63) / 64 * 64; }
@@ -670,12 +706,14 @@ int div_up(int a, int b) { return (a + b - 1) / b; }
 Plan plan(int T, int S, int H, bool f8) {
   Plan p;
   const int R = rows_of(S);
-  p.TT = f8 && S <= 4 && T >= 1024 ? 2 : 1;
+  p.TT = T <= 16 ? 1 : f8 && S <= 4 && T >= 1024 ? 4 : 2;
   p.HS = div_up(H, 64);
-  const int groups = div_up(T, 32 * p.TT);
+  const int groups = div_up(T, 16 * p.TT);
   const int want = div_up(512, groups);
   p.steps = div_up(p.HS, 4 * want);
   p.G = div_up(p.HS, 4 * p.steps);
+  p.split = S > 1 && p.TT < 4 && groups * p.G * S <= 512;
+  if (p.split) p.G *= S;
   p.SB = div_up(S * H, 128 * kColumns);
   const int groups32 = padded(T) / 32;
   int c = 256 / p.SB;
@@ -684,7 +722,7 @@ Plan plan(int T, int S, int H, bool f8) {
   p.chunks = div_up(T, p.chunk);
   size_t at = 0;
   p.planes = at;  // 64 lanes of 16 bytes for each step, plane and row tile
-  at += (size_t)S * p.HS * 4 * 3 * div_up(R, 32) * 64 * 4;
+  at += (size_t)S * p.HS * 2 * 3 * div_up(R, 16) * 64 * 4;
   p.part = at;
   at += round64((size_t)p.G * T * (R + 1 + S));
   // three planes of two bytes, 32 tokens by 16 (32) rows a step (tile)
@@ -702,10 +740,10 @@ Plan plan(int T, int S, int H, bool f8) {
   return p;
 }
 
-template <int S, bool F8, int TT>
+template <int S, bool F8, int TT, bool SPLIT>
 void dots(const PreBwd& a, const Plan& p, int T, int H, int KB, float* work, hipStream_t st) {
-  hipLaunchKernelGGL((pre_bwd_dots_kernel<S, F8, TT>),
-                     dim3((unsigned)(div_up(T, 32 * TT) * p.G)), dim3(256), 0, st, a.x,
+  hipLaunchKernelGGL((pre_bwd_dots_kernel<S, F8, TT, SPLIT>),
+                     dim3((unsigned)(div_up(T, 16 * TT) * p.G)), dim3(256), 0, st, a.x,
                      a.x_scales, reinterpret_cast<const bf16x8*>(work + p.planes), a.dy, T, H,
                      KB, p.G, p.HS, p.steps, work + p.part);
 }
@@ -724,18 +762,20 @@ void run(const PreBwd& a, int T, int H, int iters, float eps, float* work, hipSt
   const Plan p = plan(T, S, H, F8);
   float *part = work + p.part, *side = work + p.side, *red = work + p.red;
   float* dw = p.chunks > 1 ? work + p.dw : a.dfn_w;
-  constexpr int NRT = (R + 31) / 32;
-  const long frags = (long)S * p.HS * 4 * NRT * 64;
+  constexpr int NRT = steps_of(S);
+  const long frags = (long)S * p.HS * 2 * NRT * 64;
   hipLaunchKernelGGL(pre_bwd_planes_kernel, dim3((unsigned)((frags + 255) / 256)), dim3(256), 0,
-                     st, a.fn_w, R, NRT, S, H, p.HS, frags,
+                     st, a.fn_w, R, NRT, S, H, p.HS, F8, frags,
                      reinterpret_cast<bf16x8*>(work + p.planes));
-  if constexpr (F8 && S <= 4) {
-    if (p.TT == 2)
-      dots<S, F8, 2>(a, p, T, H, KB, work, st);
-    else
-      dots<S, F8, 1>(a, p, T, H, KB, work, st);
+  constexpr bool MANY = S > 1;
+  if (p.TT == 4) {
+    if constexpr (F8 && S <= 4) dots<S, F8, 4, false>(a, p, T, H, KB, work, st);
+  } else if (p.TT == 2) {
+    p.split ? dots<S, F8, 2, MANY>(a, p, T, H, KB, work, st)
+            : dots<S, F8, 2, false>(a, p, T, H, KB, work, st);
   } else {
-    dots<S, F8, 1>(a, p, T, H, KB, work, st);
+    p.split ? dots<S, F8, 1, MANY>(a, p, T, H, KB, work, st)
+            : dots<S, F8, 1, false>(a, p, T, H, KB, work, st);
   }
   hipLaunchKernelGGL((pre_bwd_gates_kernel<S>), dim3((unsigned)(padded(T) / NU)),
                      dim3(64),
