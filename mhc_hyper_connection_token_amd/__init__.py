@@ -484,25 +484,44 @@ def _gpu(t, name, dtype, shape=None):
     raise ValueError(f"{name} must be a contiguous {dtype} GPU tensor")
 
 
+_entry = {}  # name -> function, so that a small call does not look it up twice
+_gpus = None
+
+
 def _call(name, device, stream, args, others):
     """One library call on `device` (an index; the operands' own, made current where it
     is not), on `stream` or that device's current stream."""
     import torch
-    for t in others:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"operands are on GPUs {device} and {t.get_device()}")
-    lib = load_library()
+    global _gpus
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(load_library(), name)
+        _gpus = torch.cuda.device_count()
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(device)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    if device == torch.cuda.current_device():
-        rc = getattr(lib, name)(*args, stream)
-    else:
+    if _gpus > 1:
+        for t in others:
+            if t is not None and t.get_device() != device:
+                raise ValueError(f"operands are on GPUs {device} and {t.get_device()}")
         with torch.cuda.device(device):
-            rc = getattr(lib, name)(*args, stream)
+            rc = fn(*args, stream)
+    else:
+        rc = fn(*args, stream)
     if rc != 0:
-        raise MhcError(name, rc, _status_text(lib, rc))
+        raise MhcError(name, rc, _status_text(_lib, rc))
+
+
+def _outputs(out, names, shapes, dtypes, device):
+    """The outputs of a call, new or as given (checked), and their addresses."""
+    if out is None:
+        import torch
+        out = tuple([torch.empty(s, device=device, dtype=d) for s, d in zip(shapes, dtypes)])
+        return out, [o.data_ptr() for o in out]
+    if len(out) != len(shapes):
+        raise ValueError(f"out must hold {len(shapes)} tensors")
+    return out, [_gpu(o, n, d, s) for o, n, s, d in zip(out, names, shapes, dtypes)]
 
 
 def _kept(x, name, rows, H):
@@ -539,19 +558,17 @@ def f8_encode(x, *, transposed=False, square: bool = False, out=None, stream=Non
     rows = 1
     for d in lead:
         rows *= d
-    kb, rb = _blocks(cols), _blocks(rows)
-    shapes = []
-    if transposed != "only":
-        shapes += [(*lead, kb * F8_BLOCK), (rb, kb) if square else (*lead, kb)]
-    if transposed:
-        shapes += [(cols, rb * F8_BLOCK), (kb, rb) if square else (cols, rb)]
-    kinds = (torch.float8_e4m3fn, torch.uint8)
-    if out is None:
-        out = tuple(torch.empty(s, device=x.device, dtype=kinds[k & 1])
-                    for k, s in enumerate(shapes))
-    elif len(out) != len(shapes):
-        raise ValueError(f"out must hold {len(shapes)} tensors")
-    ptrs = [_gpu(o, f"out[{k}]", kinds[k & 1], s) for k, (o, s) in enumerate(zip(out, shapes))]
+    kb = _blocks(cols)
+    f8, u8 = torch.float8_e4m3fn, torch.uint8
+    if not transposed:
+        shapes = ((*lead, kb * F8_BLOCK), (_blocks(rows), kb) if square else (*lead, kb))
+    else:
+        rb = _blocks(rows)
+        shapes = ((cols, rb * F8_BLOCK), (kb, rb) if square else (cols, rb))
+        if transposed != "only":
+            shapes = ((*lead, kb * F8_BLOCK), (rb, kb) if square else (*lead, kb)) + shapes
+    out, ptrs = _outputs(out, ("out[0]", "out[1]", "out[2]", "out[3]"), shapes,
+                         (f8, u8, f8, u8), x.device)
     if not transposed:
         ptrs += [None, None]
     elif transposed == "only":
@@ -573,14 +590,9 @@ def f8_repack(codes, scales, cols: int, *, out=None, stream=None):
     rb = _blocks(rows)
     pc = _gpu(codes, "codes", torch.float8_e4m3fn, (rows, kb * F8_BLOCK))
     ps = _gpu(scales, "scales", torch.uint8, (rows, kb))
-    if out is None:
-        out = (torch.empty((cols, rb * F8_BLOCK), device=codes.device,
-                           dtype=torch.float8_e4m3fn),
-               torch.empty((cols, rb), device=codes.device, dtype=torch.uint8))
-    _call("mhc_f8_repack", codes.get_device(), stream,
-          (pc, ps, rows, cols,
-           _gpu(out[0], "out[0]", torch.float8_e4m3fn, (cols, rb * F8_BLOCK)),
-           _gpu(out[1], "out[1]", torch.uint8, (cols, rb))),
+    out, ptrs = _outputs(out, ("out[0]", "out[1]"), ((cols, rb * F8_BLOCK), (cols, rb)),
+                         (torch.float8_e4m3fn, torch.uint8), codes.device)
+    _call("mhc_f8_repack", codes.get_device(), stream, (pc, ps, rows, cols, *ptrs),
           (scales, *out))
     return out
 
@@ -621,9 +633,11 @@ def f8_matmul(a, a_scales, b, b_scales, *, dtype=None, out=None, stream=None):
     pbs = _gpu(b_scales, "b_scales", torch.uint8, (_blocks(N) if square else N, kb))
     if out is None:
         out = torch.empty((M, N), device=a.device, dtype=dtype)
+        po = out.data_ptr()
+    else:
+        po = _gpu(out, "out", dtype, (M, N))
     _call("mhc_f8_matmul", a.get_device(), stream,
-          (pa, pas, pb, pbs, int(square), M, N, K, _gpu(out, "out", dtype, (M, N)),
-           int(dtype == torch.bfloat16)),
+          (pa, pas, pb, pbs, int(square), M, N, K, po, int(dtype == torch.bfloat16)),
           (a_scales, b, b_scales, out))
     return out
 
@@ -655,14 +669,11 @@ def site_post_bwd(g, x, f, post, comb, *, out=None, stream=None):
     pg = _gpu(g, "g", f32)
     px, pxs, tx = _kept(x, "x", (T, S), H)
     pf, pfs, tf = _kept(f, "f", (T,), H)
-    shapes = ((T, S, H), (T, H), (T, S), (T, S, S))
-    if out is None:
-        out = tuple(torch.empty(s, device=g.device, dtype=f32) for s in shapes)
+    out, po = _outputs(out, ("dx", "df", "dpost", "dcomb"),
+                       ((T, S, H), (T, H), (T, S), (T, S, S)), (f32, f32, f32, f32), g.device)
     _call("mhc_site_post_bwd", g.get_device(), stream,
           (pg, px, pxs, pf, pfs, _gpu(post, "post", f32, (T, S)),
-           _gpu(comb, "comb", f32, (T, S, S)), T, S, H,
-           *(_gpu(o, n, f32, s) for o, n, s in zip(out, ("dx", "df", "dpost", "dcomb"),
-                                                   shapes))),
+           _gpu(comb, "comb", f32, (T, S, S)), T, S, H, *po),
           (*tx, *tf, post, comb, *out))
     return out
 
@@ -695,10 +706,8 @@ def site_pre_bwd(x, fn_w, scale, base, iters: int, eps: float, dy, dpost, dcomb,
     R = (2 + S) * S
     f32 = torch.float32
     px, pxs, tx = _kept(x, "x", (T, S), H)
-    shapes = ((T, S, H), (R, S * H), (3,), (R,))
-    if out is None:
-        out = tuple(torch.empty(s, device=dy.device, dtype=f32) for s in shapes)
-    po = [_gpu(o, n, f32, s) for o, n, s in zip(out, ("dx", "dfn_w", "dscale", "dbase"), shapes)]
+    out, po = _outputs(out, ("dx", "dfn_w", "dscale", "dbase"),
+                       ((T, S, H), (R, S * H), (3,), (R,)), (f32, f32, f32, f32), dy.device)
     if work is None:
         work = torch.empty(site_pre_bwd_work_bytes(T, S, H), device=dy.device, dtype=torch.uint8)
         if isinstance(stream, torch.cuda.Stream):
