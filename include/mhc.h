@@ -370,8 +370,8 @@ int mhc_site_pre_zq8_check(const float* x, const float* fn_w, const float* scale
  * ties to even; an infinity or a NaN encodes as NaN.  A power of two moves only
  * exponents, so every code has the relative rounding of e4m3 itself, and decoded
  * values are exact in fp32 (but that an entry above 248 * 2^120 = 3.296e38
- * rounds to 2^128, which fp32 holds as an infinity).  The calls take scale bytes as encode writes them
- * (1 .. 247).
+ * rounds to 2^128, which fp32 holds as an infinity).  The calls take scale bytes
+ * as encode writes them (1 .. 247).
  *
  * mhc_f8_encode: x [rows][cols] (MHC_F32 or MHC_BF16) into codes / scales and, in
  *   the same pass, its transpose into codes_t [cols][Pt], scales_t

@@ -67,6 +67,21 @@ __device__ __forceinline__ bf16x8 f8_to_bf16(int lo, int hi, float scale) {
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// 16 bytes from global memory to LDS without a register: lane i's bytes land at
+// base + 16 * i (base the same for the whole wave).
+__device__ __forceinline__ void load_to_lds(const unsigned char* src, unsigned char* base) {
+  __builtin_amdgcn_global_load_lds(
+      (const __attribute__((address_space(1))) void*)src,
+      (__attribute__((address_space(3))) void*)base, 16, 0, 0);
+}
+
+// A byte a lane, into the low byte of dword i of base.
+__device__ __forceinline__ void load_byte_to_lds(const unsigned char* src, unsigned char* base) {
+  __builtin_amdgcn_global_load_lds(
+      (const __attribute__((address_space(1))) void*)src,
+      (__attribute__((address_space(3))) void*)base, 1, 0, 0);
+}
+
 // Maximum over the 32 lanes of a half-wave; every lane ends with it.
 template <int CTRL>
 __device__ __forceinline__ unsigned dpp_umax(unsigned v) {

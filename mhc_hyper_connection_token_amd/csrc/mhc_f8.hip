@@ -203,11 +203,11 @@ void encode(const E* x, const unsigned char* xs, int rows, int cols, bool square
   const int RB = (int)(((long)rows + kF8Block - 1) / kF8Block);
   const dim3 tiles((unsigned)RB * KB);
   if (square)
-    hipLaunchKernelGGL((f8_encode_tile_kernel<E, true>), tiles, dim3(kTileThreads), 0, st, x, xs, rows,
-                       cols, KB, RB, codes, scales, codes_t, scales_t);
+    hipLaunchKernelGGL((f8_encode_tile_kernel<E, true>), tiles, dim3(kTileThreads), 0, st, x, xs,
+                       rows, cols, KB, RB, codes, scales, codes_t, scales_t);
   else
-    hipLaunchKernelGGL((f8_encode_tile_kernel<E, false>), tiles, dim3(kTileThreads), 0, st, x, xs, rows,
-                       cols, KB, RB, codes, scales, codes_t, scales_t);
+    hipLaunchKernelGGL((f8_encode_tile_kernel<E, false>), tiles, dim3(kTileThreads), 0, st, x, xs,
+                       rows, cols, KB, RB, codes, scales, codes_t, scales_t);
 }
 }  // namespace
 

@@ -35,14 +35,6 @@ __device__ __forceinline__ void store_quad(__hip_bfloat16* p, float a, float b, 
   *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(a, b), bf16_pair(c, d));
 }
 
-// 16 bytes from global memory to LDS without a register: lane i's bytes land at
-// base + 16 * i (base the same for the whole wave).
-__device__ __forceinline__ void load_to_lds(const unsigned char* src, unsigned char* base) {
-  __builtin_amdgcn_global_load_lds(
-      (const __attribute__((address_space(1))) void*)src,
-      (__attribute__((address_space(3))) void*)base, 16, 0, 0);
-}
-
 }  // namespace
 
 // ---------------------------------------------------------------- few rows
@@ -349,8 +341,8 @@ struct Args {
 
 template <int MT, int NF, int W, int U, typename O>
 void narrow(const Args<O>& p) {
-  hipLaunchKernelGGL((f8_matmul_narrow_kernel<MT, NF, W, U, O>), dim3((p.N + 16 * NF - 1) / (16 * NF)),
-                     dim3(64 * W), 0, p.st, p.a, p.as, p.b, p.bs, p.bshift, p.M, p.N, p.KB,
+  hipLaunchKernelGGL((f8_matmul_narrow_kernel<MT, NF, W, U, O>),
+                     dim3((p.N + 16 * NF - 1) / (16 * NF)), dim3(64 * W), 0, p.st, p.a, p.as, p.b, p.bs, p.bshift, p.M, p.N, p.KB,
                      p.out);
 }
 template <int FM, int FN, int WM, int WN, int NS, typename O>

@@ -9,11 +9,13 @@
 //   u_r     = r scale dz_r,   alpha = -(sum_r scale dz_r m_r) r^2 / n
 //   dx_c    = dx_in_c + pre_c dy + sum_r u_r W_r,c + alpha x_c
 //   dW      = sum_t u_t x_t^T,  dbase = sum_t dz,  dscale_g = sum_t sum_g dz m
-// Four launches: the dots (raw, ss, dy.x) split over the hidden axis; the gates
-// forward and backward, one wave per four tokens (one where S > 4); the stream
-// that writes dx and adds up dW, a wave owning 64 columns over a range of
-// tokens; and the sums over the ranges and tokens.  x and dy are read twice
-// (neither fits on chip while a token's dots are open); everything else once.
+// Five launches: W cut into bf16 planes; the dots (raw, ss, dy.x) split over the
+// hidden axis; the gates forward and backward, one wave per four tokens (one where
+// S > 4); the stream that writes dx and adds up dW, a wave owning 64 columns over
+// a range of tokens; and the sums over the ranges and tokens.  x and dy are read
+// twice (neither fits on chip while a token's dots are open); everything else once.
+// At 4096 tokens of 4 x 4096 from a checkpoint: 5 + 44 + 10 + 145 + 5 us; at 1024
+// tokens of 8 x 7168: 11 + 63 + 13 + 173 + 5.
 #include "mhc_f8.h"
 #include "mhc_kernels.h"
 
@@ -21,10 +23,12 @@ namespace mhc {
 
 namespace {
 
-constexpr int kColumns = 2;             // neighbouring columns a lane of the stream owns
-constexpr int kOutside = 0x7ffffff0;  // an offset past every buffer
+constexpr int kColumns = 2;           // neighbouring columns a lane of the stream owns
+// an offset past every buffer of fewer than 2^31 - 16 bytes (a buffer of 2^31 has no
+// columns to leave out), no lane's or row's part of 2^31 takes it round to zero
+constexpr unsigned kOutside = 0x7ffffff0;
 constexpr int kNonTemporal = 2;       // the cache policy bits of a buffer access
-constexpr int kMaxChunk = 1024;  // tokens of a range of the stream (their gates in LDS)
+constexpr int kMaxChunk = 1024;       // tokens of a range of the stream (their gates in LDS)
 
 __host__ __device__ constexpr int padded(int T) { return (T + 31) / 32 * 32; }
 constexpr int rows_of(int S) { return (2 + S) * S; }
@@ -33,7 +37,7 @@ constexpr int tiles_of(int S) { return (rows_of(S) + 31) / 32; }  // of 32 rows
 
 // Two neighbouring floats of a buffer.
 template <int POLICY>
-__device__ __forceinline__ floatx2 load_two(__amdgpu_buffer_rsrc_t buf, int offset) {
+__device__ __forceinline__ floatx2 load_two(__amdgpu_buffer_rsrc_t buf, unsigned offset) {
   return __builtin_bit_cast(floatx2,
                             __builtin_amdgcn_raw_buffer_load_b64(buf, offset, 0, POLICY));
 }
@@ -141,9 +145,8 @@ __device__ __forceinline__ void turn_groups(float& v0, float& v1, float& v2, flo
 // planes as well and takes six (the three left out are below 2^-24).
 // Every load of x and dy gives the four lane groups 64 neighbouring bytes of a
 // token; dy, four floats a lane, is then turned between the groups to meet the
-// codes' order.  60 us at 4096 tokens of 4 x 4096, where x and dy alone are 22:
-// products and conversions take 17, and a wave waits in turn for dy (22), the
-// codes (10), the planes (8) and the scales (6), which two waves a SIMD hardly hide.
+// codes' order.  Bound by waits: a wave asks in turn for dy, x, the planes and the
+// scales, which two waves a SIMD hardly hide (37 tokens of 3 x 4100 in fp32: 8.5 us).
 // SPLIT: a block takes one stream, for batches too short to fill the chip otherwise.
 template <int S, bool F8, int TT, bool SPLIT>
 __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
@@ -273,6 +276,157 @@ __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
     if (first + k < T)
       part[((size_t)gi * T + first + k) * V + v] =
           (sums[0][k][at] + sums[1][k][at]) + (sums[2][k][at] + sums[3][k][at]);
+  }
+}
+
+// The dots from a checkpoint for batches of 16 S tokens and more, staged: a block
+// takes 16 tokens a wave and walks units of one stream of one slice.  Codes, scales
+// and planes come into LDS by direct loads two units ahead, three stages in turn,
+// dy a slice ahead: the planes are read once a block, and no wave waits for one kind
+// of load after the other.  A token's chunks of 16 bytes are turned in their row
+// (codes: chunk c at place c ^ token / 4 % 4 of four; dy: c ^ token % 16 of
+// sixteen), so that 16 tokens read at one chunk meet all banks.
+// 4096 tokens of 4 x 4096: 62 us by the kernel above, 44 here (x and dy alone: 22);
+// 128 of them: 8.7 and 8.0; 64: 8.5 and 7.6; 17: 6.4 and 7.1.  With S = 8 a unit's
+// planes are 30 KiB and one block fills the unit's LDS: eight waves then
+// (2048 tokens of 8 x 4096: 78 us above, 86 with four waves, 62 with eight); 128
+// tokens 17.0 and 17.4, 64: 11.8 and 15.9.
+constexpr int staged_waves(int S) { return S <= 4 ? 4 : 8; }
+
+template <int S>
+__global__ __launch_bounds__(64 * staged_waves(S)) void pre_bwd_dots_staged_kernel(
+    const unsigned char* __restrict__ x, const unsigned char* __restrict__ xs,
+    const unsigned char* __restrict__ wp, const unsigned char* __restrict__ dy, int T, int H,
+    int KB, int G, int HS, int steps, float* __restrict__ part) {
+  constexpr int R = rows_of(S), NRT = steps_of(S), V = R + 1 + S, W = staged_waves(S);
+  constexpr int LW = (6 * NRT + W - 1) / W;  // wave loads of planes a unit
+  constexpr int CODES = 16 * W * 64, SCALES = W * 64 * 4;
+  constexpr int STAGE = CODES + SCALES + W * LW * 1024;
+  // one variable a stage: the compiler then knows which loads a read depends on
+  __shared__ __align__(16) unsigned char stage0[STAGE];
+  __shared__ __align__(16) unsigned char stage1[STAGE];
+  __shared__ __align__(16) unsigned char stage2[STAGE];
+  __shared__ float4 dyl[16 * W * 16];
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tb = blockIdx.x / G, gi = blockIdx.x - tb * G, HQ = H >> 2;
+  const int first = (tb * W + wave) * 16, t = first + r;  // this wave's tokens, this lane's
+  const int s0 = gi * steps, units = (min(s0 + steps, HS) - s0) * S;
+  auto stage_of = [&](int i) -> unsigned char* {
+    return i == 0 ? stage0 : i == 1 ? stage1 : stage2;
+  };
+  // tokens past the end read the last one
+  const size_t crow = (size_t)min(first + (lane >> 2), T - 1) * S;
+  const size_t srow = (size_t)min(t, T - 1) * S;
+  const int chunk = (lane & 3) ^ ((lane >> 4) & 3);
+  auto fetch = [&](int u, int to) {  // unit u into stage `to`: 2 + LW loads
+    const int sl = s0 + u / S, c = u % S;
+    unsigned char* st = stage_of(to);
+    load_to_lds(x + ((crow + c) * KB * 8 + 4 * sl + chunk) * 16, st + wave * 16 * 64);
+    load_byte_to_lds(xs + (srow + c) * KB + (sl >> 1), st + CODES + wave * 256);
+    const unsigned char* w = wp + ((size_t)(c * HS + sl) * 6 * NRT * 64 + lane) * 16;
+#pragma unroll
+    for (int i = 0; i < LW; ++i)
+      load_to_lds(w + (wave + W * i) * 1024, st + CODES + SCALES + (wave + W * i) * 1024);
+  };
+  auto fetch_dy = [&](int sl) {  // four loads of four tokens, a quad past the row the last
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = 4 * i + (lane >> 4), q = min(16 * sl + ((lane & 15) ^ k), HQ - 1);
+      load_to_lds(dy + ((size_t)min(first + k, T - 1) * HQ + q) * 16,
+                  reinterpret_cast<unsigned char*>(dyl + (wave * 16 + 4 * i) * 16));
+    }
+  };
+  floatx4 acc[NRT];
+  float ss = 0.f, dp[S];
+  float4 d[4];
+#pragma unroll
+  for (int i = 0; i < S; ++i) dp[i] = 0.f;
+#pragma unroll
+  for (int i = 0; i < NRT; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+  const int last = units - 1;
+  fetch_dy(s0);
+  fetch(0, 0);
+  fetch(min(1, last), 1);
+  int c = 0;
+  for (int u0 = 0; u0 < units; u0 += 3) {
+#pragma unroll
+    for (int here = 0; here < 3; ++here) {
+      const int u = u0 + here;
+      // this unit's stage has landed; what was asked for after it may be on its way: the next
+      // unit's loads, behind the four of dy where the unit before began a slice
+      if (c == 1 % S && u > 0)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 + LW + 4) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 + LW) : "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      if (c == 0) {
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int sl = s0 + u / S;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 v = dyl[(wave * 16 + r) * 16 + ((4 * g + i) ^ r)];
+          d[i] = 16 * sl + 4 * g + i < HQ ? v : zero;
+        }
+        // the wave's own rows, read just now, make room for the next slice's
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        fetch_dy(min(sl + 1, s0 + last / S));
+      }
+      // past the end the last unit again, so that the counts above hold to the end
+      fetch(min(u + 2, last), (here + 2) % 3);
+      const unsigned char* st = stage_of(here);
+      intx4 code = *reinterpret_cast<const intx4*>(st + (wave * 16 + r) * 64 +
+                                                   (g ^ ((r >> 2) & 3)) * 16);
+      if (u > last) code = intx4{0, 0, 0, 0};
+      const float scale =
+          f8_scale(*reinterpret_cast<const unsigned*>(st + CODES + wave * 256 + lane * 4) & 255u);
+      float dc = 0.f;
+#pragma unroll
+      for (int step = 0; step < 2; ++step) {
+        union {
+          bf16x8 v;
+          unsigned u[4];
+        } o;
+        o.v = f8_to_bf16(code[2 * step], code[2 * step + 1], scale);
+        const float4 xa =
+            make_float4(__uint_as_float(o.u[0] << 16), __uint_as_float(o.u[0] & 0xffff0000u),
+                        __uint_as_float(o.u[1] << 16), __uint_as_float(o.u[1] & 0xffff0000u));
+        const float4 xb =
+            make_float4(__uint_as_float(o.u[2] << 16), __uint_as_float(o.u[2] & 0xffff0000u),
+                        __uint_as_float(o.u[3] << 16), __uint_as_float(o.u[3] & 0xffff0000u));
+        ss = fma4(xb, xb, fma4(xa, xa, ss));
+        dc = fma4(d[2 * step + 1], xb, fma4(d[2 * step], xa, dc));
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int i = 0; i < NRT; ++i) {
+            const bf16x8 w = *reinterpret_cast<const bf16x8*>(
+                st + CODES + SCALES + ((step * 3 + p) * NRT + i) * 1024 + lane * 16);
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, o.v, acc[i], 0, 0, 0);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < S; ++i) dp[i] += i == c && u <= last ? dc : 0.f;
+      c = c + 1 == S ? 0 : c + 1;
+    }
+  }
+  // nothing may land in this block's memory once another block has it
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  float* mine = part + ((size_t)gi * T + min(t, T - 1)) * V;
+#pragma unroll
+  for (int i = 0; i < NRT; ++i)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int at = 16 * i + 4 * g + v;
+      if (t < T && at < R) mine[at] = acc[i][v];
+    }
+  ss = swap32_sum(swap16_sum(ss));
+  if (t < T && g == 0) mine[R] = ss;
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    const float v = swap32_sum(swap16_sum(dp[i]));
+    if (t < T && g == 0) mine[R + 1 + i] = v;
   }
 }
 
@@ -482,19 +636,19 @@ __global__ __launch_bounds__(256, 1) void pre_bwd_stream_kernel(
   // place in them an offset; tokens past the end and columns past n are out of
   // range, where loads give zero and stores are dropped.
   const int row_x = F8 ? S * KB * 128 : 4 * n, row_s = S * KB;
-  const int lane_n = in ? 4 * (4 * h * n + col) : kOutside;
-  const int lane_h = in ? 4 * (4 * h * H + hc) : kOutside;
-  const int lane_x = F8 ? (in ? 4 * h * row_x + cs * KB * 128 + hc : kOutside) : lane_n;
-  const int lane_s = in ? 4 * h * row_s + cs * KB + (hc >> 7) : kOutside;
+  const unsigned lane_n = in ? 4 * (4 * h * n + col) : kOutside;
+  const unsigned lane_h = in ? 4 * (4 * h * H + hc) : kOutside;
+  const unsigned lane_x = F8 ? (in ? 4 * h * row_x + cs * KB * 128 + hc : kOutside) : lane_n;
+  const unsigned lane_s = in ? 4 * h * row_s + cs * KB + (hc >> 7) : kOutside;
   auto rows = [&](const void* p, int t0, int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(
         const_cast<char*>(static_cast<const char*>(p)) + (size_t)t0 * bytes, (short)0,
-        p && t0 < t_end ? min(t_end - t0, 32) * bytes : 0, 0x00020000);
+        p && t0 < t_end ? (unsigned)min(t_end - t0, 32) * (unsigned)bytes : 0u, 0x00020000);
   };
   auto load = [&](int t0) {
     const auto bx = rows(x, t0, row_x), bs = rows(xs, t0, row_s), bd = rows(dy, t0, 4 * H),
                bo = rows(dx_in, t0, 4 * n);
-    int lx = lane_x, ls = lane_s, lh = lane_h, ln = lane_n;
+    unsigned lx = lane_x, ls = lane_s, lh = lane_h, ln = lane_n;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int k = 8 * (i >> 2) + (i & 3);
@@ -612,7 +766,7 @@ __global__ __launch_bounds__(256, 1) void pre_bwd_stream_kernel(
             acc[q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(uk[ks][p], wq[q], acc[q], 0, 0, 0);
       }
     const auto bo = rows(dx, t0, 4 * n);
-    int ln = lane_n;
+    unsigned ln = lane_n;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int k = 8 * (i >> 2) + (i & 3);
@@ -620,8 +774,8 @@ __global__ __launch_bounds__(256, 1) void pre_bwd_stream_kernel(
       floatx2 v;
 #pragma unroll
       for (int q = 0; q < Q; ++q) v[q] = acc[q][i];
-        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uintx2, v), bo,
-                                              ln + k * 4 * n, 0, kNonTemporal);
+      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uintx2, v), bo, ln + k * 4 * n, 0,
+                                            kNonTemporal);
     }
   }
   if (!in) return;
@@ -691,13 +845,13 @@ __global__ __launch_bounds__(256) void pre_bwd_sums_kernel(const float* __restri
 
 namespace {
 
-// The split of a call's work: token groups of 16*TT tokens times G ranges of the
-// hidden axis for the dots (4 waves, `steps` slices each), `chunks` token ranges
-// of `chunk` for the stream; about 2048 and 1024 waves (8 and 4 per compute unit)
-// where the shape has that many.
+// The split of a call's work: token groups of 16*TT tokens (staged: 16 a wave) times
+// G ranges of the hidden axis for the dots (`steps` slices for each of 4 waves;
+// staged: for the block), `chunks` token ranges of `chunk` for the stream; about
+// 2048 and 1024 waves (8 and 4 per compute unit) where the shape has that many.
 struct Plan {
   int TT, G, HS, steps, SB, chunk, chunks;
-  bool split;
+  bool split, staged;
   size_t planes, part, ua, ut, side, red, dw, floats;  // offsets and total, in floats
 };
 size_t round64(size_t v) { return (v + 63) / 64 * 64; }
@@ -706,13 +860,13 @@ int div_up(int a, int b) { return (a + b - 1) / b; }
 Plan plan(int T, int S, int H, bool f8) {
   Plan p;
   const int R = rows_of(S);
-  p.TT = T <= 16 ? 1 : f8 && S <= 4 && T >= 1024 ? 4 : 2;
-  p.HS = div_up(H, 64);
-  const int groups = div_up(T, 16 * p.TT);
-  const int want = div_up(512, groups);
-  p.steps = div_up(p.HS, 4 * want);
-  p.G = div_up(p.HS, 4 * p.steps);
-  p.split = S > 1 && p.TT < 4 && groups * p.G * S <= 512;
+  p.staged = f8 && T >= 16 * S;
+  p.TT = T <= 16 ? 1 : 2;
+  const int groups = p.staged ? div_up(T, 16 * staged_waves(S)) : div_up(T, 16 * p.TT);
+  const int waves = p.staged ? 1 : 4;  // of a block that divide its slices
+  p.steps = div_up(p.HS = div_up(H, 64), waves * div_up(p.staged && S > 4 ? 256 : 512, groups));
+  p.G = div_up(p.HS, waves * p.steps);
+  p.split = !p.staged && S > 1 && groups * p.G * S <= 512;
   if (p.split) p.G *= S;
   p.SB = div_up(S * H, 128 * kColumns);
   const int groups32 = padded(T) / 32;
@@ -722,7 +876,8 @@ Plan plan(int T, int S, int H, bool f8) {
   p.chunks = div_up(T, p.chunk);
   size_t at = 0;
   p.planes = at;  // 64 lanes of 16 bytes for each step, plane and row tile
-  at += (size_t)S * p.HS * 2 * 3 * div_up(R, 16) * 64 * 4;
+  // (the staged dots read a unit in multiples of 4 or 8 of them, past the last one)
+  at += ((size_t)S * p.HS * 2 * 3 * div_up(R, 16) + 7) * 64 * 4;
   p.part = at;
   at += round64((size_t)p.G * T * (R + 1 + S));
   // three planes of two bytes, 32 tokens by 16 (32) rows a step (tile)
@@ -768,11 +923,19 @@ void run(const PreBwd& a, int T, int H, int iters, float eps, float* work, hipSt
                      st, a.fn_w, R, NRT, S, H, p.HS, F8, frags,
                      reinterpret_cast<bf16x8*>(work + p.planes));
   constexpr bool MANY = S > 1;
-  if (p.TT == 4) {
-    if constexpr (F8 && S <= 4) dots<S, F8, 4, false>(a, p, T, H, KB, work, st);
+  if (p.staged) {
+    if constexpr (F8)
+      hipLaunchKernelGGL((pre_bwd_dots_staged_kernel<S>),
+                         dim3((unsigned)(div_up(T, 16 * staged_waves(S)) * p.G)),
+                         dim3(64 * staged_waves(S)), 0, st,
+                         static_cast<const unsigned char*>(a.x), a.x_scales,
+                         reinterpret_cast<const unsigned char*>(work + p.planes),
+                         reinterpret_cast<const unsigned char*>(a.dy), T, H, KB, p.G, p.HS,
+                         p.steps, part);
   } else if (p.TT == 2) {
-    p.split ? dots<S, F8, 2, MANY>(a, p, T, H, KB, work, st)
-            : dots<S, F8, 2, false>(a, p, T, H, KB, work, st);
+    if constexpr (!F8 || MANY)  // one stream of a checkpoint is staged from 16 tokens on
+      p.split ? dots<S, F8, 2, MANY>(a, p, T, H, KB, work, st)
+              : dots<S, F8, 2, false>(a, p, T, H, KB, work, st);
   } else {
     p.split ? dots<S, F8, 1, MANY>(a, p, T, H, KB, work, st)
             : dots<S, F8, 1, false>(a, p, T, H, KB, work, st);
@@ -807,7 +970,7 @@ size_t pre_bwd_work_bytes(int T, int S, int H) {
   return (a > b ? a : b) * sizeof(float);
 }
 
-// The history of the rounds lies in 64 KiB of LDS beside the staged dots.
+// The gates kernel keeps 512 bytes of history a round in 64 KiB of LDS, and its sums.
 int pre_bwd_max_iters() { return 120; }
 
 hipError_t launch_pre_bwd(const PreBwd& a, int T, int S, int H, int iters, float eps, void* work,

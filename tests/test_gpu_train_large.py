@@ -1,0 +1,170 @@
+"""Sizes at which the 8-bit product and the site's backward passes take their other
+kernels, against 64-bit forms of the whole result."""
+import numpy as np
+import pytest
+
+import plain_forms as pf
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+EPS = float(np.float32(1e-6))
+
+
+@pytest.fixture(scope="module")
+def mhc():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import mhc_hyper_connection_token_amd as m
+    m.load_library()
+    return m
+
+
+def _decode(codes, scales, cols, square=False):
+    """float64 values, from torch's own conversion of a code."""
+    s = torch.exp2(scales.double() - 127)
+    if square:
+        s = s.repeat_interleave(pf.BLOCK, 0)[:codes.shape[0]]
+    return (codes.double() * s.repeat_interleave(pf.BLOCK, 1))[:, :cols].contiguous()
+
+
+def _randn(seed, *shape):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+# Few rows against short and long weights, one and two blocks of 16 rows past a full
+# one, depths of 2 to 66 blocks; then squares of tiles of each size with ragged edges.
+MKN = [(1, 8324, 260), (5, 132, 8196), (16, 4096, 8196), (16, 4100, 8196), (17, 4992, 4100),
+       (32, 388, 8196), (31, 4224, 8196), (33, 260, 8188), (64, 4228, 4100), (64, 260, 8196),
+       (50, 132, 516), (1795, 260, 1668), (1664, 1284, 1924), (3845, 260, 3332),
+       (3584, 1412, 3588), (4093, 4, 4100)]
+
+
+@pytest.mark.parametrize("M,K,N", MKN)
+@pytest.mark.parametrize("square", [True, False])
+def test_matmul(mhc, M, K, N, square):
+    print(f"[case] matmul {M}x{N}x{K} square={square}", flush=True)
+    # rows of sizes that differ by 2^16: a row of a neighbour shows
+    x = _randn(M + K, M, K) * 2.0 ** (torch.arange(M, device="cuda") % 17 - 8).unsqueeze(1)
+    ea = mhc.f8_encode(x)
+    eb = mhc.f8_encode(_randn(N, N, K), square=square)
+    a, b = _decode(*ea, K), _decode(*eb, K, square)
+    want, size = a @ b.t(), a.abs() @ b.abs().t()
+    # exact products; K additions, each off by at most a unit in the last place (2^-23, a
+    # truncating adder included) of a partial sum of at most `size`
+    bound = K * 2.0 ** -23 * size
+    got = mhc.f8_matmul(*ea, *eb, dtype=torch.float32).double()
+    over = ((got - want).abs() - bound).max().item()
+    assert over <= 0, over
+    got = mhc.f8_matmul(*ea, *eb, dtype=torch.bfloat16).double()
+    # and one rounding to bf16 of a value of at most want + bound
+    over = ((got - want).abs() - bound * (1 + 2.0 ** -8) - 2.0 ** -8 * want.abs()).max().item()
+    assert over <= 0, over
+
+
+def _site(T, S, H, seed):
+    R, n = (2 + S) * S, S * H
+    return dict(x=_randn(seed, T, S, H), f=_randn(seed + 1, T, H),
+                w=_randn(seed + 2, R, n) / n ** 0.5, scale=0.5 + _randn(seed + 3, 3).abs(),
+                base=0.3 * _randn(seed + 4, R), g=_randn(seed + 5, T, S, H),
+                dy=_randn(seed + 6, T, H), dpost=_randn(seed + 7, T, S),
+                dcomb=_randn(seed + 8, T, S, S), dx_in=_randn(seed + 9, T, S, H))
+
+
+def _keep(mhc, t, f8):
+    if not f8:
+        return t, t
+    kept = mhc.f8_encode(t)
+    return kept, mhc.f8_decode(*kept, t.shape[-1])
+
+
+@pytest.mark.parametrize("T,S,H", [(2345, 4, 7168), (2400, 8, 4100), (5000, 1, 7172)])
+@pytest.mark.parametrize("f8", [True, False])
+def test_post_bwd_past_the_cache(mhc, T, S, H, f8):
+    print(f"[case] post_bwd T={T} S={S} H={H} f8={f8}", flush=True)
+    assert T * (S + 1) * H * 4 > 256 << 20
+    d = _site(T, S, H, T)
+    post, comb = 2 * torch.sigmoid(d["dpost"]), torch.softmax(d["dcomb"], 2)
+    kx, x = _keep(mhc, d["x"], f8)
+    kf, f = _keep(mhc, d["f"], f8)
+    got = mhc.site_post_bwd(d["g"], kx, kf, post, comb)
+    for t0 in range(0, T, 500):  # 64-bit forms of 500 tokens at a time
+        g, xs, fs, p, c = (t[t0:t0 + 500].double() for t in (d["g"], x, f, post, comb))
+        forms = [lambda g, x, f, p, c: (c.unsqueeze(3) * g.unsqueeze(1)).sum(2),
+                 lambda g, x, f, p, c: (p.unsqueeze(2) * g).sum(1),
+                 lambda g, x, f, p, c: (g * f.unsqueeze(1)).sum(2),
+                 lambda g, x, f, p, c: (x.unsqueeze(2) * g.unsqueeze(1)).sum(3)]
+        args = (g, xs, fs, p, c)
+        for k, (form, terms) in enumerate(zip(forms, (S, S, H, H))):
+            want, size = form(*args), form(*(a.abs() for a in args))
+            # one fp32 rounding a term and one for its product
+            over = (got[k][t0:t0 + 500].double() - want).abs() - (terms + 1) * 2.0 ** -24 * size
+            assert over.max() <= 0, (k, t0, over.max().item())
+
+
+# of the largest entry of a gradient: the same count of roundings as at the small sizes
+# (n up to 57344: sqrt(n) * 2^-24 of the long sums and 170 * 2^-24 of the short part)
+BWD_REL = 2.5e-5
+
+
+@pytest.mark.parametrize("T,S,H", [(513, 1, 132), (520, 2, 516), (777, 3, 260), (1100, 4, 1028),
+                                   (530, 5, 388), (540, 6, 132), (550, 7, 260), (600, 8, 1028),
+                                   (2049, 4, 260), (1601, 4, 4096), (1031, 8, 2052), (512, 4, 4)])
+@pytest.mark.parametrize("f8", [True, False])
+def test_pre_bwd(mhc, T, S, H, f8):
+    print(f"[case] pre_bwd T={T} S={S} H={H} f8={f8}", flush=True)
+    d = _site(T, S, H, 3 * T + S)
+    kx, x = _keep(mhc, d["x"], f8)
+    args = (kx, d["w"], d["scale"], d["base"], 20, EPS, d["dy"], d["dpost"], d["dcomb"])
+    got = mhc.site_pre_bwd(*args, dx_in=d["dx_in"])
+    want = pf.pre_grads(x, d["w"], d["scale"], d["base"], 20, EPS, d["dy"], None, d["dpost"],
+                        d["dcomb"], d["dx_in"])
+    # dscale and dbase share their sums' terms: the size of dbase bounds both
+    short = max(want[2].abs().max().item(), want[3].abs().max().item())
+    for k, n in enumerate(("dx", "dfn_w", "dscale", "dbase")):
+        assert torch.isfinite(got[k]).all(), n
+        size = short if k >= 2 else want[k].abs().max().item()
+        rel = (got[k].double() - want[k]).abs().max().item() / size
+        assert rel <= BWD_REL, f"{n}: {rel:.3e} of the largest entry"
+    for a, b in zip(got, mhc.site_pre_bwd(*args, dx_in=d["dx_in"])):
+        assert torch.equal(a, b)
+
+
+def test_pre_bwd_keeps_a_bad_token_to_itself(mhc):
+    """A token with a NaN code, in one stream: every other token's gradient is what it
+    is without it."""
+    T, S, H = 700, 4, 516
+    print(f"[case] pre_bwd NaN T={T}", flush=True)
+    d = _site(T, S, H, 2)
+    codes, scales = mhc.f8_encode(d["x"])
+
+    def call(codes):
+        return mhc.site_pre_bwd((codes, scales), d["w"], d["scale"], d["base"], 20, EPS,
+                                d["dy"], d["dpost"], d["dcomb"])[0]
+
+    want = call(codes)
+    bad = codes.clone()
+    bad.view(torch.uint8)[333, 2, 515] = 0x7f
+    got = call(bad)
+    assert torch.isnan(got[333]).any()
+    rest = [t for t in range(T) if t != 333]
+    assert torch.equal(got[rest], want[rest])
+
+
+@pytest.mark.parametrize("f8", [True, False])
+def test_pre_bwd_at_the_widest_site(mhc, f8):
+    """S * H = 2^24, where 32 tokens' rows are 2^31 bytes: offsets past 31 bits."""
+    T, S, H = 35, 2, 1 << 23
+    print(f"[case] pre_bwd T={T} S={S} H={H} f8={f8}", flush=True)
+    d = _site(T, S, H, 1)
+    kx, x = _keep(mhc, d["x"], f8)
+    args = (d["w"], d["scale"], d["base"], 20, EPS, d["dy"], d["dpost"], d["dcomb"])
+    got = mhc.site_pre_bwd(kx, *args)
+    want = pf.pre_grads(x, *args[:6], None, *args[6:], None)
+    short = max(want[2].abs().max().item(), want[3].abs().max().item())
+    for k, n in enumerate(("dx", "dfn_w", "dscale", "dbase")):
+        size = short if k >= 2 else want[k].abs().max().item()
+        # sums of 2^24 terms: sqrt(n) * 2^-24 = 2.4e-4 in place of the 1.4e-5 of n = 57344
+        rel = (got[k].double() - want[k]).abs().max().item() / size
+        assert rel <= BWD_REL + 2.4e-4, f"{n}: {rel:.3e} of the largest entry"
