@@ -14,8 +14,8 @@
 // S > 4); the stream that writes dx and adds up dW, a wave owning 64 columns over
 // a range of tokens; and the sums over the ranges and tokens.  x and dy are read
 // twice (neither fits on chip while a token's dots are open); everything else once.
-// At 4096 tokens of 4 x 4096 from a checkpoint: 5 + 44 + 10 + 145 + 5 us; at 1024
-// tokens of 8 x 7168: 11 + 63 + 13 + 173 + 5.
+// At 4096 tokens of 4 x 4096 from a checkpoint: 5 + 42 + 10 + 144 + 5 us, in fp32
+// 5 + 70 + 10 + 165 + 5; at 1024 tokens of 8 x 7168: 11 + 62 + 14 + 175 + 5.
 #include "mhc_f8.h"
 #include "mhc_kernels.h"
 
@@ -81,18 +81,18 @@ __device__ __forceinline__ void planes8(float4 a, float4 b, bf16x8 out[3]) {
 }
 
 // The dots' order of a slice of 64 hidden columns in two steps of 32: the column of
-// entry 4q (q = 0, 1) of lane group g = lane / 16.  Codes: a lane's 16 bytes at 16g,
-// eight to a step.  fp32: four floats at 4g of every 16, so that the four groups
-// read 64 neighbouring bytes.
-__device__ __forceinline__ int dots_column(bool f8, int step, int g, int q) {
-  return f8 ? 16 * g + 8 * step + 4 * q : 32 * step + 16 * q + 4 * g;
+// entry 4q (q = 0, 1) of lane group g = lane / 16.  Codes, and fp32 staged in LDS: a
+// lane's own 16 entries at 16g, eight to a step.  fp32 direct: four floats at 4g of
+// every 16, so that the four groups read 64 neighbouring bytes.
+__device__ __forceinline__ int dots_column(bool own, int step, int g, int q) {
+  return own ? 16 * g + 8 * step + 4 * q : 32 * step + 16 * q + 4 * g;
 }
 
 // W [R][S*H] as row operands of the dots: for stream c, slice, step, plane and
 // row tile of 16, 64 lanes of eight bf16 (row = lane % 16), zeros past R and H.
 __global__ __launch_bounds__(256) void pre_bwd_planes_kernel(const float* __restrict__ w, int R,
                                                              int NRT, int S, int H, int HS,
-                                                             bool f8, long total,
+                                                             bool own, long total,
                                                              bf16x8* __restrict__ out) {
   const long i = (long)blockIdx.x * 256 + threadIdx.x;
   if (i >= total) return;
@@ -105,7 +105,7 @@ __global__ __launch_bounds__(256) void pre_bwd_planes_kernel(const float* __rest
   float4 v[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int col = 64 * slice + dots_column(f8, step, lane >> 4, q);
+    const int col = 64 * slice + dots_column(own, step, lane >> 4, q);
     v[q] = row < R && col < H
                ? *reinterpret_cast<const float4*>(w + ((size_t)row * S + c) * H + col)
                : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -146,7 +146,7 @@ __device__ __forceinline__ void turn_groups(float& v0, float& v1, float& v2, flo
 // Every load of x and dy gives the four lane groups 64 neighbouring bytes of a
 // token; dy, four floats a lane, is then turned between the groups to meet the
 // codes' order.  Bound by waits: a wave asks in turn for dy, x, the planes and the
-// scales, which two waves a SIMD hardly hide (37 tokens of 3 x 4100 in fp32: 8.5 us).
+// scales, which two waves a SIMD hardly hide (one token of 4 x 4096: 4.5 us).
 // SPLIT: a block takes one stream, for batches too short to fill the chip otherwise.
 template <int S, bool F8, int TT, bool SPLIT>
 __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
@@ -279,63 +279,77 @@ __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
   }
 }
 
-// The dots from a checkpoint for batches of 16 S tokens and more, staged: a block
-// takes 16 tokens a wave and walks units of one stream of one slice.  Codes, scales
-// and planes come into LDS by direct loads two units ahead, three stages in turn,
-// dy a slice ahead: the planes are read once a block, and no wave waits for one kind
-// of load after the other.  A token's chunks of 16 bytes are turned in their row
-// (codes: chunk c at place c ^ token / 4 % 4 of four; dy: c ^ token % 16 of
-// sixteen), so that 16 tokens read at one chunk meet all banks.
-// 4096 tokens of 4 x 4096: 62 us by the kernel above, 44 here (x and dy alone: 22);
-// 128 of them: 8.7 and 8.0; 64: 8.5 and 7.6; 17: 6.4 and 7.1.  With S = 8 a unit's
-// planes are 30 KiB and one block fills the unit's LDS: eight waves then
-// (2048 tokens of 8 x 4096: 78 us above, 86 with four waves, 62 with eight); 128
-// tokens 17.0 and 17.4, 64: 11.8 and 15.9.
+// The dots of more than 16 tokens (of 16 S and more with S > 4), staged: a block
+// takes 16 tokens a wave and walks units of one stream of one slice.  x (codes and
+// scales, or fp32) and planes come into LDS by direct loads, two units ahead in
+// three stages in turn (fp32: one ahead, two stages), dy a slice ahead: the planes
+// are read once a block, and no wave waits for one kind of load after the other.  A
+// unit is read into registers before the next loads are asked for, since the
+// compiler lets no read pass a load whose place it cannot tell apart.  A token's
+// chunks of 16 bytes are turned in their row (codes: chunk c at place
+// c ^ token / 4 % 4 of four; fp32: c ^ token % 16 of sixteen), so that 16 tokens read
+// at one chunk meet all banks.
+// The kernel above and this one, us: 4 x 4096, checkpoint, 16 tokens 5.5 and 6.3, 24:
+// 7.4 and 6.3, 4096: 62 and 42; fp32 16: 7.3 and 6.4, 24: 10.3 and 6.3, 4096: 162 and
+// 70 (x and dy alone: 22 and 56).  8 x 4096, where a unit's planes are 30 KiB and
+// eight waves share them: checkpoint 64 tokens 12.1 and 16.6, 96: 16.4 and 16.0, 2048:
+// 78 and 61 (86 with four waves); fp32 64: 15.0 and 19.0, 96: 22.6 and 19.2.
 constexpr int staged_waves(int S) { return S <= 4 ? 4 : 8; }
 
-template <int S>
+template <int S, bool F8>
 __global__ __launch_bounds__(64 * staged_waves(S)) void pre_bwd_dots_staged_kernel(
     const unsigned char* __restrict__ x, const unsigned char* __restrict__ xs,
     const unsigned char* __restrict__ wp, const unsigned char* __restrict__ dy, int T, int H,
     int KB, int G, int HS, int steps, float* __restrict__ part) {
   constexpr int R = rows_of(S), NRT = steps_of(S), V = R + 1 + S, W = staged_waves(S);
-  constexpr int LW = (6 * NRT + W - 1) / W;  // wave loads of planes a unit
-  constexpr int CODES = 16 * W * 64, SCALES = W * 64 * 4;
-  constexpr int STAGE = CODES + SCALES + W * LW * 1024;
+  constexpr int NS = F8 ? 3 : 2;             // stages
+  constexpr int LX = F8 ? 2 : 4;             // a wave's loads of x and scales a unit
+  constexpr int LW = (6 * NRT + W - 1) / W;  // and of planes
+  constexpr int XB = F8 ? 16 * 64 + 64 * 4 : 16 * 256;  // a wave's bytes of them
+  constexpr int STAGE = W * (XB + LW * 1024);
   // one variable a stage: the compiler then knows which loads a read depends on
   __shared__ __align__(16) unsigned char stage0[STAGE];
   __shared__ __align__(16) unsigned char stage1[STAGE];
-  __shared__ __align__(16) unsigned char stage2[STAGE];
+  __shared__ __align__(16) unsigned char stage2[NS > 2 ? STAGE : 16];
   __shared__ float4 dyl[16 * W * 16];
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tb = blockIdx.x / G, gi = blockIdx.x - tb * G, HQ = H >> 2;
   const int first = (tb * W + wave) * 16, t = first + r;  // this wave's tokens, this lane's
-  const int s0 = gi * steps, units = (min(s0 + steps, HS) - s0) * S;
+  const int s0 = gi * steps, units = (min(s0 + steps, HS) - s0) * S, last = units - 1;
   auto stage_of = [&](int i) -> unsigned char* {
     return i == 0 ? stage0 : i == 1 ? stage1 : stage2;
   };
-  // tokens past the end read the last one
-  const size_t crow = (size_t)min(first + (lane >> 2), T - 1) * S;
-  const size_t srow = (size_t)min(t, T - 1) * S;
-  const int chunk = (lane & 3) ^ ((lane >> 4) & 3);
-  auto fetch = [&](int u, int to) {  // unit u into stage `to`: 2 + LW loads
-    const int sl = s0 + u / S, c = u % S;
-    unsigned char* st = stage_of(to);
-    load_to_lds(x + ((crow + c) * KB * 8 + 4 * sl + chunk) * 16, st + wave * 16 * 64);
-    load_byte_to_lds(xs + (srow + c) * KB + (sl >> 1), st + CODES + wave * 256);
-    const unsigned char* w = wp + ((size_t)(c * HS + sl) * 6 * NRT * 64 + lane) * 16;
-#pragma unroll
-    for (int i = 0; i < LW; ++i)
-      load_to_lds(w + (wave + W * i) * 1024, st + CODES + SCALES + (wave + W * i) * 1024);
-  };
-  auto fetch_dy = [&](int sl) {  // four loads of four tokens, a quad past the row the last
+  // four loads of four tokens of `row` quads each, from quad q0 of 16 sl on; tokens past
+  // the end read the last one, quads past the hidden size the last one too
+  auto fetch_quads = [&](const unsigned char* p, size_t row, size_t q0, int sl,
+                         unsigned char* to) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int k = 4 * i + (lane >> 4), q = min(16 * sl + ((lane & 15) ^ k), HQ - 1);
-      load_to_lds(dy + ((size_t)min(first + k, T - 1) * HQ + q) * 16,
-                  reinterpret_cast<unsigned char*>(dyl + (wave * 16 + 4 * i) * 16));
+      load_to_lds(p + ((size_t)min(first + k, T - 1) * row + q0 + q) * 16, to + i * 1024);
     }
+  };
+  auto fetch_dy = [&](int sl) {
+    fetch_quads(dy, HQ, 0, sl, reinterpret_cast<unsigned char*>(dyl + wave * 256));
+  };
+  const size_t crow = (size_t)min(first + (lane >> 2), T - 1) * S;
+  const size_t srow = (size_t)min(t, T - 1) * S;
+  const int chunk = (lane & 3) ^ ((lane >> 4) & 3);
+  auto fetch = [&](int u, int to) {  // unit u into stage `to`: LX + LW loads
+    const int sl = s0 + u / S, c = u % S;
+    unsigned char* st = stage_of(to);
+    unsigned char* sx = st + wave * XB;
+    if constexpr (F8) {
+      load_to_lds(x + ((crow + c) * KB * 8 + 4 * sl + chunk) * 16, sx);
+      load_byte_to_lds(xs + (srow + c) * KB + (sl >> 1), sx + 16 * 64);
+    } else {
+      fetch_quads(x, (size_t)S * HQ, (size_t)c * HQ, sl, sx);
+    }
+    const unsigned char* w = wp + ((size_t)(c * HS + sl) * 6 * NRT * 64 + lane) * 16;
+#pragma unroll
+    for (int i = 0; i < LW; ++i)
+      load_to_lds(w + (wave + W * i) * 1024, st + W * XB + (wave + W * i) * 1024);
   };
   floatx4 acc[NRT];
   float ss = 0.f, dp[S];
@@ -344,66 +358,96 @@ __global__ __launch_bounds__(64 * staged_waves(S)) void pre_bwd_dots_staged_kern
   for (int i = 0; i < S; ++i) dp[i] = 0.f;
 #pragma unroll
   for (int i = 0; i < NRT; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-  const int last = units - 1;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   fetch_dy(s0);
   fetch(0, 0);
-  fetch(min(1, last), 1);
+  if constexpr (NS > 2) fetch(min(1, last), 1);
   int c = 0;
-  for (int u0 = 0; u0 < units; u0 += 3) {
+  for (int u0 = 0; u0 < units; u0 += NS) {
 #pragma unroll
-    for (int here = 0; here < 3; ++here) {
-      const int u = u0 + here;
-      // this unit's stage has landed; what was asked for after it may be on its way: the next
-      // unit's loads, behind the four of dy where the unit before began a slice
-      if (c == 1 % S && u > 0)
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 + LW + 4) : "memory");
+    for (int here = 0; here < NS; ++here) {
+      const int u = u0 + here, sl = s0 + u / S;
+      // this unit's stage has landed.  Of three, the next unit's loads may be on their
+      // way, behind the four of dy where the unit before began a slice.
+      if constexpr (NS == 2)
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      else if (c == 1 % S && u > 0)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LX + LW + 4) : "memory");
       else
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 + LW) : "memory");
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LX + LW) : "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
       if (c == 0) {
-        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int sl = s0 + u / S;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float4 v = dyl[(wave * 16 + r) * 16 + ((4 * g + i) ^ r)];
           d[i] = 16 * sl + 4 * g + i < HQ ? v : zero;
         }
+      }
+      const unsigned char* st = stage_of(here);
+      const unsigned char* sx = st + wave * XB;
+      intx4 code;
+      float4 xq[4];
+      float scale;
+      if constexpr (F8) {
+        code = *reinterpret_cast<const intx4*>(sx + r * 64 + (g ^ ((r >> 2) & 3)) * 16);
+        scale = f8_scale(*reinterpret_cast<const unsigned*>(sx + 16 * 64 + lane * 4) & 255u);
+        if (u > last) code = intx4{0, 0, 0, 0};
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 v = reinterpret_cast<const float4*>(sx)[r * 16 + ((4 * g + i) ^ r)];
+          xq[i] = u <= last && 16 * sl + 4 * g + i < HQ ? v : zero;
+        }
+      }
+      bf16x8 w[6][NRT];
+#pragma unroll
+      for (int p = 0; p < 6; ++p)
+#pragma unroll
+        for (int i = 0; i < NRT; ++i)
+          w[p][i] = *reinterpret_cast<const bf16x8*>(st + W * XB + (p * NRT + i) * 1024 +
+                                                     lane * 16);
+      __builtin_amdgcn_sched_barrier(0);
+      if (c == 0) {
         // the wave's own rows, read just now, make room for the next slice's
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         fetch_dy(min(sl + 1, s0 + last / S));
       }
       // past the end the last unit again, so that the counts above hold to the end
-      fetch(min(u + 2, last), (here + 2) % 3);
-      const unsigned char* st = stage_of(here);
-      intx4 code = *reinterpret_cast<const intx4*>(st + (wave * 16 + r) * 64 +
-                                                   (g ^ ((r >> 2) & 3)) * 16);
-      if (u > last) code = intx4{0, 0, 0, 0};
-      const float scale =
-          f8_scale(*reinterpret_cast<const unsigned*>(st + CODES + wave * 256 + lane * 4) & 255u);
+      fetch(min(u + NS - 1, last), (here + NS - 1) % NS);
+      __builtin_amdgcn_sched_barrier(0);
       float dc = 0.f;
 #pragma unroll
       for (int step = 0; step < 2; ++step) {
-        union {
-          bf16x8 v;
-          unsigned u[4];
-        } o;
-        o.v = f8_to_bf16(code[2 * step], code[2 * step + 1], scale);
-        const float4 xa =
-            make_float4(__uint_as_float(o.u[0] << 16), __uint_as_float(o.u[0] & 0xffff0000u),
-                        __uint_as_float(o.u[1] << 16), __uint_as_float(o.u[1] & 0xffff0000u));
-        const float4 xb =
-            make_float4(__uint_as_float(o.u[2] << 16), __uint_as_float(o.u[2] & 0xffff0000u),
-                        __uint_as_float(o.u[3] << 16), __uint_as_float(o.u[3] & 0xffff0000u));
+        constexpr int XP = F8 ? 1 : 3;
+        bf16x8 o[XP];
+        float4 xa, xb;
+        if constexpr (F8) {
+          union {
+            bf16x8 v;
+            unsigned u[4];
+          } e;
+          e.v = f8_to_bf16(code[2 * step], code[2 * step + 1], scale);
+          xa = make_float4(__uint_as_float(e.u[0] << 16), __uint_as_float(e.u[0] & 0xffff0000u),
+                           __uint_as_float(e.u[1] << 16), __uint_as_float(e.u[1] & 0xffff0000u));
+          xb = make_float4(__uint_as_float(e.u[2] << 16), __uint_as_float(e.u[2] & 0xffff0000u),
+                           __uint_as_float(e.u[3] << 16), __uint_as_float(e.u[3] & 0xffff0000u));
+          o[0] = e.v;
+        } else {
+          xa = xq[2 * step];
+          xb = xq[2 * step + 1];
+          planes8(xa, xb, o);
+        }
         ss = fma4(xb, xb, fma4(xa, xa, ss));
         dc = fma4(d[2 * step + 1], xb, fma4(d[2 * step], xa, dc));
 #pragma unroll
         for (int p = 0; p < 3; ++p)
 #pragma unroll
           for (int i = 0; i < NRT; ++i) {
-            const bf16x8 w = *reinterpret_cast<const bf16x8*>(
-                st + CODES + SCALES + ((step * 3 + p) * NRT + i) * 1024 + lane * 16);
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, o.v, acc[i], 0, 0, 0);
+#pragma unroll
+            for (int m = 0; m < (F8 ? 1 : 3 - p); ++m)
+              acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[step * 3 + p][i], o[m], acc[i], 0,
+                                                               0, 0);
           }
       }
 #pragma unroll
@@ -860,7 +904,7 @@ int div_up(int a, int b) { return (a + b - 1) / b; }
 Plan plan(int T, int S, int H, bool f8) {
   Plan p;
   const int R = rows_of(S);
-  p.staged = f8 && T >= 16 * S;
+  p.staged = S <= 4 ? T > 16 : T >= 16 * S;
   p.TT = T <= 16 ? 1 : 2;
   const int groups = p.staged ? div_up(T, 16 * staged_waves(S)) : div_up(T, 16 * p.TT);
   const int waves = p.staged ? 1 : 4;  // of a block that divide its slices
@@ -920,20 +964,19 @@ void run(const PreBwd& a, int T, int H, int iters, float eps, float* work, hipSt
   constexpr int NRT = steps_of(S);
   const long frags = (long)S * p.HS * 2 * NRT * 64;
   hipLaunchKernelGGL(pre_bwd_planes_kernel, dim3((unsigned)((frags + 255) / 256)), dim3(256), 0,
-                     st, a.fn_w, R, NRT, S, H, p.HS, F8, frags,
+                     st, a.fn_w, R, NRT, S, H, p.HS, F8 || p.staged, frags,
                      reinterpret_cast<bf16x8*>(work + p.planes));
   constexpr bool MANY = S > 1;
   if (p.staged) {
-    if constexpr (F8)
-      hipLaunchKernelGGL((pre_bwd_dots_staged_kernel<S>),
-                         dim3((unsigned)(div_up(T, 16 * staged_waves(S)) * p.G)),
-                         dim3(64 * staged_waves(S)), 0, st,
-                         static_cast<const unsigned char*>(a.x), a.x_scales,
-                         reinterpret_cast<const unsigned char*>(work + p.planes),
-                         reinterpret_cast<const unsigned char*>(a.dy), T, H, KB, p.G, p.HS,
-                         p.steps, part);
+    hipLaunchKernelGGL((pre_bwd_dots_staged_kernel<S, F8>),
+                       dim3((unsigned)(div_up(T, 16 * staged_waves(S)) * p.G)),
+                       dim3(64 * staged_waves(S)), 0, st,
+                       static_cast<const unsigned char*>(a.x), a.x_scales,
+                       reinterpret_cast<const unsigned char*>(work + p.planes),
+                       reinterpret_cast<const unsigned char*>(a.dy), T, H, KB, p.G, p.HS, p.steps,
+                       part);
   } else if (p.TT == 2) {
-    if constexpr (!F8 || MANY)  // one stream of a checkpoint is staged from 16 tokens on
+    if constexpr (S > 4)  // staged with fewer
       p.split ? dots<S, F8, 2, MANY>(a, p, T, H, KB, work, st)
               : dots<S, F8, 2, false>(a, p, T, H, KB, work, st);
   } else {
