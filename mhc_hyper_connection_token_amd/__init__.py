@@ -488,19 +488,28 @@ _entry = {}  # name -> function, so that a small call does not look it up twice
 _gpus = None
 
 
-def _call(name, device, stream, args, others):
+def _on(stream, device, fn, *args, **kw):
+    """fn with `stream` (torch's, or a handle) as the current one, so that what the call
+    allocates belongs to that stream and is not memory that work on another one still uses."""
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the operands on {device}")
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
+
+
+def _call(name, device, args, others):
     """One library call on `device` (an index; the operands' own, made current where it
-    is not), on `stream` or that device's current stream."""
+    is not), on that device's current stream."""
     import torch
     global _gpus
     fn = _entry.get(name)
     if fn is None:
         fn = _entry[name] = getattr(load_library(), name)
         _gpus = torch.cuda.device_count()
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device)
-    elif hasattr(stream, "cuda_stream"):
-        stream = stream.cuda_stream
+    stream = torch._C._cuda_getCurrentRawStream(device)
     if _gpus > 1:
         for t in others:
             if t is not None and t.get_device() != device:
@@ -554,6 +563,8 @@ def f8_encode(x, *, transposed=False, square: bool = False, out=None, stream=Non
     if transposed not in (False, True, "only"):
         raise ValueError('transposed must be False, True or "only"')
     px = _gpu(x, "x", x.dtype)
+    if stream is not None:
+        return _on(stream, x.device, f8_encode, x, transposed=transposed, square=square, out=out)
     lead, cols = tuple(x.shape[:-1]), x.shape[-1]
     rows = 1
     for d in lead:
@@ -573,7 +584,7 @@ def f8_encode(x, *, transposed=False, square: bool = False, out=None, stream=Non
         ptrs += [None, None]
     elif transposed == "only":
         ptrs = [None, None] + ptrs
-    _call("mhc_f8_encode", x.get_device(), stream,
+    _call("mhc_f8_encode", x.get_device(),
           (px, int(x.dtype == torch.bfloat16), rows, cols, int(square), *ptrs), out)
     return out
 
@@ -583,6 +594,8 @@ def f8_repack(codes, scales, cols: int, *, out=None, stream=None):
     matrix codes [rows, P], scales [rows, P/128] of `cols` columns: a kept activation in the
     form a weight gradient's product needs.  `out` may supply that pair."""
     import torch
+    if stream is not None:
+        return _on(stream, codes.device, f8_repack, codes, scales, cols, out=out)
     kb = _blocks(cols)
     if codes.dim() != 2:
         raise ValueError("codes must be [rows, P]")
@@ -592,14 +605,15 @@ def f8_repack(codes, scales, cols: int, *, out=None, stream=None):
     ps = _gpu(scales, "scales", torch.uint8, (rows, kb))
     out, ptrs = _outputs(out, ("out[0]", "out[1]"), ((cols, rb * F8_BLOCK), (cols, rb)),
                          (torch.float8_e4m3fn, torch.uint8), codes.device)
-    _call("mhc_f8_repack", codes.get_device(), stream, (pc, ps, rows, cols, *ptrs),
-          (scales, *out))
+    _call("mhc_f8_repack", codes.get_device(), (pc, ps, rows, cols, *ptrs), (scales, *out))
     return out
 
 
 def f8_decode(codes, scales, cols: int, *, out=None, stream=None):
     """The float32 values [..., cols] of 8-bit blocks codes [..., P], scales [..., P/128]."""
     import torch
+    if stream is not None:
+        return _on(stream, codes.device, f8_decode, codes, scales, cols, out=out)
     kb = _blocks(cols)
     lead = tuple(codes.shape[:-1])
     pc = _gpu(codes, "codes", torch.float8_e4m3fn, (*lead, kb * F8_BLOCK))
@@ -609,7 +623,7 @@ def f8_decode(codes, scales, cols: int, *, out=None, stream=None):
     rows = 1
     for d in lead:
         rows *= d
-    _call("mhc_f8_decode", codes.get_device(), stream,
+    _call("mhc_f8_decode", codes.get_device(),
           (pc, ps, rows, cols, _gpu(out, "out", torch.float32, (*lead, cols))), (scales, out))
     return out
 
@@ -619,6 +633,8 @@ def f8_matmul(a, a_scales, b, b_scales, *, dtype=None, out=None, stream=None):
     bfloat16.  K is the padded width of both (a multiple of 128).  b_scales is [N, K/128],
     or [ceil(N/128), K/128] for the square form of a weight."""
     import torch
+    if stream is not None:
+        return _on(stream, a.device, f8_matmul, a, a_scales, b, b_scales, dtype=dtype, out=out)
     if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
         raise ValueError("a must be [M, K] and b [N, K]")
     (M, K), N = a.shape, b.shape[0]
@@ -636,7 +652,7 @@ def f8_matmul(a, a_scales, b, b_scales, *, dtype=None, out=None, stream=None):
         po = out.data_ptr()
     else:
         po = _gpu(out, "out", dtype, (M, N))
-    _call("mhc_f8_matmul", a.get_device(), stream,
+    _call("mhc_f8_matmul", a.get_device(),
           (pa, pas, pb, pbs, int(square), M, N, K, po, int(dtype == torch.bfloat16)),
           (a_scales, b, b_scales, out))
     return out
@@ -662,6 +678,8 @@ def site_post_bwd(g, x, f, post, comb, *, out=None, stream=None):
     that f8_encode(x), f8_encode(f) returned.  Returns (dx [T,S,H], df [T,H], dpost [T,S],
     dcomb [T,S,S]); `out` may supply that tuple."""
     import torch
+    if stream is not None:
+        return _on(stream, g.device, site_post_bwd, g, x, f, post, comb, out=out)
     if g.dim() != 3:
         raise ValueError("g must be [T, S, H]")
     T, S, H = g.shape
@@ -671,7 +689,7 @@ def site_post_bwd(g, x, f, post, comb, *, out=None, stream=None):
     pf, pfs, tf = _kept(f, "f", (T,), H)
     out, po = _outputs(out, ("dx", "df", "dpost", "dcomb"),
                        ((T, S, H), (T, H), (T, S), (T, S, S)), (f32, f32, f32, f32), g.device)
-    _call("mhc_site_post_bwd", g.get_device(), stream,
+    _call("mhc_site_post_bwd", g.get_device(),
           (pg, px, pxs, pf, pfs, _gpu(post, "post", f32, (T, S)),
            _gpu(comb, "comb", f32, (T, S, S)), T, S, H, *po),
           (*tx, *tf, post, comb, *out))
@@ -700,6 +718,9 @@ def site_pre_bwd(x, fn_w, scale, base, iters: int, eps: float, dy, dpost, dcomb,
     dfn_w, dscale, dbase); `out` may supply that tuple.  `work` is a uint8 tensor of at
     least site_pre_bwd_work_bytes bytes (allocated per call when not given)."""
     import torch
+    if stream is not None:
+        return _on(stream, dy.device, site_pre_bwd, x, fn_w, scale, base, iters, eps, dy, dpost,
+                   dcomb, dpre=dpre, dx_in=dx_in, out=out, work=work)
     if dy.dim() != 2 or dcomb.dim() != 3:
         raise ValueError("dy must be [T, H] and dcomb [T, S, S]")
     (T, H), S = dy.shape, dcomb.shape[1]
@@ -710,11 +731,7 @@ def site_pre_bwd(x, fn_w, scale, base, iters: int, eps: float, dy, dpost, dcomb,
                        ((T, S, H), (R, S * H), (3,), (R,)), (f32, f32, f32, f32), dy.device)
     if work is None:
         work = torch.empty(site_pre_bwd_work_bytes(T, S, H), device=dy.device, dtype=torch.uint8)
-        if isinstance(stream, torch.cuda.Stream):
-            work.record_stream(stream)
-        elif stream is not None:
-            work.record_stream(torch.cuda.ExternalStream(int(stream), device=dy.device))
-    _call("mhc_site_pre_bwd", dy.get_device(), stream,
+    _call("mhc_site_pre_bwd", dy.get_device(),
           (px, pxs, _gpu(fn_w, "fn_w", f32, (R, S * H)), _gpu(scale, "scale", f32, (3,)),
            _gpu(base, "base", f32, (R,)), T, S, H, int(iters), float(eps),
            _gpu(dy, "dy", f32), None if dpre is None else _gpu(dpre, "dpre", f32, (T, S)),

@@ -342,8 +342,8 @@ struct Args {
 template <int MT, int NF, int W, int U, typename O>
 void narrow(const Args<O>& p) {
   hipLaunchKernelGGL((f8_matmul_narrow_kernel<MT, NF, W, U, O>),
-                     dim3((p.N + 16 * NF - 1) / (16 * NF)), dim3(64 * W), 0, p.st, p.a, p.as, p.b, p.bs, p.bshift, p.M, p.N, p.KB,
-                     p.out);
+                     dim3((p.N + 16 * NF - 1) / (16 * NF)), dim3(64 * W), 0, p.st, p.a, p.as,
+                     p.b, p.bs, p.bshift, p.M, p.N, p.KB, p.out);
 }
 template <int FM, int FN, int WM, int WN, int NS, typename O>
 void tile(const Args<O>& p) {
@@ -366,18 +366,21 @@ void matmul(const Args<O>& p) {
   // N = K = 16384: 48 against 56).  From 33 rows of a wide weight the tiles are
   // faster (M = 64, N = 16384: 22.9 against 24.7 us).
   const bool wide = p.N >= 8192 && p.KB <= 32;
+  const int side = p.M < p.N ? p.M : p.N;
   if (p.M <= 16) {
     wide ? narrow<1, 4, 8, 4>(p) : narrow<1, 1, 16, 2>(p);
   } else if (p.M <= 32) {
     wide ? narrow<2, 4, 8, 4>(p) : narrow<2, 1, 16, 2>(p);
   } else if (p.M <= 64 && p.N < 8192) {
     narrow<4, 1, 16, 2>(p);
-  // The largest tiles that give most compute units one: 256 x 256 (7168 x 4096 x 1024:
-  // 69 us, 128 x 128 68, but at 4096 x 16384 x 4096 540 against 580), 128 x 128
-  // (1024 x 4096 x 4096: 41 us, 64 x 64 62), 64 x 64 three to a unit.
-  } else if (tiles_of(p.M, p.N, 256, 256) >= 192) {
+  // The largest tiles that give most compute units one and are not half empty: 256 x 256
+  // (7168 x 4096 x 1024: 69 us, 128 x 128 68, but at 4096 x 16384 x 4096 540 against
+  // 580; 192 x 65536 x 1024 36 and 40, 128 x 65536 x 1024 33 and 25), 128 x 128
+  // (1024 x 4096 x 4096: 41 us, 64 x 64 62; 65536 x 128 x 4096 84 and 106, 32768 x 64 x
+  // 4096 43 and 33), 64 x 64 three to a unit.
+  } else if (side > 128 && tiles_of(p.M, p.N, 256, 256) >= 192) {
     tile<4, 2, 2, 4, 2>(p);
-  } else if (tiles_of(p.M, p.N, 128, 128) >= 192) {
+  } else if (side > 64 && tiles_of(p.M, p.N, 128, 128) >= 192) {
     tile<2, 1, 2, 4, 2>(p);
   } else {
     tile<1, 1, 2, 2, 3>(p);

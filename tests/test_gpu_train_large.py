@@ -38,7 +38,8 @@ def _randn(seed, *shape):
 MKN = [(1, 8324, 260), (5, 132, 8196), (16, 4096, 8196), (16, 4100, 8196), (17, 4992, 4100),
        (32, 388, 8196), (31, 4224, 8196), (33, 260, 8188), (64, 4228, 4100), (64, 260, 8196),
        (50, 132, 516), (1795, 260, 1668), (1664, 1284, 1924), (3845, 260, 3332),
-       (3584, 1412, 3588), (4093, 4, 4100)]
+       (3584, 1412, 3588), (4093, 4, 4100), (24700, 132, 68), (100, 388, 24900),
+       (70001, 260, 4), (12500, 260, 64), (66, 516, 65540)]
 
 
 @pytest.mark.parametrize("M,K,N", MKN)
@@ -168,3 +169,39 @@ def test_pre_bwd_at_the_widest_site(mhc, f8):
         # sums of 2^24 terms: sqrt(n) * 2^-24 = 2.4e-4 in place of the 1.4e-5 of n = 57344
         rel = (got[k].double() - want[k]).abs().max().item() / size
         assert rel <= BWD_REL + 2.4e-4, f"{n}: {rel:.3e} of the largest entry"
+
+
+def test_outputs_belong_to_the_stream_given(mhc):
+    """A call on another stream must not get memory that pending work of the current
+    stream still writes: a long product, then a fill of a block that is freed at once."""
+    print("[case] outputs on a side stream", flush=True)
+    x = _randn(1, 2048, 4, 512)
+    g, f = _randn(2, 2048, 4, 512), _randn(3, 2048, 512)
+    post, comb = _randn(4, 2048, 4), _randn(5, 2048, 4, 4)
+    codes, scales = mhc.f8_encode(x)
+    wc, ws = mhc.f8_encode(_randn(6, 512, 512), square=True)
+    z = mhc.f8_encode(f)
+    w = _randn(7, 24, 2048)
+    small = _randn(8, 24)
+    calls = [lambda **k: mhc.f8_encode(x, **k),
+             lambda **k: (mhc.f8_decode(codes, scales, 512, **k),),
+             lambda **k: mhc.f8_repack(codes.view(8192, 512), scales.view(8192, 4), 512, **k),
+             lambda **k: (mhc.f8_matmul(*z, wc, ws, **k),),
+             lambda **k: mhc.site_post_bwd(g, x, f, post, comb, **k),
+             lambda **k: mhc.site_pre_bwd(x, w, small[:3], small, 20, EPS, f, post, comb, **k)]
+    want = [[t.clone() for t in call()] for call in calls]
+    side = torch.cuda.Stream()
+    a = _randn(9, 8192, 8192)
+    for how in (side, side.cuda_stream):
+        for k, call in enumerate(calls):
+            torch.cuda.synchronize()
+            a @ a  # some milliseconds
+            for t in want[k]:
+                torch.empty_like(t).view(torch.uint8).fill_(0x55)
+            got = call(stream=how)
+            torch.cuda.synchronize()
+            for p, q in zip(got, want[k]):
+                assert torch.equal(p.view(torch.uint8), q.view(torch.uint8)), k
+    if torch.cuda.device_count() > 1:
+        with pytest.raises(ValueError):
+            calls[0](stream=torch.cuda.Stream(device=1))
