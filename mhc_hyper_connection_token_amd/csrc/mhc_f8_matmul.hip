@@ -139,33 +139,38 @@ constexpr int kPanel = 32;  // k blocks whose scales are held in LDS
 // the 16 x 16 ones.  The codes of one k block (128 bytes a row) are staged in LDS
 // by direct loads, NS stages in turn: while one block is multiplied the loads of
 // the NS - 1 after it are under way, and one barrier a block keeps the waves in
-// step.  A lane's 16 bytes are read a chunk ahead of their use and converted next
-// to it; converted on the way into LDS instead (once, not by every wave) the
-// bytes in LDS double, and 333 x 7168 x 7168 took 79 us against 55.
+// step.  With KG > 1 a stage holds KG blocks, each for a group of waves of its own
+// (WM x WN waves again), and the groups' sums are added in order at the end: more
+// waves on a tile where there are few tiles.  A lane's 16 bytes are read a chunk
+// ahead of their use and converted next to it; converted on the way into LDS instead
+// (once, not by every wave) the bytes in LDS double, and 333 x 7168 x 7168 took 79 us
+// against 55.
 // Within a row's 128 bytes the 16-byte chunk c lies at place c ^ (row / 2 % 8), so
 // that sixteen rows read at one chunk meet all 64 banks; the place is chosen on
 // the global side, since a direct load writes its lanes in order.
 // What bounds it: with neither loads nor conversions the products alone take
 // 442 us at 4096 x 16384 x 4096 (1240 TFLOP/s; the library's bf16 product of these
 // sizes 420), with them 540: the conversions cost 50, the staging 50.
-template <int FM, int FN, int WM, int WN, int NS, typename O>
-__global__ __launch_bounds__(64 * WM * WN, 2) void f8_matmul_tile_kernel(
+template <int FM, int FN, int WM, int WN, int NS, int KG, typename O>
+__global__ __launch_bounds__(64 * WM * WN * KG, 2) void f8_matmul_tile_kernel(
     const unsigned char* __restrict__ a, const unsigned char* __restrict__ as,
     const unsigned char* __restrict__ b, const unsigned char* __restrict__ bs, int bshift, int M,
     int N, int KB, int MT, int NT, O* __restrict__ out) {
-  constexpr int W = WM * WN, BM = 32 * FM * WM, BN = 32 * FN * WN;
-  constexpr int LOADS = (BM + BN) / 8 / W;  // wave loads (8 rows of 128 bytes) a stage
-  static_assert(LOADS * 8 * W == BM + BN && BM % 8 == 0, "whole wave loads");
+  constexpr int W = WM * WN * KG, BM = 32 * FM * WM, BN = 32 * FN * WN, ROWS = BM + BN;
+  constexpr int LOADS = KG * ROWS / 8 / W;  // wave loads (8 rows of 128 bytes) a stage
+  constexpr int STAGE = KG * ROWS * kF8Block;
+  static_assert(LOADS * 8 * W == KG * ROWS && BM % 8 == 0, "whole wave loads");
+  static_assert(kPanel % KG == 0 && (KG - 1) * WM * WN * FM * FN * 4096 <= STAGE, "sums fit");
   // one variable a stage: the compiler then knows which loads a read depends on
-  __shared__ __align__(16) unsigned char stage0[(BM + BN) * kF8Block];
-  __shared__ __align__(16) unsigned char stage1[(BM + BN) * kF8Block];
-  __shared__ __align__(16) unsigned char stage2[NS > 2 ? (BM + BN) * kF8Block : 16];
-  __shared__ __align__(16) unsigned char stage3[NS > 3 ? (BM + BN) * kF8Block : 16];
-  __shared__ unsigned char panel[kPanel][BM + BN];
+  __shared__ __align__(16) unsigned char stage0[STAGE];
+  __shared__ __align__(16) unsigned char stage1[STAGE];
+  __shared__ __align__(16) unsigned char stage2[NS > 2 ? STAGE : 16];
+  __shared__ unsigned char panel[kPanel][ROWS];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, h = lane >> 5;
-  const int wm = wave % WM, wn = wave / WM;
+  const int wm = wave % WM, wn = wave / WM % WN, kg = wave / (WM * WN);
+  const int KI = (KB + KG - 1) / KG;  // stages of KG blocks
 
   // Blocks go to the eight dies in turn: give each die a run of tiles, and walk
   // them eight rows of tiles at a time, so that its L2 sees few panels at once.
@@ -184,7 +189,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_matmul_tile_kernel(
   const unsigned char* src[LOADS];
 #pragma unroll
   for (int i = 0; i < LOADS; ++i) {
-    const int row = 8 * (i * W + wave) + (lane >> 3);
+    const int row = 8 * (i * W + wave) % ROWS + (lane >> 3);
     const int chunk = (lane & 7) ^ ((row >> 1) & 7);
     src[i] = (row < BM ? a + min(m0 + row, M - 1) * pitch
                        : b + min(n0 + row - BM, N - 1) * pitch) + chunk * 16;
@@ -198,21 +203,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_matmul_tile_kernel(
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
 
   auto stage_of = [&](int i) -> unsigned char* {
-    return i == 0 ? stage0 : i == 1 ? stage1 : i == 2 ? stage2 : stage3;
+    return i == 0 ? stage0 : i == 1 ? stage1 : stage2;
   };
-  // part p of three of this wave's loads of k block kb, into stage `to`
-  auto fetch = [&](int kb, int to, int p) {
+  // part p of three of this wave's loads of the KG blocks ki, into stage `to` (a block
+  // past the end: the last one, which nobody reads)
+  auto fetch = [&](int ki, int to, int p) {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i)
-      if (i * 3 / LOADS == p)
+      if (i * 3 / LOADS == p) {
+        const int kb = KG == 1 ? ki : min(ki * KG + 8 * (i * W + wave) / ROWS, KB - 1);
         load_to_lds(src[i] + (size_t)kb * kF8Block,
                     stage_of(to) + 8 * (i * W + wave) * kF8Block);
+      }
   };
   // The scale bytes of the next kPanel blocks, turned so that a lane reads its row's
   // beside its neighbours': straight from memory every lane would meet a line of
   // its own, for each row of products and each block.
   auto load_panel = [&](int kb) {
-    for (int row = threadIdx.x; row < BM + BN; row += 64 * W) {
+    for (int row = threadIdx.x; row < ROWS; row += 64 * W) {
       const unsigned char* p =
           row < BM ? as + (size_t)min(m0 + row, M - 1) * KB
                    : bs + (size_t)(min(n0 + row - BM, N - 1) >> bshift) * KB;
@@ -228,31 +236,30 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_matmul_tile_kernel(
     }
   };
   float fa[FM], fb[FN];
-  // Block kb has landed (this wave's part; the barrier adds the others') while the
-  // NS - 2 blocks after it may be on their way, and every wave has taken what it
-  // needs of the block before it and of the panel.
-  auto turn = [&](int kb) {
-    if (NS > 2 && kb + NS - 2 < KB)
+  // Stage ki has landed (this wave's part; the barrier adds the others') while the
+  // NS - 2 stages after it may be on their way, and every wave has taken what it
+  // needs of the stage before it and of the panel.
+  auto turn = [&](int ki) {
+    if (NS > 2 && ki + NS - 2 < KI)
       asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LOADS * (NS - 2)) : "memory");
     else
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (kb % kPanel == 0) {
-      load_panel(kb);
+    if (ki % (kPanel / KG) == 0) {
+      load_panel(ki * KG);
       __syncthreads();
     }
+    const unsigned char* scales = panel[ki % (kPanel / KG) * KG + kg];
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-      fa[i] = f8_scale(panel[kb % kPanel][(wm * FM + i) * 32 + r]);
+    for (int i = 0; i < FM; ++i) fa[i] = f8_scale(scales[(wm * FM + i) * 32 + r]);
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-      fb[j] = f8_scale(panel[kb % kPanel][BM + (wn * FN + j) * 32 + r]);
+    for (int j = 0; j < FN; ++j) fb[j] = f8_scale(scales[BM + (wn * FN + j) * 32 + r]);
   };
   intx4 av[2][FM], bv[2][FN];
   auto read = [&](int from, int c, int to) {
-    const unsigned char* arow = stage_of(from) + (wm * FM * 32 + r) * kF8Block;
-    const unsigned char* brow = stage_of(from) + (BM + wn * FN * 32 + r) * kF8Block;
+    const unsigned char* arow = stage_of(from) + (kg * ROWS + wm * FM * 32 + r) * kF8Block;
+    const unsigned char* brow = stage_of(from) + (kg * ROWS + BM + wn * FN * 32 + r) * kF8Block;
     const int place = ((2 * c + h) ^ ((r >> 1) & 7)) * 16;
 #pragma unroll
     for (int j = 0; j < FN; ++j)
@@ -261,21 +268,21 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_matmul_tile_kernel(
     for (int i = 0; i < FM; ++i)
       av[to][i] = *reinterpret_cast<const intx4*>(arow + i * 32 * kF8Block + place);
   };
-  if (KB > 0) {
+  if (KI > 0) {
 #pragma unroll
     for (int k = 0; k < NS - 1; ++k)
 #pragma unroll
       for (int p = 0; p < 3; ++p)
-        if (k < KB) fetch(k, k, p);
+        if (k < KI) fetch(k, k, p);
     turn(0);
     read(0, 0, 0);
-    if (NS - 1 < KB) fetch(NS - 1, NS - 1, 0);
+    if (NS - 1 < KI) fetch(NS - 1, NS - 1, 0);
   }
-  for (int k0 = 0; k0 < KB; k0 += NS) {
+  for (int k0 = 0; k0 < KI; k0 += NS) {
 #pragma unroll
     for (int here = 0; here < NS; ++here) {
-      const int kb = k0 + here, free = (here + NS - 1) % NS;
-      if (kb >= KB) break;
+      const int ki = k0 + here, free = (here + NS - 1) % NS;
+      if (ki >= KI) break;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         float ga[FM], gb[FN];
@@ -285,15 +292,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_matmul_tile_kernel(
         for (int j = 0; j < FN; ++j) gb[j] = fb[j];
         // The next chunk is read while this one is multiplied; with the last chunk in
         // registers the stage is done with, the next one is turned to, and the loads
-        // of a later block into the free stage begin, a third at a time.
+        // of a later one into the free stage begin, a third at a time.
         if (c < 3) {
           read(here, c + 1, (c + 1) & 1);
-          if (c < 2 && kb + NS - 1 < KB) fetch(kb + NS - 1, free, c + 1);
-        } else if (kb + 1 < KB) {
-          turn(kb + 1);
+          if (c < 2 && ki + NS - 1 < KI) fetch(ki + NS - 1, free, c + 1);
+        } else if (ki + 1 < KI) {
+          turn(ki + 1);
           read((here + 1) % NS, 0, 0);
-          if (kb + NS < KB) fetch(kb + NS, here, 0);
+          if (ki + NS < KI) fetch(ki + NS, here, 0);
         }
+        if (KG > 1 && ki * KG + kg >= KB) continue;  // a group past the end
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           bf16x8 ax[FM], bx[FN];
@@ -311,6 +319,39 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_matmul_tile_kernel(
         }
       }
     }
+  }
+  if constexpr (KG > 1) {  // the groups' sums, in their order, through the first stage
+    float4* sums = reinterpret_cast<float4*>(stage0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (kg > 0) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            sums[(((wave - WM * WN) * FM + i) * FN + j) * 256 + v * 64 + lane] =
+                make_float4(acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2],
+                            acc[i][j][4 * v + 3]);
+    }
+    __syncthreads();
+    if (kg > 0) return;
+#pragma unroll
+    for (int k = 1; k < KG; ++k)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float4 o =
+                sums[((((k - 1) * WM * WN + wave) * FM + i) * FN + j) * 256 + v * 64 + lane];
+            acc[i][j][4 * v] += o.x;
+            acc[i][j][4 * v + 1] += o.y;
+            acc[i][j][4 * v + 2] += o.z;
+            acc[i][j][4 * v + 3] += o.w;
+          }
   }
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
@@ -345,13 +386,13 @@ void narrow(const Args<O>& p) {
                      dim3((p.N + 16 * NF - 1) / (16 * NF)), dim3(64 * W), 0, p.st, p.a, p.as,
                      p.b, p.bs, p.bshift, p.M, p.N, p.KB, p.out);
 }
-template <int FM, int FN, int WM, int WN, int NS, typename O>
+template <int FM, int FN, int WM, int WN, int NS, int KG, typename O>
 void tile(const Args<O>& p) {
   const int MT = (p.M + 32 * FM * WM - 1) / (32 * FM * WM);
   const int NT = (p.N + 32 * FN * WN - 1) / (32 * FN * WN);
-  hipLaunchKernelGGL((f8_matmul_tile_kernel<FM, FN, WM, WN, NS, O>), dim3((unsigned)(MT * NT)),
-                     dim3(64 * WM * WN), 0, p.st, p.a, p.as, p.b, p.bs, p.bshift, p.M, p.N, p.KB,
-                     MT, NT, p.out);
+  hipLaunchKernelGGL((f8_matmul_tile_kernel<FM, FN, WM, WN, NS, KG, O>),
+                     dim3((unsigned)(MT * NT)), dim3(64 * WM * WN * KG), 0, p.st, p.a, p.as, p.b,
+                     p.bs, p.bshift, p.M, p.N, p.KB, MT, NT, p.out);
 }
 long tiles_of(long M, long N, long bm, long bn) {
   return ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
@@ -359,31 +400,37 @@ long tiles_of(long M, long N, long bm, long bn) {
 
 template <typename O>
 void matmul(const Args<O>& p) {
-  // Few rows: the weight streams through.  Wide and at most 32 blocks deep, 64
-  // columns a block with the whole depth in flight (M = 8, N = 16384, K = 4096:
-  // 13.9 us, against 17.1 at 16 columns and 16 waves); else 16 columns a block, for
-  // as many blocks as there are (M = 1, N = K = 4096: 5.6 against 11 us;
-  // N = K = 16384: 48 against 56).  From 33 rows of a wide weight the tiles are
-  // faster (M = 64, N = 16384: 22.9 against 24.7 us).
-  const bool wide = p.N >= 8192 && p.KB <= 32;
+  // Few rows: the weight streams through the narrow kernel, 16 columns a block for as
+  // many blocks as there are.  Where 64 columns a block still leave a hundred blocks
+  // and more: the whole depth of 32 blocks in flight (8 x 16384 x 4096: 13.6 us, 16.7
+  // at 16 columns; 1 x 16384 x 4096 13.7 and 13.1; 8 x 8192 x 4096 12.6 and 9.9), or,
+  // for shallow products and from 17 rows on, the tiles with four blocks of the depth
+  // at a time (16 x 7168 x 2048 8.6 us against 11.3, 1 x 16384 x 2048 10.4 and 12.6, 1 x
+  // 8192 x 2048 8.8 and 8.0, 16 x 8192 x 4096 14.3 and 11.9; 32 x 8192 x 4096 14.6 and
+  // 17.9, 32 x 4096 x 4096 13.8 and 9.9).
+  const long tiles64 = tiles_of(p.M, p.N, 64, 64);
   const int side = p.M < p.N ? p.M : p.N;
-  if (p.M <= 16) {
-    wide ? narrow<1, 4, 8, 4>(p) : narrow<1, 1, 16, 2>(p);
-  } else if (p.M <= 32) {
-    wide ? narrow<2, 4, 8, 4>(p) : narrow<2, 1, 16, 2>(p);
-  } else if (p.M <= 64 && p.N < 8192) {
-    narrow<4, 1, 16, 2>(p);
+  const bool shallow = p.KB <= 16 && (p.N >= 16384 || (p.M > 8 && p.N >= 5120));
+  if (p.M <= 16 && !shallow) {
+    p.M > 4 && p.N >= 16384 ? narrow<1, 4, 8, 4>(p) : narrow<1, 1, 16, 2>(p);
+  } else if (p.M <= 32 && p.N < 5120) {
+    narrow<2, 1, 16, 2>(p);
+  // One tile to a compute unit at most: eight waves on it, in four groups that take
+  // every fourth block of the depth (100 x 7168 x 7168 23 us against 36 with four waves
+  // and no groups, 128 x 4096 x 1024 7.1 and 7.6, 70 x 4096 x 256 5.2 and 4.7).
+  } else if (p.M <= 32 || (tiles64 <= 256 && p.KB >= 8)) {
+    tile<2, 1, 1, 2, 2, 4>(p);
   // The largest tiles that give most compute units one and are not half empty: 256 x 256
   // (7168 x 4096 x 1024: 69 us, 128 x 128 68, but at 4096 x 16384 x 4096 540 against
   // 580; 192 x 65536 x 1024 36 and 40, 128 x 65536 x 1024 33 and 25), 128 x 128
   // (1024 x 4096 x 4096: 41 us, 64 x 64 62; 65536 x 128 x 4096 84 and 106, 32768 x 64 x
   // 4096 43 and 33), 64 x 64 three to a unit.
   } else if (side > 128 && tiles_of(p.M, p.N, 256, 256) >= 192) {
-    tile<4, 2, 2, 4, 2>(p);
+    tile<4, 2, 2, 4, 2, 1>(p);
   } else if (side > 64 && tiles_of(p.M, p.N, 128, 128) >= 192) {
-    tile<2, 1, 2, 4, 2>(p);
+    tile<2, 1, 2, 4, 2, 1>(p);
   } else {
-    tile<1, 1, 2, 2, 3>(p);
+    tile<1, 1, 2, 2, 3, 1>(p);
   }
 }
 }  // namespace

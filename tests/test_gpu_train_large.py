@@ -39,7 +39,9 @@ MKN = [(1, 8324, 260), (5, 132, 8196), (16, 4096, 8196), (16, 4100, 8196), (17, 
        (32, 388, 8196), (31, 4224, 8196), (33, 260, 8188), (64, 4228, 4100), (64, 260, 8196),
        (50, 132, 516), (1795, 260, 1668), (1664, 1284, 1924), (3845, 260, 3332),
        (3584, 1412, 3588), (4093, 4, 4100), (24700, 132, 68), (100, 388, 24900),
-       (70001, 260, 4), (12500, 260, 64), (66, 516, 65540)]
+       (70001, 260, 4), (12500, 260, 64), (66, 516, 65540), (16, 4096, 16388),
+       (9, 8324, 16388), (16, 2048, 5124), (3, 260, 16388), (32, 516, 20004),
+       (100, 1156, 1028), (200, 8452, 1988), (65, 1024, 16380)]
 
 
 @pytest.mark.parametrize("M,K,N", MKN)
