@@ -484,8 +484,10 @@ __global__ __launch_bounds__(64 * staged_waves(S)) void pre_bwd_dots_staged_kern
 // from it the entries and the reciprocal sums, which do not depend on the
 // gradient: they are fetched one round ahead, so that a pass of the dependent
 // chain is a product, two lane exchanges, a difference and a product.
+// Four waves: all add up the dots' ranges, wave 0 takes the rounds while wave 1 takes
+// the other gates, and each writes the results of a token of its own.
 template <int S>
-__global__ __launch_bounds__(64) void pre_bwd_gates_kernel(
+__global__ __launch_bounds__(256) void pre_bwd_gates_kernel(
     const float* __restrict__ part, int G, int T, int n, const float* __restrict__ scale,
     const float* __restrict__ base, int iters, float eps, const float* __restrict__ dpre,
     const float* __restrict__ dpost, const float* __restrict__ dcomb,
@@ -493,28 +495,37 @@ __global__ __launch_bounds__(64) void pre_bwd_gates_kernel(
     float* __restrict__ red) {
   constexpr int L = S <= 4 ? 4 : 8, NU = L == 4 ? 4 : 1;
   constexpr int R = rows_of(S), KS = steps_of(S), NRT = tiles_of(S), V = R + 1 + S;
-  __shared__ float raw[NU][V], dzs[NU][R];
+  constexpr int IN = NU * V, PARTS = 256 / IN;
+  __shared__ float sums[PARTS][IN], raw[NU][V], dzs[NU][R];
   extern __shared__ float hist[];
-  const int lane = threadIdx.x, t0 = blockIdx.x * NU;
+  const int lane = threadIdx.x & 63, t0 = blockIdx.x * NU;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const size_t TP = padded(T);
-  for (int i = lane; i < NU * V; i += 64) {
-    const int k = i / V, v = i - k * V;
-    const float* p = part + (size_t)min(t0 + k, T - 1) * V + v;
+  if (threadIdx.x < PARTS * IN) {  // every PARTS-th range of one value
+    const int q = threadIdx.x / IN, i = threadIdx.x - q * IN, k = i / V, v = i - k * V;
     const size_t step = (size_t)T * V;
+    const float* p = part + (size_t)min(t0 + k, T - 1) * V + v;
     float s = 0.f;
-    int gi = 0;
-    for (; gi + 8 <= G; gi += 8, p += 8 * step) {
+    int gi = q;
+    for (; gi + 7 * PARTS < G; gi += 8 * PARTS) {
       float w[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) w[q] = p[q * step];
+      for (int e = 0; e < 8; ++e) w[e] = p[(gi + e * PARTS) * step];
       s += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
     }
-    for (; gi + 2 <= G; gi += 2, p += 2 * step) s += p[0] + p[step];
-    if (gi < G) s += p[0];
-    raw[k][v] = s;
+    for (; gi + PARTS < G; gi += 2 * PARTS) s += p[gi * step] + p[(gi + PARTS) * step];
+    if (gi < G) s += p[gi * step];
+    sums[q][i] = s;
   }
   __syncthreads();
-  {
+  if (threadIdx.x < IN) {
+    float s = sums[0][threadIdx.x];
+#pragma unroll
+    for (int q = 1; q < PARTS; ++q) s += sums[q][threadIdx.x];
+    raw[threadIdx.x / V][threadIdx.x % V] = s;
+  }
+  __syncthreads();
+  if (wave == 1) {
     const int k = L == 4 ? lane >> 3 : 0, gt = L == 4 ? lane & 7 : lane;
     const size_t t = t0 + k;
     if (k < NU && t < (size_t)T && gt < 2 * S) {
@@ -530,7 +541,7 @@ __global__ __launch_bounds__(64) void pre_bwd_gates_kernel(
       }
     }
   }
-  {
+  if (wave == 0) {
     int j, k, tu;
     sinkhorn_lane_entry<L>(lane, tu, j, k);
     const bool valid = j < S && k < S && tu < NU && t0 + tu < T;
@@ -569,7 +580,7 @@ __global__ __launch_bounds__(64) void pre_bwd_gates_kernel(
     if (valid) dzs[tu][r] = d * c;
   }
   __syncthreads();
-  for (int k = 0; k < NU; ++k) {
+  for (int k = wave; k < NU; k += 4) {
     const size_t t = t0 + k;
     const bool live = t < (size_t)T;
     const float rinv = rms_inverse(raw[k][R], n, eps);
@@ -984,8 +995,7 @@ void run(const PreBwd& a, int T, int H, int iters, float eps, float* work, hipSt
             : dots<S, F8, 1, false>(a, p, T, H, KB, work, st);
   }
   hipLaunchKernelGGL((pre_bwd_gates_kernel<S>), dim3((unsigned)(padded(T) / NU)),
-                     dim3(64),
-                     (size_t)iters * 2 * 64 * sizeof(float), st, part, p.G, T, n, a.scale,
+                     dim3(256), (size_t)iters * 2 * 64 * sizeof(float), st, part, p.G, T, n, a.scale,
                      a.base, iters, eps, a.dpre, a.dpost, a.dcomb,
                      reinterpret_cast<unsigned short*>(work + p.ua),
                      reinterpret_cast<unsigned short*>(work + p.ut), side, red);
