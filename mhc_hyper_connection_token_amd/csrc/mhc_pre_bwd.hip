@@ -10,12 +10,13 @@
 //   dx_c    = dx_in_c + pre_c dy + sum_r u_r W_r,c + alpha x_c
 //   dW      = sum_t u_t x_t^T,  dbase = sum_t dz,  dscale_g = sum_t sum_g dz m
 // Five launches: W cut into bf16 planes; the dots (raw, ss, dy.x) split over the
-// hidden axis; the gates forward and backward, one wave per four tokens (one where
+// hidden axis; the gates forward and backward, a block per four tokens (one where
 // S > 4); the stream that writes dx and adds up dW, a wave owning 64 columns over
-// a range of tokens; and the sums over the ranges and tokens.  x and dy are read
-// twice (neither fits on chip while a token's dots are open); everything else once.
-// At 4096 tokens of 4 x 4096 from a checkpoint: 5 + 42 + 10 + 144 + 5 us, in fp32
-// 5 + 70 + 10 + 165 + 5; at 1024 tokens of 8 x 7168: 11 + 62 + 14 + 175 + 5.
+// a range of tokens; and the sums over the ranges and tokens (of a single range:
+// in the stream's launch).  x and dy are read twice (neither fits on chip while a
+// token's dots are open); everything else once.
+// At 4096 tokens of 4 x 4096 from a checkpoint: 5 + 42 + 9 + 144 + 5 us, in fp32
+// 5 + 70 + 9 + 165 + 5; at 1024 tokens of 8 x 7168: 11 + 62 + 11 + 175 + 5.
 #include "mhc_f8.h"
 #include "mhc_kernels.h"
 
@@ -644,13 +645,23 @@ __global__ __launch_bounds__(256, 1) void pre_bwd_stream_kernel(
     const void* __restrict__ x, const unsigned char* __restrict__ xs,
     const float* __restrict__ w, const float* __restrict__ dy, const bf16x8* __restrict__ ua,
     const bf16x8* __restrict__ ut, const float* __restrict__ side, const float* dx_in, int T,
-    int H, int KB, int SB, int chunk, float* dx, float* __restrict__ dw_part) {
+    int H, int KB, int SB, int chunk, float* dx, float* __restrict__ dw_part,
+    const float* __restrict__ red, float* __restrict__ dscale, float* __restrict__ dbase) {
   constexpr int R = rows_of(S), KS = steps_of(S), NRT = tiles_of(S), Q = kColumns;
   __shared__ bf16x8 wl[4][KS * 3 * Q][64];
   __shared__ float4 gate[S + 1][kMaxChunk / 4];  // side, for the block's tokens
   const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ci = blockIdx.x / SB, n = S * H;
+  if (blockIdx.x >= SB && chunk >= T) {  // past a single range: red [R + 3][T] over the tokens
+    const int row = (blockIdx.x - SB) * 4 + wave;
+    if (row >= R + 3) return;
+    float s = 0.f;
+    for (int t = lane; t < T; t += 64) s += red[(size_t)row * T + t];
+    s = sum_wave(s);
+    if (lane == 0) *(row < R ? dbase + row : dscale + row - R) = s;
+    return;
+  }
   const int t_begin = ci * chunk, t_end = min(t_begin + chunk, T);
   const size_t TP = padded(T);
   const int group = ((blockIdx.x - ci * SB) * 4 + wave) * 32 + r;
@@ -926,6 +937,9 @@ Plan plan(int T, int S, int H, bool f8) {
   p.SB = div_up(S * H, 128 * kColumns);
   const int groups32 = padded(T) / 32;
   int c = 256 / p.SB;
+  // up to two steps in one range: with the sums beside it a launch less, and no slower
+  // (37 tokens of 3 x 1028: 11.0 us for both; 100: 11.3 in two, 17.0 in one)
+  if (T <= 64) c = 1;
   c = c < div_up(T, kMaxChunk) ? div_up(T, kMaxChunk) : c > groups32 ? groups32 : c;
   p.chunk = div_up(groups32, c) * 32;
   p.chunks = div_up(T, p.chunk);
@@ -995,16 +1009,19 @@ void run(const PreBwd& a, int T, int H, int iters, float eps, float* work, hipSt
             : dots<S, F8, 1, false>(a, p, T, H, KB, work, st);
   }
   hipLaunchKernelGGL((pre_bwd_gates_kernel<S>), dim3((unsigned)(padded(T) / NU)),
-                     dim3(256), (size_t)iters * 2 * 64 * sizeof(float), st, part, p.G, T, n, a.scale,
-                     a.base, iters, eps, a.dpre, a.dpost, a.dcomb,
+                     dim3(256), (size_t)iters * 2 * 64 * sizeof(float), st, part, p.G, T, n,
+                     a.scale, a.base, iters, eps, a.dpre, a.dpost, a.dcomb,
                      reinterpret_cast<unsigned short*>(work + p.ua),
                      reinterpret_cast<unsigned short*>(work + p.ut), side, red);
+  const bool one = p.chunks == 1;
+  // beside a single range the sums over the tokens, a row a wave
   hipLaunchKernelGGL((pre_bwd_stream_kernel<S, F8>),
-                     dim3((unsigned)(p.SB * p.chunks)), dim3(256), 0, st, a.x, a.x_scales, a.fn_w,
-                     a.dy, reinterpret_cast<const bf16x8*>(work + p.ua),
+                     dim3((unsigned)(p.SB * p.chunks + (one ? (R + 6) / 4 : 0))), dim3(256), 0, st,
+                     a.x, a.x_scales, a.fn_w, a.dy, reinterpret_cast<const bf16x8*>(work + p.ua),
                      reinterpret_cast<const bf16x8*>(work + p.ut), side, a.dx_in, T, H, KB, p.SB,
-                     p.chunk, a.dx, dw);
-  const long quads = p.chunks > 1 ? (long)R * n / 4 : 0;
+                     p.chunk, a.dx, dw, red, a.dscale, a.dbase);
+  if (one) return;
+  const long quads = (long)R * n / 4;
   hipLaunchKernelGGL(pre_bwd_sums_kernel, dim3((unsigned)(R + 3 + (quads + 255) / 256)),
                      dim3(256), 0, st, red, T, R, dw, p.chunks, quads, a.dfn_w, a.dscale,
                      a.dbase);
