@@ -4,7 +4,7 @@
 // A block's scale is 2^e with e the least integer for which amax <= 448 * 2^e.
 // A power of two moves exponents only: the relative rounding of a code does not
 // depend on it, a decoded value has four significant bits and is exact in bf16
-// and fp32, and the scaled matrix instruction takes the byte e + 127 as it is.
+// and fp32, and the conversion of a code to bf16 applies it on the way.
 #pragma once
 #include <hip/hip_bf16.h>
 

@@ -16,7 +16,7 @@
 // in the stream's launch).  x and dy are read twice (neither fits on chip while a
 // token's dots are open); everything else once.
 // At 4096 tokens of 4 x 4096 from a checkpoint: 5 + 42 + 9 + 144 + 5 us, in fp32
-// 5 + 70 + 9 + 165 + 5; at 1024 tokens of 8 x 7168: 11 + 62 + 11 + 175 + 5.
+// 5 + 70 + 9 + 165 + 5; at 1024 tokens of 8 x 7168: 11 + 60 + 11 + 175.
 #include "mhc_f8.h"
 #include "mhc_kernels.h"
 
