@@ -15,6 +15,7 @@ raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 __all__ = ["site_pre", "site_post", "site_pre_zq8", "site_pre_check", "site_post_check",
@@ -556,19 +557,19 @@ def f8_encode(x, *, transposed=False, square: bool = False, out=None, stream=Non
     import torch
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
-    if x.dtype not in (torch.float32, torch.bfloat16):
+    dtype = x.dtype
+    bf16 = dtype == torch.bfloat16
+    if not bf16 and dtype != torch.float32:
         raise ValueError("x must be float32 or bfloat16")
-    if x.dim() < 2 or (square and x.dim() != 2):
+    *lead, cols = x.shape
+    if not lead or (square and len(lead) != 1):
         raise ValueError("x must be [rows, cols]" if square else "x must be [..., rows, cols]")
     if transposed not in (False, True, "only"):
         raise ValueError('transposed must be False, True or "only"')
-    px = _gpu(x, "x", x.dtype)
+    px = _gpu(x, "x", dtype)
     if stream is not None:
         return _on(stream, x.device, f8_encode, x, transposed=transposed, square=square, out=out)
-    lead, cols = tuple(x.shape[:-1]), x.shape[-1]
-    rows = 1
-    for d in lead:
-        rows *= d
+    rows = math.prod(lead)
     kb = _blocks(cols)
     f8, u8 = torch.float8_e4m3fn, torch.uint8
     if not transposed:
@@ -585,7 +586,7 @@ def f8_encode(x, *, transposed=False, square: bool = False, out=None, stream=Non
     elif transposed == "only":
         ptrs = [None, None] + ptrs
     _call("mhc_f8_encode", x.get_device(),
-          (px, int(x.dtype == torch.bfloat16), rows, cols, int(square), *ptrs), out)
+          (px, int(bf16), rows, cols, int(square), *ptrs), out)
     return out
 
 
