@@ -11,11 +11,11 @@
 //   dW      = sum_t u_t x_t^T,  dbase = sum_t dz,  dscale_g = sum_t sum_g dz m
 // Five launches: W cut into bf16 planes; the dots (raw, ss, dy.x) split over the
 // hidden axis; the gates forward and backward, a block per four tokens (one where
-// S > 4); the stream that writes dx and adds up dW, a wave owning 64 columns over
-// a range of tokens; and the sums over the ranges and tokens (of a single range:
-// in the stream's launch).  x and dy are read twice (neither fits on chip while a
-// token's dots are open); everything else once.
-// At 4096 tokens of 4 x 4096 from a checkpoint: 5 + 42 + 9 + 144 + 5 us, in fp32
+// S > 4); the stream that writes dx and adds up dW, a wave owning 64 or 128
+// columns over a range of tokens; and the sums over the ranges and tokens (of a
+// single range: in the stream's launch).  x and dy are read twice (neither fits on
+// chip while a token's dots are open); everything else once.
+// At 4096 tokens of 4 x 4096 from a checkpoint: 5 + 42 + 9 + 134 + 5 us, in fp32
 // 5 + 70 + 9 + 165 + 5; at 1024 tokens of 8 x 7168: 11 + 60 + 11 + 175.
 #include "mhc_f8.h"
 #include "mhc_kernels.h"
@@ -24,7 +24,6 @@ namespace mhc {
 
 namespace {
 
-constexpr int kColumns = 2;           // neighbouring columns a lane of the stream owns
 // an offset past every buffer of fewer than 2^31 - 16 bytes (a buffer of 2^31 has no
 // columns to leave out), no lane's or row's part of 2^31 takes it round to zero
 constexpr unsigned kOutside = 0x7ffffff0;
@@ -36,11 +35,29 @@ constexpr int rows_of(int S) { return (2 + S) * S; }
 constexpr int steps_of(int S) { return (rows_of(S) + 15) / 16; }  // of 16 rows
 constexpr int tiles_of(int S) { return (rows_of(S) + 31) / 32; }  // of 32 rows
 
-// Two neighbouring floats of a buffer.
-template <int POLICY>
-__device__ __forceinline__ floatx2 load_two(__amdgpu_buffer_rsrc_t buf, unsigned offset) {
-  return __builtin_bit_cast(floatx2,
-                            __builtin_amdgcn_raw_buffer_load_b64(buf, offset, 0, POLICY));
+typedef unsigned uintx4 __attribute__((ext_vector_type(4)));
+
+// Q neighbouring floats of a buffer.
+template <int Q>
+using Columns = float __attribute__((ext_vector_type(Q)));
+template <int Q, int POLICY>
+__device__ __forceinline__ Columns<Q> load_columns(__amdgpu_buffer_rsrc_t buf, unsigned offset) {
+  if constexpr (Q == 4)
+    return __builtin_bit_cast(Columns<4>,
+                              __builtin_amdgcn_raw_buffer_load_b128(buf, offset, 0, POLICY));
+  else
+    return __builtin_bit_cast(Columns<2>,
+                              __builtin_amdgcn_raw_buffer_load_b64(buf, offset, 0, POLICY));
+}
+template <int Q>
+__device__ __forceinline__ void store_columns(__amdgpu_buffer_rsrc_t buf, unsigned offset,
+                                              Columns<Q> v) {
+  if constexpr (Q == 4)
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uintx4, v), buf, offset, 0,
+                                           kNonTemporal);
+  else
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uintx2, v), buf, offset, 0,
+                                          kNonTemporal);
 }
 __device__ __forceinline__ float fma4(float4 a, float4 b, float acc) {
   acc = fmaf(a.x, b.x, acc);
@@ -640,14 +657,15 @@ __global__ __launch_bounds__(256) void pre_bwd_gates_kernel(
 //      k = (h, e) for token 8 (2 step + e / 4) + 4h + e % 4
 // The next step's loads start as soon as this one's have gone into the sums, and
 // run under the products.
-template <int S, bool F8>
+template <int S, bool F8, int Q>
 __global__ __launch_bounds__(256, 1) void pre_bwd_stream_kernel(
     const void* __restrict__ x, const unsigned char* __restrict__ xs,
     const float* __restrict__ w, const float* __restrict__ dy, const bf16x8* __restrict__ ua,
     const bf16x8* __restrict__ ut, const float* __restrict__ side, const float* dx_in, int T,
     int H, int KB, int SB, int chunk, float* dx, float* __restrict__ dw_part,
     const float* __restrict__ red, float* __restrict__ dscale, float* __restrict__ dbase) {
-  constexpr int R = rows_of(S), KS = steps_of(S), NRT = tiles_of(S), Q = kColumns;
+  constexpr int R = rows_of(S), KS = steps_of(S), NRT = tiles_of(S);
+  using Row = Columns<Q>;
   __shared__ bf16x8 wl[4][KS * 3 * Q][64];
   __shared__ float4 gate[S + 1][kMaxChunk / 4];  // side, for the block's tokens
   const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
@@ -671,11 +689,11 @@ __global__ __launch_bounds__(256, 1) void pre_bwd_stream_kernel(
     const float* wc = w + col;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      floatx2 v[8];
+      Row v[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int row = 16 * ks + 8 * h + e;
-        v[e] = row < R ? *reinterpret_cast<const floatx2*>(wc + (size_t)row * n) : floatx2(0.f);
+        v[e] = row < R ? *reinterpret_cast<const Row*>(wc + (size_t)row * n) : Row(0.f);
       }
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
@@ -697,7 +715,7 @@ __global__ __launch_bounds__(256, 1) void pre_bwd_stream_kernel(
 
   // what a step reads, token 8a + 4h + b at index 4a + b
   unsigned code[16], byte[16];
-  floatx2 xf[16], d[16], o[16];
+  Row xf[16], d[16], o[16];
   // A step's rows are buffers of their own (at most 2^31 bytes: n <= 2^24), a lane's
   // place in them an offset; tokens past the end and columns past n are out of
   // range, where loads give zero and stores are dropped.
@@ -721,13 +739,16 @@ __global__ __launch_bounds__(256, 1) void pre_bwd_stream_kernel(
       // opaque: the sixteen offsets would be kept in registers across the steps
       asm volatile("" : "+v"(lx), "+v"(ls), "+v"(lh), "+v"(ln));
       if constexpr (F8) {
-        code[i] = __builtin_amdgcn_raw_buffer_load_b16(bx, lx + k * row_x, 0, 0);
+        if constexpr (Q == 4)
+          code[i] = __builtin_amdgcn_raw_buffer_load_b32(bx, lx + k * row_x, 0, 0);
+        else
+          code[i] = __builtin_amdgcn_raw_buffer_load_b16(bx, lx + k * row_x, 0, 0);
         byte[i] = __builtin_amdgcn_raw_buffer_load_b8(bs, ls + k * row_s, 0, 0);
       } else {
-        xf[i] = load_two<0>(bx, lx + k * row_x);
+        xf[i] = load_columns<Q, 0>(bx, lx + k * row_x);
       }
-      d[i] = load_two<0>(bd, lh + k * 4 * H);
-      o[i] = load_two<kNonTemporal>(bo, ln + k * 4 * n);
+      d[i] = load_columns<Q, 0>(bd, lh + k * 4 * H);
+      o[i] = load_columns<Q, kNonTemporal>(bo, ln + k * 4 * n);
     }
   };
   load(t_begin);
@@ -762,11 +783,15 @@ __global__ __launch_bounds__(256, 1) void pre_bwd_stream_kernel(
         a[k] = af[(i + k) & 3];
         if constexpr (F8) {
           const float sc = f8_scale(byte[i + k]);
-          const unsigned b = __builtin_bit_cast(
-              unsigned,
-              __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)code[i + k], sc, false));
-          v[k][0] = __uint_as_float(b << 16);
-          v[k][1] = __uint_as_float(b & 0xffff0000u);
+#pragma unroll
+          for (int q = 0; q < Q; q += 2) {
+            const bf16x2 two =
+                q == 0 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)code[i + k], sc, false)
+                       : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)code[i + k], sc, true);
+            const unsigned b = __builtin_bit_cast(unsigned, two);
+            v[k][q] = __uint_as_float(b << 16);
+            v[k][q + 1] = __uint_as_float(b & 0xffff0000u);
+          }
         } else {
 #pragma unroll
           for (int q = 0; q < Q; ++q) v[k][q] = xf[i + k][q];
@@ -837,11 +862,10 @@ __global__ __launch_bounds__(256, 1) void pre_bwd_stream_kernel(
     for (int i = 0; i < 16; ++i) {
       const int k = 8 * (i >> 2) + (i & 3);
       asm volatile("" : "+v"(ln));
-      floatx2 v;
+      Row v;
 #pragma unroll
       for (int q = 0; q < Q; ++q) v[q] = acc[q][i];
-      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uintx2, v), bo, ln + k * 4 * n, 0,
-                                            kNonTemporal);
+      store_columns<Q>(bo, ln + k * 4 * n, v);
     }
   }
   if (!in) return;
@@ -851,10 +875,10 @@ __global__ __launch_bounds__(256, 1) void pre_bwd_stream_kernel(
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int row = 32 * k + 8 * (i >> 2) + 4 * h + (i & 3);
-      floatx2 v;
+      Row v;
 #pragma unroll
       for (int q = 0; q < Q; ++q) v[q] = dw[k][q][i];
-      if (row < R) *reinterpret_cast<floatx2*>(part + (size_t)row * n) = v;
+      if (row < R) *reinterpret_cast<Row*>(part + (size_t)row * n) = v;
     }
 }
 
@@ -916,7 +940,7 @@ namespace {
 // staged: for the block), `chunks` token ranges of `chunk` for the stream; about
 // 2048 and 1024 waves (8 and 4 per compute unit) where the shape has that many.
 struct Plan {
-  int TT, G, HS, steps, SB, chunk, chunks;
+  int TT, G, HS, steps, Q, SB, chunk, chunks;
   bool split, staged;
   size_t planes, part, ua, ut, side, red, dw, floats;  // offsets and total, in floats
 };
@@ -934,13 +958,25 @@ Plan plan(int T, int S, int H, bool f8) {
   p.G = div_up(p.HS, waves * p.steps);
   p.split = !p.staged && S > 1 && groups * p.G * S <= 512;
   if (p.split) p.G *= S;
-  p.SB = div_up(S * H, 128 * kColumns);
-  const int groups32 = padded(T) / 32;
-  int c = 256 / p.SB;
-  // up to two steps in one range: with the sums beside it a launch less, and no slower
-  // (37 tokens of 3 x 1028: 11.0 us for both; 100: 11.3 in two, 17.0 in one)
-  if (T <= 64) c = 1;
-  c = c < div_up(T, kMaxChunk) ? div_up(T, kMaxChunk) : c > groups32 ? groups32 : c;
+  // The stream's split: of the counts of ranges that fill one to four rounds of the
+  // compute units (a block each), the one with the fewest steps in a row, two more a
+  // round for its beginning and end (3000 tokens of 4 x 7168: 336 blocks in three
+  // ranges 240 us, 448 in four 205).  Four columns a lane instead of two, where a step
+  // takes 1.85 times as long, from checkpoints of up to four streams (4096 tokens of
+  // 4 x 4096: 146 and 135 us; fp32 170 and 165, but 2048 tokens 86 and 96).  Up to two
+  // steps go in one range: with the sums beside it a launch less, and no slower (37
+  // tokens of 3 x 1028: 11.0 us for both; 100: 11.3 in two, 17.0 in one).
+  const int groups32 = padded(T) / 32, least = div_up(T, kMaxChunk);
+  int c = 1;
+  float best = 0.f;
+  for (int Q = 2; Q <= (f8 && S <= 4 && T > 64 ? 4 : 2); Q += 2)
+    for (int r = 1; r <= 4; ++r) {
+      const int SB = div_up(S * H, 128 * Q), fill = 256 * r / SB;
+      const int k = T <= 64 ? 1 : fill < least ? least : fill < groups32 ? fill : groups32;
+      const float cost = (float)(((long)SB * k + 255) / 256) * (float)(div_up(groups32, k) + 2) *
+                         (Q == 4 ? 1.85f : 1.f);
+      if (best == 0.f || cost < best) best = cost, c = k, p.Q = Q, p.SB = SB;
+    }
   p.chunk = div_up(groups32, c) * 32;
   p.chunks = div_up(T, p.chunk);
   size_t at = 0;
@@ -1015,11 +1051,21 @@ void run(const PreBwd& a, int T, int H, int iters, float eps, float* work, hipSt
                      reinterpret_cast<unsigned short*>(work + p.ut), side, red);
   const bool one = p.chunks == 1;
   // beside a single range the sums over the tokens, a row a wave
-  hipLaunchKernelGGL((pre_bwd_stream_kernel<S, F8>),
-                     dim3((unsigned)(p.SB * p.chunks + (one ? (R + 6) / 4 : 0))), dim3(256), 0, st,
-                     a.x, a.x_scales, a.fn_w, a.dy, reinterpret_cast<const bf16x8*>(work + p.ua),
-                     reinterpret_cast<const bf16x8*>(work + p.ut), side, a.dx_in, T, H, KB, p.SB,
-                     p.chunk, a.dx, dw, red, a.dscale, a.dbase);
+  auto stream = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(p.SB * p.chunks + (one ? (R + 6) / 4 : 0))),
+                       dim3(256), 0, st, a.x, a.x_scales, a.fn_w, a.dy,
+                       reinterpret_cast<const bf16x8*>(work + p.ua),
+                       reinterpret_cast<const bf16x8*>(work + p.ut), side, a.dx_in, T, H, KB, p.SB,
+                       p.chunk, a.dx, dw, red, a.dscale, a.dbase);
+  };
+  if constexpr (F8 && S <= 4) {
+    if (p.Q == 4)
+      stream(pre_bwd_stream_kernel<S, F8, 4>);
+    else
+      stream(pre_bwd_stream_kernel<S, F8, 2>);
+  } else {
+    stream(pre_bwd_stream_kernel<S, F8, 2>);
+  }
   if (one) return;
   const long quads = (long)R * n / 4;
   hipLaunchKernelGGL(pre_bwd_sums_kernel, dim3((unsigned)(R + 3 + (quads + 255) / 256)),

@@ -113,7 +113,9 @@ BWD_REL = 2.5e-5
 
 @pytest.mark.parametrize("T,S,H", [(513, 1, 132), (520, 2, 516), (777, 3, 260), (1100, 4, 1028),
                                    (530, 5, 388), (540, 6, 132), (550, 7, 260), (600, 8, 1028),
-                                   (2049, 4, 260), (1601, 4, 4096), (1031, 8, 2052), (512, 4, 4)])
+                                   (2049, 4, 260), (1601, 4, 4096), (1031, 8, 2052), (512, 4, 4),
+                                   (4097, 4, 4096), (4100, 3, 4100), (2100, 2, 16388),
+                                   (1200, 1, 32772), (3001, 4, 7168)])
 @pytest.mark.parametrize("f8", [True, False])
 def test_pre_bwd(mhc, T, S, H, f8):
     print(f"[case] pre_bwd T={T} S={S} H={H} f8={f8}", flush=True)
