@@ -408,6 +408,7 @@ void matmul(const Args<O>& p) {
   // at a time (16 x 7168 x 2048 8.6 us against 11.3, 1 x 16384 x 2048 10.4 and 12.6, 1 x
   // 8192 x 2048 8.8 and 8.0, 16 x 8192 x 4096 14.3 and 11.9; 32 x 8192 x 4096 14.6 and
   // 17.9, 32 x 4096 x 4096 13.8 and 9.9).
+  auto rounds = [&](int b) { return (tiles_of(p.M, p.N, b, b) + 255) / 256; };
   const long tiles64 = tiles_of(p.M, p.N, 64, 64);
   const int side = p.M < p.N ? p.M : p.N;
   const bool shallow = p.KB <= 16 && (p.N >= 16384 || (p.M > 8 && p.N >= 5120));
@@ -420,13 +421,14 @@ void matmul(const Args<O>& p) {
   // and no groups, 128 x 4096 x 1024 7.1 and 7.6, 70 x 4096 x 256 5.2 and 4.7).
   } else if (p.M <= 32 || (tiles64 <= 256 && p.KB >= 8)) {
     tile<2, 1, 1, 2, 2, 4>(p);
-  // The largest tiles that give most compute units one and are not half empty: 256 x 256
-  // (7168 x 4096 x 1024: 69 us, 128 x 128 68, but at 4096 x 16384 x 4096 540 against
-  // 580; 192 x 65536 x 1024 36 and 40, 128 x 65536 x 1024 33 and 25), 128 x 128
-  // (1024 x 4096 x 4096: 41 us, 64 x 64 62; 65536 x 128 x 4096 84 and 106, 32768 x 64 x
-  // 4096 43 and 33), 64 x 64 three to a unit.
-  } else if (side > 128 && tiles_of(p.M, p.N, 256, 256) >= 192) {
+  // By the rounds of 256 tiles: one of 256 x 256 takes 3.1 times as long as one of 128 x
+  // 128 (4096 rows, K = 4096, us in large and in small tiles: N = 4096 110 and 130, 4608
+  // 184 and 156, 6144 192 and 195, 7168 198 and 224, 8192 251 and 267; 4096 x 9216 x 2048
+  // 163 and 152; 128 x 65536 x 1024 33 and 25).
+  } else if (31 * rounds(256) <= 10 * rounds(128)) {
     tile<4, 2, 2, 4, 2, 1>(p);
+  // 128 x 128 against 64 x 64, three of those to a unit: 1024 x 4096 x 4096 41 and 49 us,
+  // 512 x 4096 x 4096 37 and 27; 65536 x 128 x 4096 84 and 106, 32768 x 64 x 4096 43 and 33.
   } else if (side > 64 && tiles_of(p.M, p.N, 128, 128) >= 192) {
     tile<2, 1, 2, 4, 2, 1>(p);
   } else {

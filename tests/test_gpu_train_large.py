@@ -41,7 +41,8 @@ MKN = [(1, 8324, 260), (5, 132, 8196), (16, 4096, 8196), (16, 4100, 8196), (17, 
        (3584, 1412, 3588), (4093, 4, 4100), (24700, 132, 68), (100, 388, 24900),
        (70001, 260, 4), (12500, 260, 64), (66, 516, 65540), (16, 4096, 16388),
        (9, 8324, 16388), (16, 2048, 5124), (3, 260, 16388), (32, 516, 20004),
-       (100, 1156, 1028), (200, 8452, 1988), (65, 1024, 16380)]
+       (100, 1156, 1028), (200, 8452, 1988), (65, 1024, 16380), (3900, 516, 3988),
+       (4100, 260, 4500), (250, 388, 49000)]
 
 
 @pytest.mark.parametrize("M,K,N", MKN)
