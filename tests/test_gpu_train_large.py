@@ -210,3 +210,83 @@ def test_outputs_belong_to_the_stream_given(mhc):
     if torch.cuda.device_count() > 1:
         with pytest.raises(ValueError):
             calls[0](stream=torch.cuda.Stream(device=1))
+
+
+# ------------------------------------------------------------------ past 32 bits
+def _same(a, b):
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+def test_encode_past_32_bits(mhc):
+    """2.2e9 entries, 4.4 GB: the last rows and columns are what they are alone."""
+    rows, cols, tail = 128 * 4219, 4096, 1280
+    print(f"[case] encode {rows}x{cols}", flush=True)
+    x = torch.empty(rows, cols, device="cuda", dtype=torch.bfloat16)
+    x.copy_(_randn(1, 1, cols))
+    x[-tail:] = _randn(2, tail, cols).bfloat16()
+    got = mhc.f8_encode(x, transposed=True)
+    want = mhc.f8_encode(x[-tail:], transposed=True)
+    assert _same(got[0][-tail:], want[0]) and _same(got[1][-tail:], want[1])
+    assert _same(got[2][:, -tail:], want[2]) and _same(got[3][:, -tail // 128:], want[3])
+    alone = mhc.f8_encode(x)
+    assert _same(alone[0], got[0]) and _same(alone[1], got[1])
+    again = mhc.f8_repack(got[0], got[1], cols)
+    part = mhc.f8_repack(got[0][-tail:], got[1][-tail:], cols)
+    assert _same(again[0][:, -tail:], part[0]) and _same(again[1][:, -tail // 128:], part[1])
+    back = mhc.f8_decode(got[0], got[1], cols)
+    assert _same(back[-tail:], mhc.f8_decode(got[0][-tail:], got[1][-tail:], cols))
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_matmul_past_32_bits(mhc, M):
+    """4.5e9 codes, as the weight and as the activations of a product."""
+    N, K, tail = 1100004, 4096, 100
+    print(f"[case] matmul {M}x{N}x{K}", flush=True)
+    b = torch.empty(N, K, device="cuda", dtype=torch.bfloat16)
+    b.copy_(_randn(1, 1, K))
+    b[-tail:] = _randn(2, tail, K).bfloat16()
+    eb, ea = mhc.f8_encode(b), mhc.f8_encode(_randn(3, M, K))
+    va, vb = _decode(*ea, K), _decode(eb[0][-tail:], eb[1][-tail:], K)
+    bound = K * 2.0 ** -23 * (va.abs() @ vb.abs().t())  # as above
+    got = mhc.f8_matmul(*ea, *eb)[:, -tail:].double()
+    assert ((got - va @ vb.t()).abs() <= bound).all()
+    got = mhc.f8_matmul(*eb, *mhc.f8_encode(b[-64:], square=True))
+    va, vb = vb, _decode(*mhc.f8_encode(b[-64:], square=True), K, True)
+    bound = K * 2.0 ** -23 * (va.abs() @ vb.abs().t())
+    assert ((got[-tail:].double() - va @ vb.t()).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("f8", [True, False])
+def test_site_bwd_past_32_bits(mhc, f8):
+    """8.5 GB of state: the last tokens' gradients are what they are alone."""
+    T, S, H, tail = 65500, 8, 4096, 100
+    print(f"[case] site backward T={T} S={S} H={H} f8={f8}", flush=True)
+    assert 2 ** 31 > T * S * H > 2 ** 31 * 0.99
+    d = _site(T, S, H, 5)
+    post, comb = 2 * torch.sigmoid(d["dpost"]), torch.softmax(d["dcomb"], 2)
+    kx, _ = _keep(mhc, d["x"], f8)
+    kf, _ = _keep(mhc, d["f"], f8)
+    cut = lambda k: tuple(t[-tail:] for t in k) if f8 else k[-tail:]  # noqa: E731
+    got = mhc.site_post_bwd(d["g"], kx, kf, post, comb)
+    want = mhc.site_post_bwd(d["g"][-tail:], cut(kx), cut(kf), post[-tail:], comb[-tail:])
+    for p, q in zip(got, want):
+        assert _same(p[-tail:], q)
+    dx = got[0]
+    del got, want
+    weights = (d["w"], d["scale"], d["base"], 20, EPS)
+    want = mhc.site_pre_bwd(cut(kx), *weights, d["dy"][-tail:], d["dpost"][-tail:],
+                            d["dcomb"][-tail:], dx_in=dx[-tail:])
+    half = T // 2 + 7  # the sums over tokens, in two calls
+    cuts = (slice(0, half), slice(half, T))
+    parts = [mhc.site_pre_bwd(tuple(t[c] for t in kx) if f8 else kx[c], *weights, d["dy"][c],
+                              d["dpost"][c], d["dcomb"][c])[1:] for c in cuts]
+    got = mhc.site_pre_bwd(kx, *weights, d["dy"], d["dpost"], d["dcomb"], dx_in=dx, out=(
+        dx, *(torch.empty_like(t) for t in parts[0])))
+    # the dots' and the token sums' order differs with T: each side is within BWD_REL
+    size = want[0].abs().max()
+    assert (got[0][-tail:] - want[0]).abs().max() <= 2 * BWD_REL * size
+    short = max((parts[0][k] + parts[1][k]).abs().max() for k in (1, 2))
+    for k in range(3):
+        both = parts[0][k].double() + parts[1][k].double()
+        size = both.abs().max() if k == 0 else short
+        assert (got[1 + k].double() - both).abs().max() <= 3 * BWD_REL * size, k
