@@ -9,14 +9,17 @@
 //   u_r     = r scale dz_r,   alpha = -(sum_r scale dz_r m_r) r^2 / n
 //   dx_c    = dx_in_c + pre_c dy + sum_r u_r W_r,c + alpha x_c
 //   dW      = sum_t u_t x_t^T,  dbase = sum_t dz,  dscale_g = sum_t sum_g dz m
-// Five launches: W cut into bf16 planes; the dots (raw, ss, dy.x) split over the
-// hidden axis; the gates forward and backward, a block per four tokens (one where
-// S > 4); the stream that writes dx and adds up dW, a wave owning 64 or 128
-// columns over a range of tokens; and the sums over the ranges and tokens (of a
-// single range: in the stream's launch).  x and dy are read twice (neither fits on
-// chip while a token's dots are open); everything else once.
+// Three to five launches: W cut into bf16 planes (a group of few tokens does it on
+// the way); the dots (raw, ss, dy.x) split over the hidden axis; the gates forward
+// and backward, a block per four tokens (one where S > 4); the stream that writes
+// dx and adds up dW, a wave owning 64 or 128 columns over a range of tokens; and the
+// sums over the ranges and tokens (of a single range: in the stream's launch).  x
+// and dy are read twice (neither fits on chip while a token's dots are open);
+// everything else once.
 // At 4096 tokens of 4 x 4096 from a checkpoint: 5 + 42 + 9 + 134 + 5 us, in fp32
 // 5 + 70 + 9 + 165 + 5; at 1024 tokens of 8 x 7168: 11 + 60 + 11 + 175.
+#include <type_traits>
+
 #include "mhc_f8.h"
 #include "mhc_kernels.h"
 
@@ -98,19 +101,12 @@ __device__ __forceinline__ void planes8(float4 a, float4 b, bf16x8 out[3]) {
   }
 }
 
-// The dots' order of a slice of 64 hidden columns in two steps of 32: the column of
-// entry 4q (q = 0, 1) of lane group g = lane / 16.  Codes, and fp32 staged in LDS: a
-// lane's own 16 entries at 16g, eight to a step.  fp32 direct: four floats at 4g of
-// every 16, so that the four groups read 64 neighbouring bytes.
-__device__ __forceinline__ int dots_column(bool own, int step, int g, int q) {
-  return own ? 16 * g + 8 * step + 4 * q : 32 * step + 16 * q + 4 * g;
-}
-
-// W [R][S*H] as row operands of the dots: for stream c, slice, step, plane and
-// row tile of 16, 64 lanes of eight bf16 (row = lane % 16), zeros past R and H.
+// W [R][S*H] as row operands of the dots of many tokens: for stream c, slice of 64
+// columns, step of 32, plane and row tile of 16, 64 lanes of eight bf16 (row = lane % 16,
+// columns 16g + 8 step on, g = lane / 16), zeros past R and H.
 __global__ __launch_bounds__(256) void pre_bwd_planes_kernel(const float* __restrict__ w, int R,
                                                              int NRT, int S, int H, int HS,
-                                                             bool own, long total,
+                                                             long total,
                                                              bf16x8* __restrict__ out) {
   const long i = (long)blockIdx.x * 256 + threadIdx.x;
   if (i >= total) return;
@@ -123,7 +119,7 @@ __global__ __launch_bounds__(256) void pre_bwd_planes_kernel(const float* __rest
   float4 v[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int col = 64 * slice + dots_column(own, step, lane >> 4, q);
+    const int col = 64 * slice + 16 * (lane >> 4) + 8 * step + 4 * q;
     v[q] = row < R && col < H
                ? *reinterpret_cast<const float4*>(w + ((size_t)row * S + c) * H + col)
                : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -158,6 +154,9 @@ __device__ __forceinline__ void turn_groups(float& v0, float& v1, float& v2, flo
 // A wave takes 16*TT tokens and `steps` slices of 64 hidden columns in all S
 // streams; the four waves of a block take neighbouring ranges and are added up
 // in LDS, the G blocks of a token group by the gates kernel.
+// A slice goes in two steps of 32 columns; entry 4q (q = 0, 1) of lane group g = lane /
+// 16 is column 16g + 8 step + 4q of codes (a lane's 16 bytes) and 32 step + 16q + 4g of
+// fp32.  W, which a few tokens need only once, is cut into planes on the way.
 // The dots run on v_mfma_f32_16x16x32_bf16 with W in three planes.  A decoded
 // code is exact in bf16, so three products give fp32 dots; an fp32 x is cut into
 // planes as well and takes six (the three left out are below 2^-24).
@@ -169,7 +168,7 @@ __device__ __forceinline__ void turn_groups(float& v0, float& v1, float& v2, flo
 template <int S, bool F8, int TT, bool SPLIT>
 __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
     const void* __restrict__ x, const unsigned char* __restrict__ xs,
-    const bf16x8* __restrict__ wp, const float* __restrict__ dy, int T, int H, int KB, int G,
+    const float* __restrict__ w, const float* __restrict__ dy, int T, int H, int KB, int G,
     int HS, int steps, float* __restrict__ part) {
   constexpr int R = rows_of(S), NRT = steps_of(S), V = R + 1 + S, VP = 16 * NRT + 1 + S;
   constexpr int UC = S <= 4 && !SPLIT ? S : 1;  // unrolled further, the streams' loads spill
@@ -212,7 +211,6 @@ __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
 #pragma unroll UC
     for (int c = c0; c < c1; ++c) {
       float dc[TT];
-      const bf16x8* wc = wp + (size_t)(c * HS + sl) * 2 * 3 * NRT * 64 + lane;
       intx4 code[TT];
       float scale[TT];
 #pragma unroll
@@ -226,11 +224,15 @@ __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
       }
 #pragma unroll
       for (int step = 0; step < 2; ++step) {
-        bf16x8 wv[3][NRT];
+        const int q0 = 16 * sl + (F8 ? 4 * g + 2 * step : 8 * step + g);
+        const int q1 = q0 + (F8 ? 1 : 4);
+        bf16x8 wv[NRT][3];
 #pragma unroll
-        for (int p = 0; p < 3; ++p)
-#pragma unroll
-          for (int i = 0; i < NRT; ++i) wv[p][i] = wc[((step * 3 + p) * NRT + i) * 64];
+        for (int i = 0; i < NRT; ++i) {  // rows past R: the last one, which nobody reads
+          const float4* p = reinterpret_cast<const float4*>(w) +
+                            ((size_t)min(16 * i + r, R - 1) * S + c) * HQ;
+          planes8(q0 < HQ ? p[q0] : zero, q1 < HQ ? p[q1] : zero, wv[i]);
+        }
 #pragma unroll
         for (int k = 0; k < TT; ++k) {
           float4 xa, xb;
@@ -247,10 +249,9 @@ __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
             xb = make_float4(__uint_as_float(o.u[2] << 16), __uint_as_float(o.u[2] & 0xffff0000u),
                              __uint_as_float(o.u[3] << 16), __uint_as_float(o.u[3] & 0xffff0000u));
           } else {
-            const int q = 16 * sl + 8 * step + g;
             const float4* p = static_cast<const float4*>(x) + (t[k] * S + c) * HQ;
-            xa = q < HQ ? p[q] : zero;
-            xb = q + 4 < HQ ? p[q + 4] : zero;
+            xa = q0 < HQ ? p[q0] : zero;
+            xb = q1 < HQ ? p[q1] : zero;
             planes8(xa, xb, xp);
           }
           ss[k] = fma4(xb, xb, fma4(xa, xa, ss[k]));
@@ -261,7 +262,7 @@ __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
             for (int p = 0; p < 3; ++p)
 #pragma unroll
               for (int m = 0; m < (F8 ? 1 : 3 - p); ++m)
-                acc[k][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[p][i], xp[m], acc[k][i],
+                acc[k][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[i][p], xp[m], acc[k][i],
                                                                     0, 0, 0);
           }
         }
@@ -297,7 +298,7 @@ __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
   }
 }
 
-// The dots of more than 16 tokens (of 16 S and more with S > 4), staged: a block
+// The dots of more than 16 tokens (more than 64 with S > 4), staged: a block
 // takes 16 tokens a wave and walks units of one stream of one slice.  x (codes and
 // scales, or fp32) and planes come into LDS by direct loads, two units ahead in
 // three stages in turn (fp32: one ahead, two stages), dy a slice ahead: the planes
@@ -307,22 +308,26 @@ __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
 // chunks of 16 bytes are turned in their row (codes: chunk c at place
 // c ^ token / 4 % 4 of four; fp32: c ^ token % 16 of sixteen), so that 16 tokens read
 // at one chunk meet all banks.
-// The kernel above and this one, us: 4 x 4096, checkpoint, 16 tokens 5.5 and 6.3, 24:
-// 7.4 and 6.3, 4096: 62 and 42; fp32 16: 7.3 and 6.4, 24: 10.3 and 6.3, 4096: 162 and
-// 70 (x and dy alone: 22 and 56).  8 x 4096, where a unit's planes are 30 KiB and
-// eight waves share them: checkpoint 64 tokens 12.1 and 16.6, 96: 16.4 and 16.0, 2048:
-// 78 and 61 (86 with four waves); fp32 64: 15.0 and 19.0, 96: 22.6 and 19.2.
+// The kernel above (with planes made beforehand) and this one, us: 4 x 4096,
+// checkpoint, 16 tokens 5.5 and 6.3, 24: 7.4 and 6.3, 4096: 62 and 42; fp32 16: 7.3 and
+// 6.4, 24: 10.3 and 6.3, 4096: 162 and 70 (x and dy alone: 22 and 56).  8 x 4096, where
+// a unit's planes are 30 KiB and eight waves share them: checkpoint 64 tokens 12.1 and
+// 16.6, 96: 16.4 and 16.0, 2048: 78 and 61 (86 with four waves).
+// DIRECT: one group of tokens, which needs W once: its fp32 rows are staged instead
+// and each wave cuts its operands from them.  37 tokens of 3 x 1028 in fp32: 6.6 us
+// against 8.7 with the planes' launch, and 5 us less a call; 128 of 8 x 4096 from a
+// checkpoint 29 and 24, a call the same.
 constexpr int staged_waves(int S) { return S <= 4 ? 4 : 8; }
 
-template <int S, bool F8>
+template <int S, bool F8, bool DIRECT>
 __global__ __launch_bounds__(64 * staged_waves(S)) void pre_bwd_dots_staged_kernel(
     const unsigned char* __restrict__ x, const unsigned char* __restrict__ xs,
-    const unsigned char* __restrict__ wp, const unsigned char* __restrict__ dy, int T, int H,
+    const unsigned char* __restrict__ w, const unsigned char* __restrict__ dy, int T, int H,
     int KB, int G, int HS, int steps, float* __restrict__ part) {
   constexpr int R = rows_of(S), NRT = steps_of(S), V = R + 1 + S, W = staged_waves(S);
   constexpr int NS = F8 ? 3 : 2;             // stages
   constexpr int LX = F8 ? 2 : 4;             // a wave's loads of x and scales a unit
-  constexpr int LW = (6 * NRT + W - 1) / W;  // and of planes
+  constexpr int LW = ((DIRECT ? 4 : 6) * NRT + W - 1) / W;  // and of planes, or of W
   constexpr int XB = F8 ? 16 * 64 + 64 * 4 : 16 * 256;  // a wave's bytes of them
   constexpr int STAGE = W * (XB + LW * 1024);
   // one variable a stage: the compiler then knows which loads a read depends on
@@ -338,18 +343,18 @@ __global__ __launch_bounds__(64 * staged_waves(S)) void pre_bwd_dots_staged_kern
   auto stage_of = [&](int i) -> unsigned char* {
     return i == 0 ? stage0 : i == 1 ? stage1 : stage2;
   };
-  // four loads of four tokens of `row` quads each, from quad q0 of 16 sl on; tokens past
-  // the end read the last one, quads past the hidden size the last one too
-  auto fetch_quads = [&](const unsigned char* p, size_t row, size_t q0, int sl,
+  // a load of slice sl of rows k .. k + 3 (of `count`, past the end the last one) of
+  // `pitch` quads each, from quad q0 on; quads past the hidden size are its last one
+  auto fetch_quads = [&](const unsigned char* p, int k, int count, size_t pitch, size_t q0, int sl,
                          unsigned char* to) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = 4 * i + (lane >> 4), q = min(16 * sl + ((lane & 15) ^ k), HQ - 1);
-      load_to_lds(p + ((size_t)min(first + k, T - 1) * row + q0 + q) * 16, to + i * 1024);
-    }
+    const int row = k + (lane >> 4), q = min(16 * sl + ((lane ^ row) & 15), HQ - 1);
+    load_to_lds(p + ((size_t)min(row, count - 1) * pitch + q0 + q) * 16, to);
   };
   auto fetch_dy = [&](int sl) {
-    fetch_quads(dy, HQ, 0, sl, reinterpret_cast<unsigned char*>(dyl + wave * 256));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      fetch_quads(dy, first + 4 * i, T, HQ, 0, sl,
+                  reinterpret_cast<unsigned char*>(dyl + wave * 256 + i * 64));
   };
   const size_t crow = (size_t)min(first + (lane >> 2), T - 1) * S;
   const size_t srow = (size_t)min(t, T - 1) * S;
@@ -362,12 +367,20 @@ __global__ __launch_bounds__(64 * staged_waves(S)) void pre_bwd_dots_staged_kern
       load_to_lds(x + ((crow + c) * KB * 8 + 4 * sl + chunk) * 16, sx);
       load_byte_to_lds(xs + (srow + c) * KB + (sl >> 1), sx + 16 * 64);
     } else {
-      fetch_quads(x, (size_t)S * HQ, (size_t)c * HQ, sl, sx);
-    }
-    const unsigned char* w = wp + ((size_t)(c * HS + sl) * 6 * NRT * 64 + lane) * 16;
 #pragma unroll
-    for (int i = 0; i < LW; ++i)
-      load_to_lds(w + (wave + W * i) * 1024, st + W * XB + (wave + W * i) * 1024);
+      for (int i = 0; i < 4; ++i)
+        fetch_quads(x, first + 4 * i, T, (size_t)S * HQ, (size_t)c * HQ, sl, sx + i * 1024);
+    }
+    const unsigned char* wu = w + ((size_t)(c * HS + sl) * 6 * NRT * 64 + lane) * 16;
+#pragma unroll
+    for (int i = 0; i < LW; ++i) {
+      const int j = wave + W * i;
+      unsigned char* to = st + W * XB + j * 1024;
+      if constexpr (DIRECT)
+        fetch_quads(w, 4 * j, R, (size_t)S * HQ, (size_t)c * HQ, sl, to);
+      else
+        load_to_lds(wu + j * 1024, to);
+    }
   };
   floatx4 acc[NRT];
   float ss = 0.f, dp[S];
@@ -418,13 +431,16 @@ __global__ __launch_bounds__(64 * staged_waves(S)) void pre_bwd_dots_staged_kern
           xq[i] = u <= last && 16 * sl + 4 * g + i < HQ ? v : zero;
         }
       }
-      bf16x8 w[6][NRT];
+      // planes 3 step + p, or columns 4 step + e of W
+      constexpr int WQ = DIRECT ? 4 : 6;
+      typedef typename std::conditional<DIRECT, float4, bf16x8>::type Part;
+      Part wr[WQ][NRT];
 #pragma unroll
-      for (int p = 0; p < 6; ++p)
+      for (int p = 0; p < WQ; ++p)
 #pragma unroll
         for (int i = 0; i < NRT; ++i)
-          w[p][i] = *reinterpret_cast<const bf16x8*>(st + W * XB + (p * NRT + i) * 1024 +
-                                                     lane * 16);
+          wr[p][i] = reinterpret_cast<const Part*>(st + W * XB)[
+              DIRECT ? (16 * i + r) * 16 + ((4 * g + p) ^ r) : (p * NRT + i) * 64 + lane];
       __builtin_amdgcn_sched_barrier(0);
       if (c == 0) {
         // the wave's own rows, read just now, make room for the next slice's
@@ -459,14 +475,21 @@ __global__ __launch_bounds__(64 * staged_waves(S)) void pre_bwd_dots_staged_kern
         ss = fma4(xb, xb, fma4(xa, xa, ss));
         dc = fma4(d[2 * step + 1], xb, fma4(d[2 * step], xa, dc));
 #pragma unroll
-        for (int p = 0; p < 3; ++p)
+        for (int i = 0; i < NRT; ++i) {
+          bf16x8 wv[3];
+          if constexpr (DIRECT) {
+            const int q = 16 * sl + 4 * g + 2 * step;
+            planes8(q < HQ ? wr[2 * step][i] : zero, q + 1 < HQ ? wr[2 * step + 1][i] : zero, wv);
+          } else {
 #pragma unroll
-          for (int i = 0; i < NRT; ++i) {
+            for (int p = 0; p < 3; ++p) wv[p] = wr[step * 3 + p][i];
+          }
+#pragma unroll
+          for (int p = 0; p < 3; ++p)
 #pragma unroll
             for (int m = 0; m < (F8 ? 1 : 3 - p); ++m)
-              acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[step * 3 + p][i], o[m], acc[i], 0,
-                                                               0, 0);
-          }
+              acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[p], o[m], acc[i], 0, 0, 0);
+        }
       }
 #pragma unroll
       for (int i = 0; i < S; ++i) dp[i] += i == c && u <= last ? dc : 0.f;
@@ -941,7 +964,7 @@ namespace {
 // 2048 and 1024 waves (8 and 4 per compute unit) where the shape has that many.
 struct Plan {
   int TT, G, HS, steps, Q, SB, chunk, chunks;
-  bool split, staged;
+  bool split, staged, direct;
   size_t planes, part, ua, ut, side, red, dw, floats;  // offsets and total, in floats
 };
 size_t round64(size_t v) { return (v + 63) / 64 * 64; }
@@ -950,12 +973,13 @@ int div_up(int a, int b) { return (a + b - 1) / b; }
 Plan plan(int T, int S, int H, bool f8) {
   Plan p;
   const int R = rows_of(S);
-  p.staged = S <= 4 ? T > 16 : T >= 16 * S;
+  p.staged = T > (S <= 4 ? 16 : 64);
   p.TT = T <= 16 ? 1 : 2;
   const int groups = p.staged ? div_up(T, 16 * staged_waves(S)) : div_up(T, 16 * p.TT);
   const int waves = p.staged ? 1 : 4;  // of a block that divide its slices
   p.steps = div_up(p.HS = div_up(H, 64), waves * div_up(p.staged && S > 4 ? 256 : 512, groups));
   p.G = div_up(p.HS, waves * p.steps);
+  p.direct = !p.staged || groups == 1;  // W cut into planes by the dots themselves
   p.split = !p.staged && S > 1 && groups * p.G * S <= 512;
   if (p.split) p.G *= S;
   // The stream's split: of the counts of ranges that fill one to four rounds of the
@@ -982,7 +1006,7 @@ Plan plan(int T, int S, int H, bool f8) {
   size_t at = 0;
   p.planes = at;  // 64 lanes of 16 bytes for each step, plane and row tile
   // (the staged dots read a unit in multiples of 4 or 8 of them, past the last one)
-  at += ((size_t)S * p.HS * 2 * 3 * div_up(R, 16) + 7) * 64 * 4;
+  if (!p.direct) at += ((size_t)S * p.HS * 2 * 3 * div_up(R, 16) + 7) * 64 * 4;
   p.part = at;
   at += round64((size_t)p.G * T * (R + 1 + S));
   // three planes of two bytes, 32 tokens by 16 (32) rows a step (tile)
@@ -1004,8 +1028,7 @@ template <int S, bool F8, int TT, bool SPLIT>
 void dots(const PreBwd& a, const Plan& p, int T, int H, int KB, float* work, hipStream_t st) {
   hipLaunchKernelGGL((pre_bwd_dots_kernel<S, F8, TT, SPLIT>),
                      dim3((unsigned)(div_up(T, 16 * TT) * p.G)), dim3(256), 0, st, a.x,
-                     a.x_scales, reinterpret_cast<const bf16x8*>(work + p.planes), a.dy, T, H,
-                     KB, p.G, p.HS, p.steps, work + p.part);
+                     a.x_scales, a.fn_w, a.dy, T, H, KB, p.G, p.HS, p.steps, work + p.part);
 }
 
 template <int S, bool F8>
@@ -1022,20 +1045,24 @@ void run(const PreBwd& a, int T, int H, int iters, float eps, float* work, hipSt
   const Plan p = plan(T, S, H, F8);
   float *part = work + p.part, *side = work + p.side, *red = work + p.red;
   float* dw = p.chunks > 1 ? work + p.dw : a.dfn_w;
-  constexpr int NRT = steps_of(S);
-  const long frags = (long)S * p.HS * 2 * NRT * 64;
-  hipLaunchKernelGGL(pre_bwd_planes_kernel, dim3((unsigned)((frags + 255) / 256)), dim3(256), 0,
-                     st, a.fn_w, R, NRT, S, H, p.HS, F8 || p.staged, frags,
-                     reinterpret_cast<bf16x8*>(work + p.planes));
-  constexpr bool MANY = S > 1;
-  if (p.staged) {
-    hipLaunchKernelGGL((pre_bwd_dots_staged_kernel<S, F8>),
-                       dim3((unsigned)(div_up(T, 16 * staged_waves(S)) * p.G)),
+  auto staged = [&](auto kernel, const void* w) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(div_up(T, 16 * staged_waves(S)) * p.G)),
                        dim3(64 * staged_waves(S)), 0, st,
                        static_cast<const unsigned char*>(a.x), a.x_scales,
-                       reinterpret_cast<const unsigned char*>(work + p.planes),
+                       static_cast<const unsigned char*>(w),
                        reinterpret_cast<const unsigned char*>(a.dy), T, H, KB, p.G, p.HS, p.steps,
                        part);
+  };
+  constexpr bool MANY = S > 1;
+  if (p.staged && p.direct) {
+    staged(pre_bwd_dots_staged_kernel<S, F8, true>, a.fn_w);
+  } else if (p.staged) {
+    constexpr int NRT = steps_of(S);
+    const long frags = (long)S * p.HS * 2 * NRT * 64;
+    hipLaunchKernelGGL(pre_bwd_planes_kernel, dim3((unsigned)((frags + 255) / 256)), dim3(256), 0,
+                       st, a.fn_w, R, NRT, S, H, p.HS, frags,
+                       reinterpret_cast<bf16x8*>(work + p.planes));
+    staged(pre_bwd_dots_staged_kernel<S, F8, false>, work + p.planes);
   } else if (p.TT == 2) {
     if constexpr (S > 4)  // staged with fewer
       p.split ? dots<S, F8, 2, MANY>(a, p, T, H, KB, work, st)

@@ -116,7 +116,9 @@ BWD_REL = 2.5e-5
                                    (530, 5, 388), (540, 6, 132), (550, 7, 260), (600, 8, 1028),
                                    (2049, 4, 260), (1601, 4, 4096), (1031, 8, 2052), (512, 4, 4),
                                    (4097, 4, 4096), (4100, 3, 4100), (2100, 2, 16388),
-                                   (1200, 1, 32772), (3001, 4, 7168)])
+                                   (1200, 1, 32772), (3001, 4, 7168), (17, 1, 4), (64, 4, 1028),
+                                   (65, 4, 1028), (50, 2, 4100), (100, 5, 388), (97, 6, 132),
+                                   (112, 7, 260), (128, 8, 1028), (16, 8, 4100), (90, 8, 516)])
 @pytest.mark.parametrize("f8", [True, False])
 def test_pre_bwd(mhc, T, S, H, f8):
     print(f"[case] pre_bwd T={T} S={S} H={H} f8={f8}", flush=True)
