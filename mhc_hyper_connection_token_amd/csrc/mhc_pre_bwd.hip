@@ -22,6 +22,7 @@
 
 #include "mhc_f8.h"
 #include "mhc_kernels.h"
+#include "mhc_waits.h"
 
 namespace mhc {
 
@@ -301,7 +302,8 @@ __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
 // The dots of more than 16 tokens (more than 64 with S > 4), staged: a block
 // takes 16 tokens a wave and walks units of one stream of one slice.  x (codes and
 // scales, or fp32) and planes come into LDS by direct loads, two units ahead in
-// three stages in turn (fp32: one ahead, two stages), dy a slice ahead: the planes
+// three stages in turn (fp32: one ahead, two stages), dy a slice ahead (what a wave
+// waits for: mhc_waits.h): the planes
 // are read once a block, and no wave waits for one kind of load after the other.  A
 // unit is read into registers before the next loads are asked for, since the
 // compiler lets no read pass a load whose place it cannot tell apart.  A token's
@@ -352,7 +354,7 @@ __global__ __launch_bounds__(64 * staged_waves(S)) void pre_bwd_dots_staged_kern
   };
   auto fetch_dy = [&](int sl) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kDyLoads; ++i)
       fetch_quads(dy, first + 4 * i, T, HQ, 0, sl,
                   reinterpret_cast<unsigned char*>(dyl + wave * 256 + i * 64));
   };
@@ -398,14 +400,16 @@ __global__ __launch_bounds__(64 * staged_waves(S)) void pre_bwd_dots_staged_kern
 #pragma unroll
     for (int here = 0; here < NS; ++here) {
       const int u = u0 + here, sl = s0 + u / S;
-      // this unit's stage has landed.  Of three, the next unit's loads may be on their
-      // way, behind the four of dy where the unit before began a slice.
+      // this unit's stage has landed, and dy where it begins a slice; of three stages the
+      // next unit's loads may be on their way
       if constexpr (NS == 2)
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-      else if (c == 1 % S && u > 0)
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LX + LW + 4) : "memory");
+      else if (c == 1)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(dots_in_flight(S, 1, LX + LW))
+                     : "memory");
       else
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LX + LW) : "memory");
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(dots_in_flight(S, 0, LX + LW))
+                     : "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
       if (c == 0) {

@@ -139,6 +139,24 @@ def test_pre_bwd(mhc, T, S, H, f8):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("S", [1, 2])
+def test_pre_bwd_reads_each_slice_of_dy(mhc, S):
+    """Several slices of the hidden axis to a block, each with a dy of its own.  With
+    x = 1, W = 0 and base = 0 every pre gate is 1/2 and dz = dy.x / 4; all sums are of whole
+    numbers with a common factor and below 2^24 of it, so they are exact: 64 * (1 + .. + 64)
+    a token and stream."""
+    T, H = 4096, 4096
+    print(f"[case] pre_bwd slices of dy S={S}", flush=True)
+    x = mhc.f8_encode(torch.ones(T, S, H, device="cuda"))
+    dy = (torch.arange(H, device="cuda") // 64 + 1).float().expand(T, H).contiguous()
+    R = (2 + S) * S
+    z = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    dx, _, _, dbase = mhc.site_pre_bwd(x, z(R, S * H), z(3) + 1, z(R), 20, EPS, dy, z(T, S),
+                                       z(T, S, S))
+    assert (dbase[:S] == T * 64 * 2080 / 4).all(), dbase[:S]
+    assert torch.equal(dx, (dy / 2).unsqueeze(1).expand(T, S, H))
+
+
 def test_pre_bwd_keeps_a_bad_token_to_itself(mhc):
     """A token with a NaN code, in one stream: every other token's gradient is what it
     is without it."""
