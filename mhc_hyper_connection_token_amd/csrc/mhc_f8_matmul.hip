@@ -45,7 +45,7 @@ template <int MT, int NF, int W, int U, typename O>
 __global__ __launch_bounds__(64 * W) void f8_matmul_narrow_kernel(
     const unsigned char* __restrict__ a, const unsigned char* __restrict__ as,
     const unsigned char* __restrict__ b, const unsigned char* __restrict__ bs, int bshift, int M,
-    int N, int KB, O* __restrict__ out) {
+    int N, int KB, int pitch_o, O* __restrict__ out) {
   __shared__ floatx4 part[W][MT * NF][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
   const int n0 = blockIdx.x * 16 * NF;
@@ -126,7 +126,7 @@ __global__ __launch_bounds__(64 * W) void f8_matmul_narrow_kernel(
 #pragma unroll
     for (int w = 1; w < W; ++w) s += part[w][f][l];
     const int m = 16 * (f / NF) + (l & 15), nq = n0 + 16 * (f % NF) + 4 * (l >> 4);
-    if (m < M && nq < N) store_quad(out + (size_t)m * N + nq, s[0], s[1], s[2], s[3]);
+    if (m < M && nq < N) store_quad(out + (size_t)m * pitch_o + nq, s[0], s[1], s[2], s[3]);
   }
 }
 
@@ -155,7 +155,7 @@ template <int FM, int FN, int WM, int WN, int NS, int KG, typename O>
 __global__ __launch_bounds__(64 * WM * WN * KG, 2) void f8_matmul_tile_kernel(
     const unsigned char* __restrict__ a, const unsigned char* __restrict__ as,
     const unsigned char* __restrict__ b, const unsigned char* __restrict__ bs, int bshift, int M,
-    int N, int KB, int MT, int NT, O* __restrict__ out) {
+    int N, int KB, int pitch_o, int MT, int NT, O* __restrict__ out) {
   constexpr int W = WM * WN * KG, BM = 32 * FM * WM, BN = 32 * FN * WN, ROWS = BM + BN;
   constexpr int LOADS = KG * ROWS / 8 / W;  // wave loads (8 rows of 128 bytes) a stage
   constexpr int STAGE = KG * ROWS * kF8Block;
@@ -357,7 +357,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void f8_matmul_tile_kernel(
   for (int i = 0; i < FM; ++i) {
     const int m = m0 + (wm * FM + i) * 32 + r;
     if (m >= M) continue;
-    O* orow = out + (size_t)m * N;
+    O* orow = out + (size_t)m * pitch_o;
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
@@ -375,7 +375,7 @@ namespace {
 template <typename O>
 struct Args {
   const unsigned char *a, *as, *b, *bs;
-  int bshift, M, N, KB;
+  int bshift, M, N, KB, pitch_o;
   O* out;
   hipStream_t st;
 };
@@ -384,7 +384,7 @@ template <int MT, int NF, int W, int U, typename O>
 void narrow(const Args<O>& p) {
   hipLaunchKernelGGL((f8_matmul_narrow_kernel<MT, NF, W, U, O>),
                      dim3((p.N + 16 * NF - 1) / (16 * NF)), dim3(64 * W), 0, p.st, p.a, p.as,
-                     p.b, p.bs, p.bshift, p.M, p.N, p.KB, p.out);
+                     p.b, p.bs, p.bshift, p.M, p.N, p.KB, p.pitch_o, p.out);
 }
 template <int FM, int FN, int WM, int WN, int NS, int KG, typename O>
 void tile(const Args<O>& p) {
@@ -392,14 +392,30 @@ void tile(const Args<O>& p) {
   const int NT = (p.N + 32 * FN * WN - 1) / (32 * FN * WN);
   hipLaunchKernelGGL((f8_matmul_tile_kernel<FM, FN, WM, WN, NS, KG, O>),
                      dim3((unsigned)(MT * NT)), dim3(64 * WM * WN * KG), 0, p.st, p.a, p.as, p.b,
-                     p.bs, p.bshift, p.M, p.N, p.KB, MT, NT, p.out);
+                     p.bs, p.bshift, p.M, p.N, p.KB, p.pitch_o, MT, NT, p.out);
 }
 long tiles_of(long M, long N, long bm, long bn) {
   return ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
 }
 
+// Columns of one launch: its threads stay below the 2^32 that a grid's dimension may
+// have (64 a column at most, in the narrow kernel), its rounding up in an int.
+constexpr int kLaunchCols = 1 << 24;
+
 template <typename O>
 void matmul(const Args<O>& p) {
+  if (p.N > kLaunchCols) {
+    for (int n0 = 0; n0 < p.N;) {
+      Args<O> part = p;
+      part.b += (size_t)n0 * p.KB * kF8Block;
+      part.bs += (size_t)(n0 >> p.bshift) * p.KB;
+      part.out += n0;
+      part.N = p.N - n0 < kLaunchCols ? p.N - n0 : kLaunchCols;
+      n0 += part.N;
+      matmul(part);
+    }
+    return;
+  }
   // Few rows: the weight streams through the narrow kernel, 16 columns a block for as
   // many blocks as there are.  Where 64 columns a block still leave a hundred blocks
   // and more: the whole depth of 32 blocks in flight (8 x 16384 x 4096: 13.6 us, 16.7
@@ -442,10 +458,10 @@ hipError_t launch_f8_matmul(const unsigned char* a, const unsigned char* as,
                             int N, int K, void* out, bool bf16, hipStream_t st) {
   const int KB = K / kF8Block, bshift = square ? 7 : 0;
   if (bf16)
-    matmul(Args<__hip_bfloat16>{a, as, b, bs, bshift, M, N, KB,
+    matmul(Args<__hip_bfloat16>{a, as, b, bs, bshift, M, N, KB, N,
                                 static_cast<__hip_bfloat16*>(out), st});
   else
-    matmul(Args<float>{a, as, b, bs, bshift, M, N, KB, static_cast<float*>(out), st});
+    matmul(Args<float>{a, as, b, bs, bshift, M, N, KB, N, static_cast<float*>(out), st});
   return hipGetLastError();
 }
 

@@ -276,6 +276,39 @@ def test_matmul_past_32_bits(mhc, M):
     assert ((got[-tail:].double() - va @ vb.t()).abs() <= bound).all()
 
 
+@pytest.mark.parametrize("N", [1 << 29, (1 << 31) - 4])
+def test_matmul_of_no_depth_for_very_many_columns(mhc, N):
+    """More columns than one launch's threads: K = 0 needs nothing but the output."""
+    print(f"[case] matmul 1x{N}x0", flush=True)
+    e = lambda r, k, t: torch.empty(r, k, device="cuda", dtype=t)  # noqa: E731
+    out = torch.full((1, N), 3.0, device="cuda", dtype=torch.bfloat16)
+    mhc.f8_matmul(e(1, 0, torch.float8_e4m3fn), e(1, 0, torch.uint8),
+                  e(N, 0, torch.float8_e4m3fn), e(N, 0, torch.uint8), out=out)
+    assert not out.view(torch.int16).any()
+
+
+@pytest.mark.parametrize("M", [1, 6, 40])
+@pytest.mark.parametrize("square", [True, False])
+def test_matmul_in_several_launches(mhc, M, square):
+    """The columns next to a launch's last one, and the last of all."""
+    edge, N, K = 1 << 24, (1 << 24) + 132, 128
+    print(f"[case] matmul {M}x{N}x{K} square={square}", flush=True)
+    b = torch.zeros(N, K, device="cuda", dtype=torch.bfloat16)
+    b[:] = _randn(1, 1, K)
+    b[edge - 256:] = _randn(2, 388, K).bfloat16() * 2.0 ** (torch.arange(388, device="cuda") %
+                                                            9).unsqueeze(1)
+    eb, ea = mhc.f8_encode(b, square=square), mhc.f8_encode(_randn(3, M, K))
+    at = (edge - 256) // (128 if square else 1)
+    va, vb = _decode(*ea, K), _decode(eb[0][edge - 256:], eb[1][at:], K, square)
+    bound = K * 2.0 ** -23 * (va.abs() @ vb.abs().t())  # as above
+    out = torch.full((M + 1, N), 7.0, device="cuda")
+    got = mhc.f8_matmul(*ea, *eb, out=out[:M])[:, edge - 256:].double()
+    assert ((got - va @ vb.t()).abs() <= bound).all()
+    assert (out[M] == 7.0).all(), "the row behind the last one was written"
+    same = mhc.f8_matmul(*ea, eb[0][:64].contiguous(), eb[1][:1 if square else 64].contiguous())
+    assert torch.allclose(out[:M, :64], same, rtol=0, atol=2 * bound.max().item())
+
+
 @pytest.mark.parametrize("f8", [True, False])
 def test_site_bwd_past_32_bits(mhc, f8):
     """8.5 GB of state: the last tokens' gradients are what they are alone."""
