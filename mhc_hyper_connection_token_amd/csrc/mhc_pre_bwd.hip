@@ -9,7 +9,7 @@
 //   u_r     = r scale dz_r,   alpha = -(sum_r scale dz_r m_r) r^2 / n
 //   dx_c    = dx_in_c + pre_c dy + sum_r u_r W_r,c + alpha x_c
 //   dW      = sum_t u_t x_t^T,  dbase = sum_t dz,  dscale_g = sum_t sum_g dz m
-// Three to five launches: W cut into bf16 planes (a group of few tokens does it on
+// Three to five launches: W split into bf16 planes (a group of few tokens does it on
 // the way); the dots (raw, ss, dy.x) split over the hidden axis; the gates forward
 // and backward, a block per four tokens (one where S > 4); the stream that writes
 // dx and adds up dW, a wave owning 64 or 128 columns over a range of tokens; and the
@@ -72,34 +72,50 @@ __device__ __forceinline__ float fma4(float4 a, float4 b, float acc) {
 }  // namespace
 
 // ---------------------------------------------------------------- weight planes
-// An fp32 value as three bf16 of eight bits each, high to low: v = p0 + p1 + p2
-// exactly (v cut at 8 bits, the rest cut at 8 bits, and what is left).
-__device__ __forceinline__ void planes(float v, float& p0, float& p1, float& p2) {
-  p0 = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
-  const float rest = v - p0;
-  p1 = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
-  p2 = rest - p1;
-}
-// The bf16 in the upper halves of two floats, as one dword.
+// The two upper halves of two floats, as one dword.
 __device__ __forceinline__ unsigned upper_halves(float lo, float hi) {
   return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+}
+__device__ __forceinline__ unsigned bf16_halves(float lo, float hi) {  // rounded to nearest
+  return __builtin_bit_cast(unsigned, __builtin_convertvector(floatx2{lo, hi}, bf16x2));
+}
+// Two fp32 values as three bf16 each, high to low, one dword a plane: v = p0 + p1 + p2
+// exactly, p0 being v rounded to eight bits, p1 the rest rounded to eight bits and p2
+// what is left (seven bits and less).  |p1| <= 2^-8 and |p2| <= 2^-17 for v in [1, 2),
+// either sign: of a product of two such values the planes' p1 p2, p2 p1 and p2 p2, left
+// out below, are at most 2^-24 (1 + 2^-9) of it, and their signs do not follow its own.
+// Cut instead of rounded, the rests are twice as large and of v's sign: up to 2^-21, and
+// the loss of a sum grows with its length.  The conversion rounds two values in one
+// instruction, so this costs what cutting does, but for p0, which is kept finite (an
+// entry above the largest bf16 would round to an infinity): in fp32 37 tokens of 3 x 1028
+// 24.2 us a call and 23.8, 1024 of 8 x 7168 307 and 305, 4096 of 4 x 4096 254 both.
+__device__ __forceinline__ void planes2(float a, float b, unsigned out[3]) {
+  constexpr float kMax = 0x1.fep127f;  // the largest bf16
+  out[0] = bf16_halves(__builtin_amdgcn_fmed3f(a, -kMax, kMax),
+                       __builtin_amdgcn_fmed3f(b, -kMax, kMax));
+#pragma unroll
+  for (int k = 1; k < 3; ++k) {
+    a -= __uint_as_float(out[k - 1] << 16);
+    b -= __uint_as_float(out[k - 1] & 0xffff0000u);
+    out[k] = bf16_halves(a, b);
+  }
 }
 // Eight fp32 values to their planes, one matrix operand each.
 __device__ __forceinline__ void planes8(float4 a, float4 b, bf16x8 out[3]) {
   const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  float p[3][8];
+  union {
+    unsigned u[4];
+    bf16x8 v;
+  } o[3];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) planes(v[i], p[0][i], p[1][i], p[2][i]);
+  for (int i = 0; i < 4; ++i) {
+    unsigned p[3];
+    planes2(v[2 * i], v[2 * i + 1], p);
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    union {
-      unsigned u[4];
-      bf16x8 v;
-    } o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o.u[i] = upper_halves(p[k][2 * i], p[k][2 * i + 1]);
-    out[k] = o.v;
+    for (int k = 0; k < 3; ++k) o[k].u[i] = p[k];
   }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) out[k] = o[k].v;
 }
 
 // W [R][S*H] as row operands of the dots of many tokens: for stream c, slice of 64
@@ -157,10 +173,10 @@ __device__ __forceinline__ void turn_groups(float& v0, float& v1, float& v2, flo
 // in LDS, the G blocks of a token group by the gates kernel.
 // A slice goes in two steps of 32 columns; entry 4q (q = 0, 1) of lane group g = lane /
 // 16 is column 16g + 8 step + 4q of codes (a lane's 16 bytes) and 32 step + 16q + 4g of
-// fp32.  W, which a few tokens need only once, is cut into planes on the way.
+// fp32.  W, which a few tokens need only once, is split into planes on the way.
 // The dots run on v_mfma_f32_16x16x32_bf16 with W in three planes.  A decoded
-// code is exact in bf16, so three products give fp32 dots; an fp32 x is cut into
-// planes as well and takes six (the three left out are below 2^-24).
+// code is exact in bf16, so three products give fp32 dots; an fp32 x is split into
+// planes as well and takes six (planes2 says what the three left out are).
 // Every load of x and dy gives the four lane groups 64 neighbouring bytes of a
 // token; dy, four floats a lane, is then turned between the groups to meet the
 // codes' order.  Bound by waits: a wave asks in turn for dy, x, the planes and the
@@ -316,7 +332,7 @@ __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
 // a unit's planes are 30 KiB and eight waves share them: checkpoint 64 tokens 12.1 and
 // 16.6, 96: 16.4 and 16.0, 2048: 78 and 61 (86 with four waves).
 // DIRECT: one group of tokens, which needs W once: its fp32 rows are staged instead
-// and each wave cuts its operands from them.  37 tokens of 3 x 1028 in fp32: 6.6 us
+// and each wave makes its operands from them.  37 tokens of 3 x 1028 in fp32: 6.6 us
 // against 8.7 with the planes' launch, and 5 us less a call; 128 of 8 x 4096 from a
 // checkpoint 29 and 24, a call the same.
 constexpr int staged_waves(int S) { return S <= 4 ? 4 : 8; }
@@ -643,11 +659,11 @@ __global__ __launch_bounds__(256) void pre_bwd_gates_kernel(
         uv = scale[grp] * dz * rinv;
         red[(size_t)r * T + t] = dz;
       }
-      float p[3];
-      planes(uv, p[0], p[1], p[2]);
+      unsigned p[3];
+      planes2(uv, uv, p);
 #pragma unroll
       for (int q = 0; q < 3; ++q) {
-        const unsigned short v = (unsigned short)(__float_as_uint(p[q]) >> 16);
+        const unsigned short v = (unsigned short)p[q];
         if (r < 16 * KS)
           ua[((((t >> 5) * KS + (r >> 4)) * 3 + q) * 64 + i + 32 * ((r >> 3) & 1)) * 8 +
              (r & 7)] = v;
@@ -673,8 +689,8 @@ __global__ __launch_bounds__(256) void pre_bwd_gates_kernel(
 // of a step.  Product q takes the q-th column of every group, so that each lane
 // moves Q neighbouring floats of 16 tokens and the results land where they are
 // stored from:
-//   dx: D[token][column] += u W over the rows, both in planes (six products; the
-//       three left out are below 2^-24), started from dx_in + pre dy + alpha x
+//   dx: D[token][column] += u W over the rows, both in planes (six products, as in the
+//       dots), started from dx_in + pre dy + alpha x
 //   dW: D[row][column] += u^T x over the tokens, x exact in bf16 (fp32: in planes)
 // The weight's planes are the lanes' own columns: each wave makes them once, in
 // LDS.  u comes in operand order from the gates kernel:
@@ -826,18 +842,16 @@ __global__ __launch_bounds__(256, 1) void pre_bwd_stream_kernel(
       }
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        float pl[2][3];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < 2; ++k)
           acc[q][i + k] = fmaf(a[k], v[k][q], fmaf(p[k], d[i + k][q], o[i + k][q]));
-          if constexpr (F8)
-            pl[k][0] = v[k][q];
-          else
-            planes(v[k][q], pl[k][0], pl[k][1], pl[k][2]);
-        }
+        unsigned pl[3];
+        if constexpr (F8)
+          pl[0] = upper_halves(v[0][q], v[1][q]);
+        else
+          planes2(v[0][q], v[1][q], pl);
 #pragma unroll
-        for (int m = 0; m < XP; ++m)
-          xo[i >> 3][q][m].u[(i & 7) >> 1] = upper_halves(pl[0][m], pl[1][m]);
+        for (int m = 0; m < XP; ++m) xo[i >> 3][q][m].u[(i & 7) >> 1] = pl[m];
       }
     }
     // u first: loads come back in order, and what is asked for after the next step's
@@ -983,7 +997,7 @@ Plan plan(int T, int S, int H, bool f8) {
   const int waves = p.staged ? 1 : 4;  // of a block that divide its slices
   p.steps = div_up(p.HS = div_up(H, 64), waves * div_up(p.staged && S > 4 ? 256 : 512, groups));
   p.G = div_up(p.HS, waves * p.steps);
-  p.direct = !p.staged || groups == 1;  // W cut into planes by the dots themselves
+  p.direct = !p.staged || groups == 1;  // W split into planes by the dots themselves
   p.split = !p.staged && S > 1 && groups * p.G * S <= 512;
   if (p.split) p.G *= S;
   // The stream's split: of the counts of ranges that fill one to four rounds of the
