@@ -508,8 +508,8 @@ def _call(name, device, args, others):
     global _gpus
     fn = _entry.get(name)
     if fn is None:
+        _gpus = torch.cuda.device_count()  # before the entry, which says that it is there
         fn = _entry[name] = getattr(load_library(), name)
-        _gpus = torch.cuda.device_count()
     stream = torch._C._cuda_getCurrentRawStream(device)
     if _gpus > 1:
         for t in others:

@@ -147,3 +147,35 @@ def test_plain_code_table_matches_torch():
     v = v[np.abs(v) <= 448]
     want = torch.from_numpy(v).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
     np.testing.assert_array_equal(pf.e4m3_codes(v.astype(np.float64)), want)
+
+
+def test_first_calls_from_two_threads(lib, monkeypatch):
+    """A second thread's call while the first one's is still being prepared: neither meets
+    a half-prepared state (no GPU: the entry is a stand-in that counts its calls)."""
+    import threading
+    torch = pytest.importorskip("torch")
+    calls, errors = [], []
+    monkeypatch.setattr(mhc, "_entry", {})
+    monkeypatch.setattr(mhc, "_gpus", None)
+    monkeypatch.setattr(mhc, "load_library", lambda: type("L", (), {
+        "mhc_f8_decode": staticmethod(lambda *a: calls.append(a) or 0)}))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
+    second = threading.Event()
+
+    def call():
+        try:
+            mhc._call("mhc_f8_decode", 0, (1, 2), ())
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    def count():
+        if not second.is_set():  # the first thread, between its two steps
+            second.set()
+            t = threading.Thread(target=call)
+            t.start()
+            t.join(30)
+        return 1
+
+    monkeypatch.setattr(torch.cuda, "device_count", count)
+    call()
+    assert errors == [] and calls == [(1, 2, 0), (1, 2, 0)]
