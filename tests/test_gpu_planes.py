@@ -110,6 +110,27 @@ def test_gradient_of_the_weight(mhc, T, S, H, f8):
     _check(dw, d, (left_out + pi.SUMS + pi.ROUND * d["leaks"]) * d["size"] + pi.LEAK, "dW")
 
 
+@pytest.mark.parametrize("T,S,H", [(16, 4, 1028), (50, 7, 516), (37, 3, 132), (300, 4, 516),
+                                   (200, 8, 388)])
+@pytest.mark.parametrize("f8", [False, True])
+def test_small_tokens_beside_large_ones(mhc, T, S, H, f8):
+    """The gradient is linear in what comes in, token by token: a token's gradients times a
+    power of two give that power times its dx, bit for bit, whatever its neighbours have."""
+    print(f"[case] powers of two T={T} S={S} H={H} f8={f8}", flush=True)
+    g = torch.Generator().manual_seed(T)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    R = (2 + S) * S
+    fixed = dict(x=r(T, S, H), w=r(R, S * H) / (S * H) ** 0.5)
+    grads = dict(dy=r(T, H), dpre=r(T, S), dpost=r(T, S), dcomb=r(T, S, S), dx_in=r(T, S, H))
+    by = 2.0 ** (torch.arange(T) * 7 % 41 - 20).float()
+    if f8:
+        fixed["x"] = mhc.f8_decode(*mhc.f8_encode(fixed["x"].cuda()), H).cpu()
+    want = _call(mhc, fixed | grads, f8, 20, 1e-6)[0].cpu()
+    scaled = {k: v * by.reshape(-1, *[1] * (v.dim() - 1)) for k, v in grads.items()}
+    got = _call(mhc, fixed | scaled, f8, 20, 1e-6)[0].cpu()
+    assert torch.equal(got, want * by.reshape(-1, 1, 1))
+
+
 def test_entries_above_the_largest_bf16(mhc):
     """An fp32 entry that rounds to an infinity in bf16 is still itself: a weight that meets
     no gradient, and one that does."""
