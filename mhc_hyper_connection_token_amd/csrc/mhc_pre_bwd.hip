@@ -3,7 +3,7 @@
 // 8-bit checkpoint.  Per token, with n = S*H:
 //   raw = W x, ss = |x|^2, r = 1/sqrt(ss/n + eps), m = r raw, z = scale m + base
 //   dpre_c  = (given) + sum_i dy_i x_c,i
-//   dz      = dpre p(1-p), dpost q(1 - q/2), and exp(z) times the gradient that
+//   dz      = dpre p(1-p), dpost 2 q(1-q) with post = 2 q, and exp(z) times the gradient that
 //             the Sinkhorn rounds hand back: a pass c' = c/s, s = sum c + eps,
 //             has dc = (dc' - sum dc' c') / s over the same row or column
 //   u_r     = r scale dz_r,   alpha = -(sum_r scale dz_r m_r) r^2 / n
@@ -536,6 +536,12 @@ __global__ __launch_bounds__(64 * staged_waves(S)) void pre_bwd_dots_staged_kern
 }
 
 // ---------------------------------------------------------------- gates
+// p (1 - p) of p = sigmoid(z).  Above 1/2, 1 - p is the difference of two close numbers
+// (at z = 12 it has lost 12 of its 24 bits, from 17 on all): there it is e^-z p.
+__device__ __forceinline__ float sigmoid_slope(float z, float p) {
+  return z > 0.0f ? expf(-z) * p * p : p * (1.0f - p);
+}
+
 // One wave per four tokens (one where S > 4): the gates from the dots, then back.
 //   side [S + 1][TP]   the pre gates and alpha (TP: T rounded up to 32)
 //   red [R + 3][T]     dz and, per scale, the sum of dz * m
@@ -591,14 +597,13 @@ __global__ __launch_bounds__(256) void pre_bwd_gates_kernel(
     const size_t t = t0 + k;
     if (k < NU && t < (size_t)T && gt < 2 * S) {
       const float rinv = rms_inverse(raw[k][R], n, eps), m = raw[k][gt] * rinv;
+      const float z = fmaf(scale[gt < S ? 0 : 1], m, base[gt]), p = sigmoid_exact_ends(z);
       if (gt < S) {
-        const float p = sigmoid_exact_ends(fmaf(scale[0], m, base[gt]));
         const float d = raw[k][R + 1 + gt] + (dpre ? dpre[t * S + gt] : 0.f);
         side[gt * TP + t] = p;
-        dzs[k][gt] = d * p * (1.0f - p);
+        dzs[k][gt] = d * sigmoid_slope(z, p);
       } else {
-        const float p = sigmoid_exact_ends(fmaf(scale[1], m, base[gt]));
-        dzs[k][gt] = dpost[t * S + gt - S] * 2.0f * p * (1.0f - p);
+        dzs[k][gt] = dpost[t * S + gt - S] * 2.0f * sigmoid_slope(z, p);
       }
     }
   }

@@ -147,6 +147,30 @@ def test_pre_bwd_in_place_and_most_rounds(mhc):
                                                   want[2].abs().max().item()) if k > 1 else None)
 
 
+@pytest.mark.parametrize("S", [4, 8])
+@pytest.mark.parametrize("T", [1, 30])
+def test_pre_bwd_of_saturated_gates(mhc, S, T):
+    """With W = 0 a gate's argument is its base, and the gradient of base is the gate's slope
+    p (1 - p) (twice that for post): every slope to its own size.  exp, a sum, a reciprocal
+    and three products: at most 16 roundings, 2^-20, but for fp32's least normal number."""
+    print(f"[case] pre_bwd saturated gates T={T} S={S}", flush=True)
+    z = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    R, H = (2 + S) * S, 132
+    for lo, hi in ((-40, 40), (0, 20), (-100, 100), (10, 17.5)):
+        base = torch.zeros(R)
+        base[:2 * S] = torch.linspace(lo, hi, 2 * S)
+        one = z(T, S)
+        one[T // 2] = 1.0
+        got = mhc.site_pre_bwd(z(T, S, H), z(R, S * H), z(3) + 1, base.cuda(), 20, EPS, z(T, H),
+                               one, z(T, S, S), dpre=one)[3].double().cpu()
+        b = base.double()
+        want = torch.sigmoid(b) * torch.sigmoid(-b)
+        want[S:2 * S] *= 2
+        want[2 * S:] = 0
+        bound = 2.0 ** -20 * want + 2.0 ** -126
+        assert ((got - want).abs() <= bound).all(), (got / want)[:2 * S]
+
+
 def test_pre_bwd_of_no_tokens_is_zero(mhc):
     print("[case] pre_bwd T=0", flush=True)
     d = _site(1, 4, 128, 4)
