@@ -74,7 +74,7 @@ __global__ __launch_bounds__(64 * W) void f8_matmul_narrow_kernel(
     unsigned bsv[U][NF], asv[U][MT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      // a block past the end reads the row's last one, its weight codes as zeros
+      // a block past the end reads the row's last one, its codes as zeros
       const int k = min(kb + W * u, KB - 1);
       const size_t at = (size_t)k * kF8Block;
 #pragma unroll
@@ -92,9 +92,12 @@ __global__ __launch_bounds__(64 * W) void f8_matmul_narrow_kernel(
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (kb + W * u >= KB)
+      if (kb + W * u >= KB) {  // of both operands: zero times an infinity is not zero
 #pragma unroll
         for (int j = 0; j < NF; ++j) bv[u][j][0] = bv[u][j][1] = intx4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < MT; ++i) av[u][i][0] = av[u][i][1] = intx4{0, 0, 0, 0};
+      }
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         bf16x8 ax[MT];

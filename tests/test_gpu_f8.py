@@ -200,6 +200,28 @@ def test_matmul_keeps_nan_to_its_row(mhc, M):
     _check_product(got[keep], a[keep], b, "the other rows")
 
 
+@pytest.mark.parametrize("M", [1, 5, 24, 40, 300])
+@pytest.mark.parametrize("K", [128, 384, 2176, 4224])
+def test_matmul_of_an_infinite_value(mhc, M, K):
+    """An entry above 248 * 2^120 decodes to an infinity (include/mhc.h): its row of the
+    product is that infinity with the sign of the other operand, wherever it stands."""
+    print(f"[case] matmul infinity M={M} K={K}", flush=True)
+    N = 20
+    for at in (3, K - 1):
+        a, b = torch.zeros(M, K), torch.ones(N, K)
+        a[0, at] = 3.4e38
+        b[1::2] = -1.0
+        for flip in (False, True):
+            got = mhc.f8_matmul(*mhc.f8_encode(a.cuda()), *mhc.f8_encode(b.cuda())).cpu()
+            want = torch.zeros(M, N)
+            want[0, 0::2], want[0, 1::2] = float("inf"), float("-inf")
+            assert torch.equal(got, want), (at, flip)
+            a[0, 0] = 1.0  # and beside other entries
+    ea, eb = mhc.f8_encode(b.cuda()), mhc.f8_encode(torch.cat([a, torch.zeros(4, K)]).cuda())
+    got = mhc.f8_matmul(*ea, eb[0][:M - M % 4 + 4].contiguous(), eb[1][:M - M % 4 + 4].contiguous())
+    assert torch.isinf(got[:, 0]).all() and not got[:, 1:].any()
+
+
 @pytest.mark.parametrize("M", [4, 40, 300])
 def test_matmul_at_the_ends_of_the_scales(mhc, M):
     """Scale bytes 1 and 247: products near the least and the largest fp32."""
