@@ -99,6 +99,40 @@ def test_every_code_round_trips_and_infinities_are_nan(mhc):
     assert np.isnan(back[3]).all()
 
 
+@pytest.mark.parametrize("rows,cols", [(5, 260), (130, 132), (300, 516)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_encode_of_infinities_and_nan(mhc, rows, cols, dtype):
+    """In every form: single entries, a whole row and column, and a whole 128 x 128 square
+    without a finite entry (scale 2^0, every code NaN)."""
+    print(f"[case] encode non-finite {rows}x{cols} {dtype}", flush=True)
+    g = np.random.default_rng(rows)
+    bad = np.array([np.inf, -np.inf, np.nan])
+    x = g.standard_normal((rows, cols)) * 2.0 ** g.integers(-20, 20, (rows, 1))
+    x[g.random((rows, cols)) < 0.02] = np.inf
+    x[g.random((rows, cols)) < 0.02] = np.nan
+    x[3] = g.choice(bad, cols)
+    x[:, 2] = g.choice(bad, rows)
+    x[:, cols - 1] = -np.inf
+    x[128:256, 128:256] = g.choice(bad, x[128:256, 128:256].shape)
+    x[256:, :128] = g.choice(bad, x[256:, :128].shape)
+    xd = torch.from_numpy(x.astype(np.float32)).to(getattr(torch, dtype)).cuda()
+    x = xd.double().cpu().numpy()
+    assert np.isinf(x).any() and np.isnan(x).any()
+    rows_form, cols_form = pf.encode(x), pf.encode(x.T)
+    square = pf.encode(x, square=True) + pf.encode(x.T, square=True)
+    got = [mhc.f8_encode(xd) + mhc.f8_encode(xd, transposed="only"),
+           mhc.f8_encode(xd, transposed=True), mhc.f8_encode(xd, transposed=True, square=True)]
+    for have, want in zip(got, (rows_form + cols_form, rows_form + cols_form, square)):
+        for k in (0, 2):
+            _check_codes(have[k], want[k], f"codes {k}")
+            np.testing.assert_array_equal(_bytes(have[k + 1]), want[k + 1])
+    values = pf.decode(*rows_form, cols)
+    np.testing.assert_array_equal(mhc.f8_decode(*got[0][:2], cols).double().cpu().numpy(), values)
+    again, want = mhc.f8_repack(*got[0][:2], cols), pf.encode(values.T)
+    _check_codes(again[0], want[0], "repack")
+    np.testing.assert_array_equal(_bytes(again[1]), want[1])
+
+
 @pytest.mark.parametrize("rows,cols", SHAPES)
 def test_decode_and_repack(mhc, rows, cols):
     print(f"[case] decode, repack {rows}x{cols}", flush=True)
