@@ -15,7 +15,6 @@ namespace mhc {
 constexpr int kF8Block = 128;
 
 typedef int intx4 __attribute__((ext_vector_type(4)));
-typedef int intx8 __attribute__((ext_vector_type(8)));
 typedef float floatx2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -109,6 +108,14 @@ __device__ __forceinline__ float4 load_quad<__hip_bfloat16>(const __hip_bfloat16
   const uintx2 v = __builtin_nontemporal_load(reinterpret_cast<const uintx2*>(p));
   return make_float4(__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xffff0000u),
                      __uint_as_float(v[1] << 16), __uint_as_float(v[1] & 0xffff0000u));
+}
+
+// acc + a.b, the four products in order.
+__device__ __forceinline__ float dot4(float4 a, float4 b, float acc) {
+  acc = fmaf(a.x, b.x, acc);
+  acc = fmaf(a.y, b.y, acc);
+  acc = fmaf(a.z, b.z, acc);
+  return fmaf(a.w, b.w, acc);
 }
 
 }  // namespace mhc

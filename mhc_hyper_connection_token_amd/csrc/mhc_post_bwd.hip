@@ -26,13 +26,6 @@ __device__ __forceinline__ float4 kept_quad(const void* p, const unsigned char* 
   }
 }
 
-__device__ __forceinline__ float dot4(float4 a, float4 b, float acc) {
-  acc = fmaf(a.x, b.x, acc);
-  acc = fmaf(a.y, b.y, acc);
-  acc = fmaf(a.z, b.z, acc);
-  return fmaf(a.w, b.w, acc);
-}
-
 template <bool STREAM>
 __device__ __forceinline__ void store_out(float* p, float4 v) {
   if constexpr (STREAM)

@@ -63,12 +63,6 @@ __device__ __forceinline__ void store_columns(__amdgpu_buffer_rsrc_t buf, unsign
     __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uintx2, v), buf, offset, 0,
                                           kNonTemporal);
 }
-__device__ __forceinline__ float fma4(float4 a, float4 b, float acc) {
-  acc = fmaf(a.x, b.x, acc);
-  acc = fmaf(a.y, b.y, acc);
-  acc = fmaf(a.z, b.z, acc);
-  return fmaf(a.w, b.w, acc);
-}
 }  // namespace
 
 // ---------------------------------------------------------------- weight planes
@@ -271,8 +265,8 @@ __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
             xb = q1 < HQ ? p[q1] : zero;
             planes8(xa, xb, xp);
           }
-          ss[k] = fma4(xb, xb, fma4(xa, xa, ss[k]));
-          dc[k] = fma4(d[k][2 * step + 1], xb, fma4(d[k][2 * step], xa, dc[k]));
+          ss[k] = dot4(xb, xb, dot4(xa, xa, ss[k]));
+          dc[k] = dot4(d[k][2 * step + 1], xb, dot4(d[k][2 * step], xa, dc[k]));
 #pragma unroll
           for (int i = 0; i < NRT; ++i) {
 #pragma unroll
@@ -492,8 +486,8 @@ __global__ __launch_bounds__(64 * staged_waves(S)) void pre_bwd_dots_staged_kern
           xb = xq[2 * step + 1];
           planes8(xa, xb, o);
         }
-        ss = fma4(xb, xb, fma4(xa, xa, ss));
-        dc = fma4(d[2 * step + 1], xb, fma4(d[2 * step], xa, dc));
+        ss = dot4(xb, xb, dot4(xa, xa, ss));
+        dc = dot4(d[2 * step + 1], xb, dot4(d[2 * step], xa, dc));
 #pragma unroll
         for (int i = 0; i < NRT; ++i) {
           bf16x8 wv[3];
