@@ -153,7 +153,9 @@ constexpr int kPanel = 32;  // k blocks whose scales are held in LDS
 // the global side, since a direct load writes its lanes in order.
 // What bounds it: with neither loads nor conversions the products alone take
 // 442 us at 4096 x 16384 x 4096 (1240 TFLOP/s; the library's bf16 product of these
-// sizes 420), with them 540: the conversions cost 50, the staging 50.
+// sizes 420), with them 540: the conversions cost 50, the staging 50.  The staging is
+// not all asynchronous (see the stages below), nor is a panel of scales, whose loads are
+// waited for one after the other.
 template <int FM, int FN, int WM, int WN, int NS, int KG, typename O>
 __global__ __launch_bounds__(64 * WM * WN * KG, 2) void f8_matmul_tile_kernel(
     const unsigned char* __restrict__ a, const unsigned char* __restrict__ as,
@@ -164,7 +166,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void f8_matmul_tile_kernel(
   constexpr int STAGE = KG * ROWS * kF8Block;
   static_assert(LOADS * 8 * W == KG * ROWS && BM % 8 == 0, "whole wave loads");
   static_assert(kPanel % KG == 0 && (KG - 1) * WM * WN * FM * FN * 4096 <= STAGE, "sums fit");
-  // one variable a stage: the compiler then knows which loads a read depends on
+  // One variable a stage, by which the compiler can tell a read from the loads under way
+  // into the others.  It does at some places only: elsewhere (four of the eight chunks of
+  // two stages in 256 x 256 tiles, the first of three stages in 64 x 64) it waits for every
+  // load before it reads, and what was asked for a chunk before is waited for there.
   __shared__ __align__(16) unsigned char stage0[STAGE];
   __shared__ __align__(16) unsigned char stage1[STAGE];
   __shared__ __align__(16) unsigned char stage2[NS > 2 ? STAGE : 16];
@@ -420,13 +425,17 @@ void matmul(const Args<O>& p) {
     return;
   }
   // Few rows: the weight streams through the narrow kernel, 16 columns a block for as
-  // many blocks as there are.  Where 64 columns a block still leave a hundred blocks
-  // and more: the whole depth of 32 blocks in flight (8 x 16384 x 4096: 13.6 us, 16.7
-  // at 16 columns; 1 x 16384 x 4096 13.7 and 13.1; 8 x 8192 x 4096 12.6 and 9.9), or,
-  // for shallow products and from 17 rows on, the tiles with four blocks of the depth
-  // at a time (16 x 7168 x 2048 8.6 us against 11.3, 1 x 16384 x 2048 10.4 and 12.6, 1 x
-  // 8192 x 2048 8.8 and 8.0, 16 x 8192 x 4096 14.3 and 11.9; 32 x 8192 x 4096 14.6 and
-  // 17.9, 32 x 4096 x 4096 13.8 and 9.9).
+  // many blocks as there are.  From five rows on and where 64 columns a block still fill
+  // the 256 units: 32 blocks of the depth in flight at a time.  us at 16 and at 64
+  // columns, 8 rows: N = 8192 9.6 and 12.0 at K = 4096, 16.6 and 21.5 at 8192; N = 12288
+  // 13.0 and 12.2, 23.3 and 21.9 (the crossing); N = 16384 16.4 and 13.5, 30.4 and 24.7; N
+  // = 24576, a round and a half, 23.3 and 23.5, 46 and 52; N = 32768 30.0 and 25.5, 60 and
+  // 57.  One row: 12.7 and 13.2, 22.3 and 24.4 at N = 16384, 22.3 and 25.2 at 32768.
+  // Shallow products, and from 17 rows on, take the tiles with four blocks of the depth at
+  // a time: 16 columns and tiles, at K = 2048, 1 x 8192 7.3 and 8.3, 1 x 16384 12.1 and
+  // 9.9, 1 x 24576 16.8 and 17.3, 16 x 5120 10.4 and 7.8, 16 x 16384 18.7 and 10.1; at
+  // K = 4096 16 x 8192 11.6 and 13.7; 32 x 8192 x 4096 14.6 and, narrow, 17.9, 32 x 4096 x
+  // 4096 13.8 and 9.9.
   auto rounds = [&](int b) { return (tiles_of(p.M, p.N, b, b) + 255) / 256; };
   const long tiles64 = tiles_of(p.M, p.N, 64, 64);
   const int side = p.M < p.N ? p.M : p.N;

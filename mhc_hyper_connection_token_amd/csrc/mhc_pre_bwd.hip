@@ -175,7 +175,9 @@ __device__ __forceinline__ void turn_groups(float& v0, float& v1, float& v2, flo
 // token; dy, four floats a lane, is then turned between the groups to meet the
 // codes' order.  Bound by waits: a wave asks in turn for dy, x, the planes and the
 // scales, which two waves a SIMD hardly hide (one token of 4 x 4096: 4.5 us).
-// SPLIT: a block takes one stream, for batches too short to fill the chip otherwise.
+// SPLIT: a block takes one stream, for batches too short to fill the chip otherwise.  In
+// fp32 at S = 8 and TT = 2 the kernel without it spills 14 registers (80 bytes a lane): 64
+// tokens of 8 x 16384 166 us a call, 164 with planes that are cut and spill none.
 template <int S, bool F8, int TT, bool SPLIT>
 __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
     const void* __restrict__ x, const unsigned char* __restrict__ xs,
@@ -316,7 +318,8 @@ __global__ __launch_bounds__(256, 2) void pre_bwd_dots_kernel(
 // waits for: mhc_waits.h): the planes
 // are read once a block, and no wave waits for one kind of load after the other.  A
 // unit is read into registers before the next loads are asked for, since the
-// compiler lets no read pass a load whose place it cannot tell apart.  A token's
+// compiler lets no read pass a load whose place it cannot tell apart (eight streams in
+// fp32 spill three registers on the way, 16 bytes a lane).  A token's
 // chunks of 16 bytes are turned in their row (codes: chunk c at place
 // c ^ token / 4 % 4 of four; fp32: c ^ token % 16 of sixteen), so that 16 tokens read
 // at one chunk meet all banks.
@@ -342,7 +345,10 @@ __global__ __launch_bounds__(64 * staged_waves(S)) void pre_bwd_dots_staged_kern
   constexpr int LW = ((DIRECT ? 4 : 6) * NRT + W - 1) / W;  // and of planes, or of W
   constexpr int XB = F8 ? 16 * 64 + 64 * 4 : 16 * 256;  // a wave's bytes of them
   constexpr int STAGE = W * (XB + LW * 1024);
-  // one variable a stage: the compiler then knows which loads a read depends on
+  // One variable a stage, by which the compiler can tell a read from the loads under way
+  // into the others.  With four and eight streams it does so for the second of three stages
+  // only: before the reads of the others, and of dyl at every slice, it waits for all
+  // loads, so that the prefetch is drained there.
   __shared__ __align__(16) unsigned char stage0[STAGE];
   __shared__ __align__(16) unsigned char stage1[STAGE];
   __shared__ __align__(16) unsigned char stage2[NS > 2 ? STAGE : 16];
