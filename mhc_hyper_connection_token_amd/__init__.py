@@ -632,7 +632,8 @@ def f8_decode(codes, scales, cols: int, *, out=None, stream=None):
 def f8_matmul(a, a_scales, b, b_scales, *, dtype=None, out=None, stream=None):
     """a [M, K] times b [N, K] transposed, both 8-bit blocks: [M, N] float32 (default) or
     bfloat16.  K is the padded width of both (a multiple of 128).  b_scales is [N, K/128],
-    or [ceil(N/128), K/128] for the square form of a weight."""
+    or [ceil(N/128), K/128] for the square form of a weight.  `out` may supply the result;
+    its dtype is then the product's."""
     import torch
     if stream is not None:
         return _on(stream, a.device, f8_matmul, a, a_scales, b, b_scales, dtype=dtype, out=out)
