@@ -455,6 +455,9 @@ int mhc_site_post_bwd(const float* g, const void* x, const unsigned char* x_scal
  *   work, work_bytes     device scratch of the caller, at least
  *                        mhc_site_pre_bwd_work_bytes bytes (MHC_EINVAL if less);
  *                        in use until the call's work is done
+ * What comb adds to the gradients of z passes through differences
+ * (dc' - sum dc' c') in each of its passes: it is accurate to fp32's rounding of
+ * dcomb, not of itself where it is far smaller (comb next to a permutation).
  * Sums over tokens are added in an order fixed by the shape: equal inputs give
  * equal bits.  streams * hidden <= 2^24 (MHC_EUNSUPPORTED above).
  *
