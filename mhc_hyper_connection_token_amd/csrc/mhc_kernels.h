@@ -158,4 +158,59 @@ int pre_bwd_max_iters();
 hipError_t launch_pre_bwd(const PreBwd& p, int T, int S, int H, int iters, float eps, void* work,
                           hipStream_t st);
 
+// The norm before a branch; z is fp32 or bf16.
+hipError_t launch_branch_norm(const float* y, const float* nw, int T, int H, float eps, void* z,
+                              bool bf16, hipStream_t st);
+
+// Post mix of a branch output behind its norm, gate and scale.  Kinds: 0 fp32, 1 bf16.
+// gate may be null; gate_rows: one row of it a token, else one row for all.
+struct PostNorm {
+  const float* x;
+  const void* f;
+  const float* nw;
+  const void* gate;
+  const float* post;
+  const float* comb;
+  float* x_out;
+  float alpha;
+  int f_kind, gate_kind, gate_rows, gate_act;
+};
+hipError_t launch_post_norm(const PostNorm& p, int T, int S, int H, float eps, hipStream_t st);
+
+// Their gradients.  dz: 0 fp32, 1 bf16; y, x and f: also 2, 8-bit blocks with their scales
+// (x_scales null: fp32).  work holds norm_bwd_work_bytes of scratch for each [H] sum over
+// the tokens (one, or two with a gate of one row).
+struct NormBwd {
+  const void* dz;
+  const void* y;
+  const unsigned char* y_scales;
+  const float* nw;
+  float* dy;
+  float* dnw;
+  int dz_kind;
+};
+struct PostNormBwd {
+  const float* g;
+  const void* x;
+  const unsigned char* x_scales;
+  const void* f;
+  const unsigned char* f_scales;
+  const float* nw;
+  const void* gate;
+  const float* post;
+  const float* comb;
+  float* dx;
+  float* df;
+  float* dpost;
+  float* dcomb;
+  float* dnw;
+  float* dgate;
+  float alpha;
+  int f_kind, gate_kind, gate_rows, gate_act;
+};
+size_t norm_bwd_work_bytes(int T, int H, int sums);
+hipError_t launch_norm_bwd(const NormBwd& p, int T, int H, float eps, void* work, hipStream_t st);
+hipError_t launch_post_norm_bwd(const PostNormBwd& p, int T, int S, int H, float eps, void* work,
+                                hipStream_t st);
+
 }  // namespace mhc
