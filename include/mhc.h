@@ -471,6 +471,116 @@ int mhc_site_pre_bwd(const void* x, const unsigned char* x_scales, const float* 
                      float* dfn_w, float* dscale, float* dbase, void* work, size_t work_bytes,
                      void* stream);
 
+/*
+ * The norms around a branch, and their gradients.
+ *
+ * mhc_branch_norm: the norm before a branch, for branches that take fp32 or bf16
+ *   (mhc_site_pre_zq8 has it with int8 codes):
+ *     z[t,i] = y[t,i] * nw[i] / sqrt(mean_i y[t,i]^2 + norm_eps)
+ * mhc_site_post_norm: mhc_site_post with the norm behind the branch, its gate and the
+ *   residual scale in front of the mix:
+ *     n[t,i]       = f[t,i] / sqrt(mean_i f[t,i]^2 + norm_eps)
+ *     h[t,i]       = alpha * a(gate[t,i]) * n[t,i] * nw[i]
+ *     x_out[t,k,i] = post[t,k] * h[t,i] + sum_j comb[t,j,k] * x[t,j,i]
+ *   a(v) = v (MHC_GATE_PLAIN), 1/(1+exp(-v)) (MHC_GATE_SIGMOID) or v/(1+exp(-v))
+ *   (MHC_GATE_SILU); without a gate, a = 1.
+ * mhc_branch_norm_bwd: from dz = dL/dz, with n = y / sqrt(mean y^2 + norm_eps) = y r:
+ *     dy[t,i] = r (dz nw - n mean_i(dz nw n));  dnw[i] = sum_t dz n
+ * mhc_site_post_norm_bwd: from g = dL/dx_out, with e[t,i] = sum_k post[t,k] g[t,k,i]:
+ *     dx[t,j,i] = sum_k comb[t,j,k] g[t,k,i];  dcomb[t,j,k] = sum_i x[t,j,i] g[t,k,i]
+ *     dpost[t,k] = sum_i g[t,k,i] h[t,i]
+ *     df: as dy above with dz = alpha e a(gate);  dnw[i] = sum_t alpha e a(gate) n
+ *     dgate[t,i] = alpha e a'(gate) n nw, summed over t where the gate has one row
+ *
+ * Arguments:
+ *   y [T][H] fp32; in the gradient fp32 with y_scales NULL, or the codes and scales of
+ *     its 8-bit checkpoint (mhc_f8_encode)
+ *   nw [H]; norm_eps > 0 and finite
+ *   z, z_type and dz, dz_type   MHC_F32 or MHC_BF16 (z rounded to nearest even)
+ *   x, post, comb, T, streams, hidden   as mhc_site_post; in the gradient x as in
+ *     mhc_site_post_bwd
+ *   f, f_type   [T][H], MHC_F32 or MHC_BF16; in the gradient, where f_scales is given,
+ *     its 8-bit checkpoint (f_type is not read then)
+ *   gate, gate_type, gate_rows, gate_act   [gate_rows][H] of MHC_F32 or MHC_BF16, one row
+ *     for all tokens (gate_rows = 1) or one a token (gate_rows = T); NULL for none (the
+ *     other three are not read then)
+ *   alpha   any finite number
+ *   dy, dx, df, dpost, dcomb, dnw [H]   out, fp32
+ *   dgate   [gate_rows][H] fp32 out, NULL without a gate
+ *   work, work_bytes   device scratch of the caller, at least mhc_norm_bwd_work_bytes
+ *     bytes (MHC_EINVAL if less); in use until the call's work is done
+ * hidden <= 16384 (MHC_EUNSUPPORTED above).  T = 0 does nothing but to zero the sums over
+ * tokens.  Sums are fp32, those over tokens added in an order fixed by the shape: equal
+ * inputs give equal bits.  A token's squares must stay within fp32.
+ *
+ * mhc_norm_bwd_work_bytes: 0 for T < 1 or a hidden that the calls reject.
+ */
+enum { MHC_GATE_PLAIN = 0, MHC_GATE_SIGMOID = 1, MHC_GATE_SILU = 2 };
+
+int mhc_branch_norm(const float* y, const float* nw, int T, int hidden, float norm_eps, void* z,
+                    int z_type, void* stream);
+int mhc_site_post_norm(const float* x, const void* f, int f_type, const float* nw,
+                       const void* gate, int gate_type, int gate_rows, int gate_act, float alpha,
+                       const float* post, const float* comb, int T, int streams, int hidden,
+                       float norm_eps, float* x_out, void* stream);
+size_t mhc_norm_bwd_work_bytes(int T, int hidden);
+int mhc_branch_norm_bwd(const void* dz, int dz_type, const void* y,
+                        const unsigned char* y_scales, const float* nw, int T, int hidden,
+                        float norm_eps, float* dy, float* dnw, void* work, size_t work_bytes,
+                        void* stream);
+int mhc_site_post_norm_bwd(const float* g, const void* x, const unsigned char* x_scales,
+                           const void* f, int f_type, const unsigned char* f_scales,
+                           const float* nw, const void* gate, int gate_type, int gate_rows,
+                           int gate_act, float alpha, const float* post, const float* comb, int T,
+                           int streams, int hidden, float norm_eps, float* dx, float* df,
+                           float* dpost, float* dcomb, float* dnw, float* dgate, void* work,
+                           size_t work_bytes, void* stream);
+
+/*
+ * 4-bit groups: the weights of a branch's products for decoding.
+ *
+ * A weight w [N][K], K a multiple of 32, in groups of G = 32, 64 or 128 consecutive
+ * columns of a row, KG = ceil(K/G) of them (the last may be short):
+ *   w[n][k] = scale[n][k/G] * (code[n][k] - zero[n][k/G])
+ *   scales [N][KG]   MHC_BF16 or MHC_F16
+ *   zeros  [N][KG]   one byte, 0 .. 15; NULL: 8 everywhere
+ *   codes  [N][P/2]  0 .. 15, P = K rounded up to 128.  Of the 64 bytes of 128 columns,
+ *                    byte 16 g + 4 b + e (g, b, e < 4) holds column 32 b + 8 g + e in its
+ *                    low half and the column 4 past it in its high half; zero past K
+ *
+ * mhc_q4_encode: w (MHC_F32 or MHC_BF16) into codes and bf16 scales.  With zeros NULL
+ *   scale = max|w| / 7 of the group and the codes are 1 .. 15; else, with lo = min(w, 0)
+ *   and hi = max(w, 0), scale = hi/15 - lo/15 and zero = -lo/scale, rounded.  The scale
+ *   is rounded to bf16 first (at least 2^-126), then code = w/scale + zero, each
+ *   rounded to nearest even, within the codes' range: what is off by rounding is at most
+ *   half a scale (but at a group's ends, where a scale rounded down may cut off up to
+ *   2^-9 of the range).  Infinities and NaN set no scale; an infinity takes the code at
+ *   its end of the range, a NaN the zero point.
+ * mhc_q4_decode: the values, fp32 [N][K] (exact).
+ * mhc_q4_matmul: out[m][n] = sum_k a[m][k] * w[n][k], out [M][N] of out_type MHC_F32 or
+ *   MHC_BF16 (rounded to nearest even).
+ *   a [M][K], a_type   MHC_F32 or MHC_BF16 with a_scales NULL; or MHC_I8 with a_scales
+ *     [M][K/32], value a * a_scales: the q and d of mhc_site_pre_zq8
+ *   Products are exact and summed in fp32 in an order fixed by the shape (int8: exactly
+ *   within 32 columns); a part of an fp32 value that is under 2^-126 may count as zero.  A
+ *   row of a with an infinity or a NaN gives a row that is not finite; other rows do not
+ *   see it.
+ *
+ * N <= 2^24, K <= 2^20, M <= 2^20, M * N < 2^31 (MHC_EUNSUPPORTED); K % 32 == 0
+ * (MHC_EALIGN); M = 0 does nothing.  Pointers are 16-byte aligned; outputs must not
+ * overlap inputs or each other.  No scratch.
+ */
+enum { MHC_F16 = 2, MHC_I8 = 3 }; /* beside MHC_F32 and MHC_BF16 */
+
+int mhc_q4_encode(const void* w, int w_type, int N, int K, int group, unsigned char* codes,
+                  void* scales, unsigned char* zeros, void* stream);
+int mhc_q4_decode(const unsigned char* codes, const void* scales, int scale_type,
+                  const unsigned char* zeros, int N, int K, int group, float* out,
+                  void* stream);
+int mhc_q4_matmul(const void* a, int a_type, const float* a_scales, const unsigned char* codes,
+                  const void* scales, int scale_type, const unsigned char* zeros, int M, int N,
+                  int K, int group, void* out, int out_type, void* stream);
+
 /* The argument checks of the calls above alone (no HIP call). */
 int mhc_f8_encode_check(const void* x, int x_type, int rows, int cols, int square,
                         const unsigned char* codes, const unsigned char* scales,
@@ -488,6 +598,32 @@ int mhc_site_pre_bwd_check(const void* x, const unsigned char* x_scales, const f
                            const float* dpost, const float* dcomb, const float* dx_in,
                            const float* dx, const float* dfn_w, const float* dscale,
                            const float* dbase, const void* work, size_t work_bytes);
+
+int mhc_branch_norm_check(const float* y, const float* nw, int T, int hidden, float norm_eps,
+                          const void* z, int z_type);
+int mhc_branch_norm_bwd_check(const void* dz, int dz_type, const void* y,
+                              const unsigned char* y_scales, const float* nw, int T, int hidden,
+                              float norm_eps, const float* dy, const float* dnw,
+                              const void* work, size_t work_bytes);
+int mhc_site_post_norm_check(const float* x, const void* f, int f_type, const float* nw,
+                             const void* gate, int gate_type, int gate_rows, int gate_act,
+                             float alpha, const float* post, const float* comb, int T,
+                             int streams, int hidden, float norm_eps, const float* x_out);
+int mhc_site_post_norm_bwd_check(const float* g, const void* x, const unsigned char* x_scales,
+                                 const void* f, int f_type, const unsigned char* f_scales,
+                                 const float* nw, const void* gate, int gate_type, int gate_rows,
+                                 int gate_act, float alpha, const float* post, const float* comb,
+                                 int T, int streams, int hidden, float norm_eps, const float* dx,
+                                 const float* df, const float* dpost, const float* dcomb,
+                                 const float* dnw, const float* dgate, const void* work,
+                                 size_t work_bytes);
+int mhc_q4_encode_check(const void* w, int w_type, int N, int K, int group,
+                        const unsigned char* codes, const void* scales,
+                        const unsigned char* zeros);
+int mhc_q4_matmul_check(const void* a, int a_type, const float* a_scales,
+                        const unsigned char* codes, const void* scales, int scale_type,
+                        const unsigned char* zeros, int M, int N, int K, int group,
+                        const void* out, int out_type);
 
 /* Static text for a return code (never NULL). */
 const char* mhc_status_string(int status);

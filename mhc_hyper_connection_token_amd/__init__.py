@@ -26,6 +26,10 @@ __all__ = ["site_pre", "site_post", "site_pre_zq8", "site_pre_check", "site_post
            "f8_encode", "f8_repack", "f8_decode", "f8_matmul", "f8_encode_check",
            "f8_matmul_check", "site_post_bwd", "site_post_bwd_check", "site_pre_bwd",
            "site_pre_bwd_check", "site_pre_bwd_work_bytes",
+           "branch_norm", "branch_norm_bwd", "site_post_norm", "site_post_norm_bwd",
+           "norm_bwd_work_bytes", "branch_norm_check", "branch_norm_bwd_check",
+           "site_post_norm_check", "site_post_norm_bwd_check",
+           "q4_encode", "q4_decode", "q4_matmul", "q4_encode_check", "q4_matmul_check",
            "workspace_bytes", "load_library", "MhcError", "LIB_PATH", "EXPORTED_SYMBOLS",
            "STATUS"]
 
@@ -45,7 +49,12 @@ EXPORTED_SYMBOLS = ("mhc_site_pre", "mhc_site_post", "mhc_site_pre_exact", "mhc_
                     "mhc_f8_encode", "mhc_f8_repack", "mhc_f8_decode", "mhc_f8_matmul",
                     "mhc_f8_encode_check", "mhc_f8_matmul_check", "mhc_site_post_bwd",
                     "mhc_site_post_bwd_check", "mhc_site_pre_bwd", "mhc_site_pre_bwd_check",
-                    "mhc_site_pre_bwd_work_bytes")
+                    "mhc_site_pre_bwd_work_bytes",
+                    "mhc_branch_norm", "mhc_branch_norm_check", "mhc_branch_norm_bwd",
+                    "mhc_branch_norm_bwd_check", "mhc_norm_bwd_work_bytes",
+                    "mhc_site_post_norm", "mhc_site_post_norm_check", "mhc_site_post_norm_bwd",
+                    "mhc_site_post_norm_bwd_check", "mhc_q4_encode", "mhc_q4_encode_check",
+                    "mhc_q4_decode", "mhc_q4_matmul", "mhc_q4_matmul_check")
 
 STATUS = {0: "MHC_OK", 1: "MHC_EINVAL", 2: "MHC_EALIGN", 3: "MHC_EUNSUPPORTED",
           4: "MHC_EHIP", 5: "MHC_EOVERLAP", 6: "MHC_ECAPTURE"}
@@ -156,6 +165,35 @@ def load_library() -> ctypes.CDLL:
     lib.mhc_site_pre_bwd_check.restype = i
     lib.mhc_site_pre_bwd_work_bytes.argtypes = [i, i, i]
     lib.mhc_site_pre_bwd_work_bytes.restype = sz
+    lib.mhc_branch_norm.argtypes = [vp, vp, i, i, fl, vp, i, vp]
+    lib.mhc_branch_norm.restype = i
+    lib.mhc_branch_norm_check.argtypes = [vp, vp, i, i, fl, vp, i]
+    lib.mhc_branch_norm_check.restype = i
+    lib.mhc_norm_bwd_work_bytes.argtypes = [i, i]
+    lib.mhc_norm_bwd_work_bytes.restype = sz
+    lib.mhc_branch_norm_bwd.argtypes = [vp, i, vp, vp, vp, i, i, fl, vp, vp, vp, sz, vp]
+    lib.mhc_branch_norm_bwd.restype = i
+    lib.mhc_branch_norm_bwd_check.argtypes = [vp, i, vp, vp, vp, i, i, fl, vp, vp, vp, sz]
+    lib.mhc_branch_norm_bwd_check.restype = i
+    lib.mhc_site_post_norm.argtypes = [vp, vp, i, vp, vp, i, i, i, fl, vp, vp, i, i, i, fl, vp, vp]
+    lib.mhc_site_post_norm.restype = i
+    lib.mhc_site_post_norm_check.argtypes = lib.mhc_site_post_norm.argtypes[:-1]
+    lib.mhc_site_post_norm_check.restype = i
+    lib.mhc_site_post_norm_bwd.argtypes = [vp, vp, vp, vp, i, vp, vp, vp, i, i, i, fl, vp, vp, i,
+                                           i, i, fl] + [vp] * 7 + [sz, vp]
+    lib.mhc_site_post_norm_bwd.restype = i
+    lib.mhc_site_post_norm_bwd_check.argtypes = lib.mhc_site_post_norm_bwd.argtypes[:-1]
+    lib.mhc_site_post_norm_bwd_check.restype = i
+    lib.mhc_q4_encode.argtypes = [vp, i, i, i, i, vp, vp, vp, vp]
+    lib.mhc_q4_encode.restype = i
+    lib.mhc_q4_encode_check.argtypes = [vp, i, i, i, i, vp, vp, vp]
+    lib.mhc_q4_encode_check.restype = i
+    lib.mhc_q4_decode.argtypes = [vp, vp, i, vp, i, i, i, vp, vp]
+    lib.mhc_q4_decode.restype = i
+    lib.mhc_q4_matmul.argtypes = [vp, i, vp, vp, vp, i, vp, i, i, i, i, vp, i, vp]
+    lib.mhc_q4_matmul.restype = i
+    lib.mhc_q4_matmul_check.argtypes = lib.mhc_q4_matmul.argtypes[:-1]
+    lib.mhc_q4_matmul_check.restype = i
     if lib.mhc_workspace_struct_bytes() != ctypes.sizeof(_WsStruct):
         raise RuntimeError("mhc_workspace layout of the library and the binding differ")
     _lib = lib
@@ -752,6 +790,304 @@ def site_pre_bwd_check(x_ptr, x_scales_ptr, fn_w_ptr, scale_ptr, base_ptr, T, S,
         x_ptr, x_scales_ptr, fn_w_ptr, scale_ptr, base_ptr, T, S, H, iters, float(eps), dy_ptr,
         dpre_ptr, dpost_ptr, dcomb_ptr, dx_in_ptr, dx_ptr, dfn_w_ptr, dscale_ptr, dbase_ptr,
         work_ptr, work_bytes)
+
+
+_GATE_ACTS = {None: 0, "sigmoid": 1, "silu": 2}
+
+
+def _typed(t, name, shape=None):
+    """Address of a contiguous float32 or bfloat16 GPU tensor, and 1 where it is bfloat16."""
+    import torch
+    dtype = getattr(t, "dtype", None)
+    if dtype == torch.bfloat16:
+        return _gpu(t, name, dtype, shape), 1
+    if isinstance(t, torch.Tensor) and dtype != torch.float32:
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    return _gpu(t, name, torch.float32, shape), 0
+
+
+def _gate(gate, act, T, H):
+    """Address, type, rows and activation of a gate [H] or [T, H], or of none."""
+    if act not in _GATE_ACTS:
+        raise ValueError('gate_act must be None, "sigmoid" or "silu"')
+    if gate is None:
+        if act is not None:
+            raise ValueError("gate_act without a gate")
+        return None, 0, 1, 0
+    rows = (H,) if gate.dim() == 1 else (T, H)
+    pg, bf16 = _typed(gate, "gate", rows)
+    return pg, bf16, 1 if gate.dim() == 1 else T, _GATE_ACTS[act]
+
+
+def branch_norm(y, nw, eps: float = 1e-5, *, dtype=None, out=None, stream=None):
+    """Norm before a branch: y [T,H] / sqrt(mean y^2 + eps) * nw [H], as float32 (default)
+    or bfloat16.  `out` may supply the result; its dtype is then the norm's.
+    (site_pre_zq8 has the norm with the branch's int8 codes.)"""
+    import torch
+    if stream is not None:
+        return _on(stream, y.device, branch_norm, y, nw, eps, dtype=dtype, out=out)
+    if y.dim() != 2:
+        raise ValueError("y must be [T, H]")
+    T, H = y.shape
+    dtype = out.dtype if out is not None else dtype if dtype is not None else torch.float32
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("the norm is float32 or bfloat16")
+    f32 = torch.float32
+    py, pn = _gpu(y, "y", f32), _gpu(nw, "nw", f32, (H,))
+    if out is None:
+        out = torch.empty((T, H), device=y.device, dtype=dtype)
+        po = out.data_ptr()
+    else:
+        po = _gpu(out, "out", dtype, (T, H))
+    _call("mhc_branch_norm", y.get_device(),
+          (py, pn, T, H, float(eps), po, int(dtype == torch.bfloat16)), (nw, out))
+    return out
+
+
+def norm_bwd_work_bytes(T: int, hidden: int) -> int:
+    """Bytes of device scratch a branch_norm_bwd or site_post_norm_bwd call needs."""
+    return int(load_library().mhc_norm_bwd_work_bytes(T, hidden))
+
+
+def _norm_work(work, T, H, device):
+    import torch
+    if work is None:
+        work = torch.empty(norm_bwd_work_bytes(T, H), device=device, dtype=torch.uint8)
+    return work, _gpu(work, "work", torch.uint8)
+
+
+def branch_norm_bwd(dz, y, nw, eps: float = 1e-5, *, out=None, work=None, stream=None):
+    """Gradient of branch_norm: from dz [T,H] (float32 or bfloat16) and the forward's y
+    [T,H] (a float32 tensor or the (codes, scales) pair that f8_encode(y) returned).
+    Returns (dy [T,H], dnw [H]) in float32; `out` may supply that pair.  `work` is a uint8
+    tensor of at least norm_bwd_work_bytes bytes (allocated per call when not given)."""
+    import torch
+    if stream is not None:
+        return _on(stream, dz.device, branch_norm_bwd, dz, y, nw, eps, out=out, work=work)
+    if dz.dim() != 2:
+        raise ValueError("dz must be [T, H]")
+    T, H = dz.shape
+    f32 = torch.float32
+    pz, z_bf16 = _typed(dz, "dz")
+    py, pys, ty = _kept(y, "y", (T,), H)
+    out, po = _outputs(out, ("dy", "dnw"), ((T, H), (H,)), (f32, f32), dz.device)
+    work, pw = _norm_work(work, T, H, dz.device)
+    _call("mhc_branch_norm_bwd", dz.get_device(),
+          (pz, z_bf16, py, pys, _gpu(nw, "nw", f32, (H,)), T, H, float(eps), *po, pw,
+           work.numel()), (*ty, nw, *out, work))
+    return out
+
+
+def site_post_norm(x, f, nw, post, comb, eps: float = 1e-5, *, gate=None, gate_act=None,
+                   alpha: float = 1.0, out=None, stream=None):
+    """site_post of h = alpha * a(gate) * f / sqrt(mean f^2 + eps) * nw: the norm behind a
+    branch, its gate and the residual scale, in the post mix.  x [T,S,H], f [T,H] (float32 or
+    bfloat16), nw [H], post [T,S], comb [T,S,S]; gate [H] or [T,H] (float32 or bfloat16) or
+    None; gate_act None (a(gate) = gate), "sigmoid" or "silu".  Returns x' [T,S,H]; `out` may
+    supply it."""
+    import torch
+    if stream is not None:
+        return _on(stream, x.device, site_post_norm, x, f, nw, post, comb, eps, gate=gate,
+                   gate_act=gate_act, alpha=alpha, out=out)
+    if x.dim() != 3:
+        raise ValueError("x must be [T, S, H]")
+    T, S, H = x.shape
+    f32 = torch.float32
+    px = _gpu(x, "x", f32)
+    if out is None:
+        out = torch.empty((T, S, H), device=x.device, dtype=f32)
+        po = out.data_ptr()
+    else:
+        po = _gpu(out, "out", f32, (T, S, H))
+    _call("mhc_site_post_norm", x.get_device(),
+          (px, *_typed(f, "f", (T, H)), _gpu(nw, "nw", f32, (H,)), *_gate(gate, gate_act, T, H),
+           float(alpha), _gpu(post, "post", f32, (T, S)), _gpu(comb, "comb", f32, (T, S, S)), T,
+           S, H, float(eps), po), (f, nw, gate, post, comb, out))
+    return out
+
+
+def site_post_norm_bwd(g, x, f, nw, post, comb, eps: float = 1e-5, *, gate=None, gate_act=None,
+                       alpha: float = 1.0, out=None, work=None, stream=None):
+    """Gradient of site_post_norm: from g [T,S,H] = dL/dx' and the forward's operands; x and f
+    may be the (codes, scales) pairs that f8_encode(x), f8_encode(f) returned.  Returns
+    (dx [T,S,H], df [T,H], dpost [T,S], dcomb [T,S,S], dnw [H], dgate), all float32, dgate of
+    the gate's shape or None; `out` may supply that tuple.  `work` is a uint8 tensor of at
+    least norm_bwd_work_bytes bytes (allocated per call when not given)."""
+    import torch
+    if stream is not None:
+        return _on(stream, g.device, site_post_norm_bwd, g, x, f, nw, post, comb, eps, gate=gate,
+                   gate_act=gate_act, alpha=alpha, out=out, work=work)
+    if g.dim() != 3:
+        raise ValueError("g must be [T, S, H]")
+    T, S, H = g.shape
+    f32 = torch.float32
+    pg = _gpu(g, "g", f32)
+    px, pxs, tx = _kept(x, "x", (T, S), H)
+    if isinstance(f, (tuple, list)):
+        pf, pfs, tf = _kept(f, "f", (T,), H)
+        f_bf16 = 0
+    else:
+        (pf, f_bf16), pfs, tf = _typed(f, "f", (T, H)), None, (f,)
+    how = _gate(gate, gate_act, T, H)
+    names = ("dx", "df", "dpost", "dcomb", "dnw")
+    shapes = ((T, S, H), (T, H), (T, S), (T, S, S), (H,))
+    if gate is not None:
+        names, shapes = names + ("dgate",), shapes + (tuple(gate.shape),)
+    elif out is not None:
+        if len(out) != 6 or out[5] is not None:
+            raise ValueError("out must hold 5 tensors and None, the gradient of no gate")
+        out = out[:5]
+    out, po = _outputs(out, names, shapes, (f32,) * len(shapes), g.device)
+    if gate is None:
+        out, po = (*out, None), [*po, None]
+    work, pw = _norm_work(work, T, H, g.device)
+    _call("mhc_site_post_norm_bwd", g.get_device(),
+          (pg, px, pxs, pf, f_bf16, pfs, _gpu(nw, "nw", f32, (H,)), *how, float(alpha),
+           _gpu(post, "post", f32, (T, S)), _gpu(comb, "comb", f32, (T, S, S)), T, S, H,
+           float(eps), *po, pw, work.numel()),
+          (*tx, *tf, nw, gate, post, comb, *out, work))
+    return out
+
+
+def branch_norm_check(y_ptr, nw_ptr, T, H, eps, z_ptr, z_type) -> int:
+    """The library's host-side argument check of mhc_branch_norm on raw addresses."""
+    return load_library().mhc_branch_norm_check(y_ptr, nw_ptr, T, H, float(eps), z_ptr, z_type)
+
+
+def branch_norm_bwd_check(dz_ptr, dz_type, y_ptr, y_scales_ptr, nw_ptr, T, H, eps, dy_ptr,
+                          dnw_ptr, work_ptr, work_bytes) -> int:
+    """The library's host-side argument check of mhc_branch_norm_bwd on raw addresses."""
+    return load_library().mhc_branch_norm_bwd_check(dz_ptr, dz_type, y_ptr, y_scales_ptr, nw_ptr,
+                                                    T, H, float(eps), dy_ptr, dnw_ptr, work_ptr,
+                                                    work_bytes)
+
+
+def site_post_norm_check(x_ptr, f_ptr, f_type, nw_ptr, gate_ptr, gate_type, gate_rows, gate_act,
+                         alpha, post_ptr, comb_ptr, T, S, H, eps, x_out_ptr) -> int:
+    """The library's host-side argument check of mhc_site_post_norm on raw addresses."""
+    return load_library().mhc_site_post_norm_check(
+        x_ptr, f_ptr, f_type, nw_ptr, gate_ptr, gate_type, gate_rows, gate_act, float(alpha),
+        post_ptr, comb_ptr, T, S, H, float(eps), x_out_ptr)
+
+
+def site_post_norm_bwd_check(g_ptr, x_ptr, x_scales_ptr, f_ptr, f_type, f_scales_ptr, nw_ptr,
+                             gate_ptr, gate_type, gate_rows, gate_act, alpha, post_ptr, comb_ptr,
+                             T, S, H, eps, dx_ptr, df_ptr, dpost_ptr, dcomb_ptr, dnw_ptr,
+                             dgate_ptr, work_ptr, work_bytes) -> int:
+    """The library's host-side argument check of mhc_site_post_norm_bwd on raw addresses."""
+    return load_library().mhc_site_post_norm_bwd_check(
+        g_ptr, x_ptr, x_scales_ptr, f_ptr, f_type, f_scales_ptr, nw_ptr, gate_ptr, gate_type,
+        gate_rows, gate_act, float(alpha), post_ptr, comb_ptr, T, S, H, float(eps), dx_ptr,
+        df_ptr, dpost_ptr, dcomb_ptr, dnw_ptr, dgate_ptr, work_ptr, work_bytes)
+
+
+def _q4_weight(codes, scales, zeros, K):
+    """Addresses of a 4-bit weight, its scale type (C ABI), rows and group size."""
+    import torch
+    if codes.dim() != 2 or scales.dim() != 2:
+        raise ValueError("codes must be [N, P/2] and scales [N, groups]")
+    if K < 1 or K % 32:
+        raise ValueError("K must be a multiple of 32")
+    N, kg = scales.shape
+    # the group size that gives this many groups (where two do, there is one group)
+    group = next((g for g in (128, 64, 32) if -(-K // g) == kg), None)
+    if group is None:
+        raise ValueError(f"scales has {kg} groups a row: none of 32, 64 and 128 columns gives "
+                         f"that at K = {K}")
+    if scales.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("scales must be bfloat16 or float16")
+    pc = _gpu(codes, "codes", torch.uint8, (N, _blocks(K) * 64))
+    ps = _gpu(scales, "scales", scales.dtype)
+    pz = None if zeros is None else _gpu(zeros, "zeros", torch.uint8, (N, kg))
+    return pc, ps, 1 if scales.dtype == torch.bfloat16 else 2, pz, N, group
+
+
+def q4_encode(w, *, group: int = 128, zeros: bool = False, out=None, stream=None):
+    """4-bit groups of a weight w [N, K] (float32 or bfloat16; include/mhc.h, "4-bit groups"):
+    (codes [N, P/2] uint8, scales [N, ceil(K/group)] bfloat16), P = K rounded up to 128; with
+    zeros=True a zero point for each group as well, uint8 like the scales.  group is 32, 64
+    or 128.  `out` may supply the tuple that the call returns."""
+    import torch
+    if not isinstance(w, torch.Tensor):
+        raise TypeError("w must be a torch.Tensor")
+    if stream is not None:
+        return _on(stream, w.device, q4_encode, w, group=group, zeros=zeros, out=out)
+    if w.dim() != 2:
+        raise ValueError("w must be [N, K]")
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    pw, bf16 = _typed(w, "w")
+    N, K = w.shape
+    kg = -(-K // group)
+    u8 = torch.uint8
+    shapes = ((N, _blocks(K) * 64), (N, kg)) + (((N, kg),) if zeros else ())
+    out, po = _outputs(out, ("codes", "scales", "zeros"), shapes,
+                       (u8, torch.bfloat16, u8)[:len(shapes)], w.device)
+    _call("mhc_q4_encode", w.get_device(),
+          (pw, bf16, N, K, group, *po, *(() if zeros else (None,))), out)
+    return out
+
+
+def q4_decode(codes, scales, zeros=None, *, cols: int, out=None, stream=None):
+    """The float32 values [N, cols] of a weight in 4-bit groups."""
+    import torch
+    if stream is not None:
+        return _on(stream, codes.device, q4_decode, codes, scales, zeros, cols=cols, out=out)
+    pc, ps, kind, pz, N, group = _q4_weight(codes, scales, zeros, cols)
+    if out is None:
+        out = torch.empty((N, cols), device=codes.device, dtype=torch.float32)
+    _call("mhc_q4_decode", codes.get_device(),
+          (pc, ps, kind, pz, N, cols, group, _gpu(out, "out", torch.float32, (N, cols))),
+          (scales, zeros, out))
+    return out
+
+
+def q4_matmul(a, codes, scales, zeros=None, *, dtype=None, out=None, stream=None):
+    """a [M, K] times a weight w [N, K] in 4-bit groups, transposed: [M, N] float32 (default)
+    or bfloat16.  a is float32, bfloat16, or the pair (q [M, K] int8, d [M, K/32] float32) of
+    site_pre_zq8.  The weight is what q4_encode returned (its scales may also be float16).
+    `out` may supply the result; its dtype is then the product's."""
+    import torch
+    pair = isinstance(a, (tuple, list))
+    q = a[0] if pair else a
+    if stream is not None:
+        return _on(stream, q.device, q4_matmul, a, codes, scales, zeros, dtype=dtype, out=out)
+    if q.dim() != 2:
+        raise ValueError("a must be [M, K]")
+    M, K = q.shape
+    dtype = out.dtype if out is not None else dtype if dtype is not None else torch.float32
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("the product is float32 or bfloat16")
+    pc, ps, kind, pz, N, group = _q4_weight(codes, scales, zeros, K)
+    if pair:
+        pa, a_type = _gpu(q, "q", torch.int8), 3
+        pd = _gpu(a[1], "d", torch.float32, (M, K // 32))
+        others = (a[1], codes, scales, zeros)
+    else:
+        (pa, a_type), pd, others = _typed(a, "a"), None, (codes, scales, zeros)
+    if out is None:
+        out = torch.empty((M, N), device=q.device, dtype=dtype)
+        po = out.data_ptr()
+    else:
+        po = _gpu(out, "out", dtype, (M, N))
+    _call("mhc_q4_matmul", q.get_device(),
+          (pa, a_type, pd, pc, ps, kind, pz, M, N, K, group, po, int(dtype == torch.bfloat16)),
+          (*others, out))
+    return out
+
+
+def q4_encode_check(w_ptr, w_type, N, K, group, codes_ptr, scales_ptr, zeros_ptr) -> int:
+    """The library's host-side argument check of mhc_q4_encode on raw addresses."""
+    return load_library().mhc_q4_encode_check(w_ptr, w_type, N, K, group, codes_ptr, scales_ptr,
+                                              zeros_ptr)
+
+
+def q4_matmul_check(a_ptr, a_type, a_scales_ptr, codes_ptr, scales_ptr, scale_type, zeros_ptr, M,
+                    N, K, group, out_ptr, out_type) -> int:
+    """The library's host-side argument check of mhc_q4_matmul on raw addresses."""
+    return load_library().mhc_q4_matmul_check(a_ptr, a_type, a_scales_ptr, codes_ptr, scales_ptr,
+                                              scale_type, zeros_ptr, M, N, K, group, out_ptr,
+                                              out_type)
 
 
 def bandwidth_probe(src, dst, copy: bool, *, stream=None):

@@ -119,6 +119,27 @@ hipError_t launch_f8_matmul(const unsigned char* a, const unsigned char* as,
                             const unsigned char* b, const unsigned char* bs, bool square, int M,
                             int N, int K, void* out, bool bf16, hipStream_t st);
 
+// 4-bit groups (mhc_q4.h): a scale (two bytes), and with zeros a zero point, per `group`
+// columns; encode writes bf16 scales.
+hipError_t launch_q4_encode(const void* w, bool bf16, int N, int K, int group,
+                            unsigned char* codes, void* scales, unsigned char* zeros,
+                            hipStream_t st);
+hipError_t launch_q4_decode(const unsigned char* codes, const void* scales, bool f16,
+                            const unsigned char* zeros, int N, int K, int group, float* out,
+                            hipStream_t st);
+// out[M][N] (fp32 or bf16) = a[M][K] * W[N][K]^T; a_kind 0 fp32, 1 bf16, 2 int8 with
+// a_scales [M][K/32].
+struct Q4Matmul {
+  const void* a;
+  const float* a_scales;
+  const unsigned char* codes;
+  const void* scales;
+  const unsigned char* zeros;
+  void* out;
+  int a_kind, f16_scales, bf16_out;
+};
+hipError_t launch_q4_matmul(const Q4Matmul& q, int M, int N, int K, int group, hipStream_t st);
+
 // Gradient of the post mix; x and f are 8-bit blocks where their scales are given.
 struct PostBwd {
   const float* g;

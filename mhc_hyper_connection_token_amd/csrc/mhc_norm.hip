@@ -1,0 +1,191 @@
+// mhc_norm.hip -- the norm before a branch, and the post mix with the norm behind it:
+//   branch_norm     z[t,i] = y[t,i] * r_t * nw[i],  r_t = 1/sqrt(mean_i y[t,i]^2 + eps)
+//   site_post_norm  h[t,i] = alpha * a(gate) * f[t,i] * r_t * nw[i]   (r_t of f)
+//                   x'[t,k,i] = post[t,k] * h[t,i] + sum_j comb[t,j,k] * x[t,j,i]
+// Both are one pass over memory: a token's row stays in the registers of the threads
+// that sum its squares until r_t is known.  HBM-bound.
+#include "mhc_norm.h"
+
+namespace mhc {
+
+// ---------------------------------------------------------------- norm before a branch
+// W waves hold a token's row, Q quads a thread; with W = 1 a block has four tokens.
+template <int W, int Q>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void branch_norm_kernel(
+    const float* __restrict__ y, const float* __restrict__ nw, int T, int HQ, float eps,
+    void* __restrict__ z, int bf16) {
+  constexpr int NT = 64 * W;
+  const int wave = threadIdx.x >> 6;
+  const int t = W == 1 ? blockIdx.x * 4 + wave : blockIdx.x;
+  const int tid = W == 1 ? threadIdx.x & 63 : threadIdx.x;
+  if (W == 1 && t >= T) return;
+  float4 v[Q];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const int q = tid + NT * i;
+    v[i] = q < HQ ? nt_load4(y + ((size_t)t * HQ + q) * 4) : zero4();
+  }
+#pragma unroll
+  for (int i = 0; i < Q; ++i) ss = sq4(v[i], ss);
+  ss = wave_total(ss);
+  if constexpr (W > 1) {
+    __shared__ float part[W];
+    if ((threadIdx.x & 63) == 0) part[wave] = ss;
+    __syncthreads();
+    ss = part[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) ss += part[w];
+  }
+  const float r = rms_inverse(ss, 4 * HQ, eps);
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const int q = tid + NT * i;
+    if (q >= HQ) break;
+    const float4 o = zq8_norm(v[i], r, reinterpret_cast<const float4*>(nw)[q]);
+    if (bf16)
+      reinterpret_cast<uintx2*>(z)[(size_t)t * HQ + q] = bf16_quad(o);
+    else
+      reinterpret_cast<float4*>(z)[(size_t)t * HQ + q] = o;
+  }
+}
+
+hipError_t launch_branch_norm(const float* y, const float* nw, int T, int H, float eps, void* z,
+                              bool bf16, hipStream_t st) {
+  const int HQ = H / 4;
+#define MHC_NORM(W, Q)                                                                        \
+  hipLaunchKernelGGL((branch_norm_kernel<W, Q>), dim3((unsigned)(W == 1 ? (T + 3) / 4 : T)),   \
+                     dim3(W == 1 ? 256 : 64 * W), 0, st, y, nw, T, HQ, eps, z, (int)bf16)
+  if (HQ <= 64)
+    MHC_NORM(1, 1);
+  else if (HQ <= 256)
+    MHC_NORM(1, 4);
+  else if (HQ <= 1024)
+    MHC_NORM(4, 4);
+  else
+    MHC_NORM(8, 8);
+#undef MHC_NORM
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- post mix with the norm
+// The branch's quad behind its norm, gate and scale.
+__device__ __forceinline__ float4 branch_out(float4 f, float r, float4 w, uintx4 graw,
+                                             const PostNorm& p) {
+  float4 h = mul4(scale4(f, p.alpha * r), w);
+  if (p.gate) {
+    float4 a, s;
+    gate_quad<false>(raw_values(graw, p.gate_kind), p.gate_act, a, s);
+    h = mul4(h, a);
+  }
+  return h;
+}
+
+template <int S>
+__device__ __forceinline__ void mix_store(const float* pk, const float (*ck)[S], const float4* xv,
+                                          float4 h, float* out, size_t t, int HQ, int q) {
+  float4* o = reinterpret_cast<float4*>(out) + t * S * HQ + q;
+#pragma unroll
+  for (int k = 0; k < S; ++k) o[(size_t)k * HQ] = post_mix4<S>(pk[k], &ck[0][k], S, xv, h, S);
+}
+
+// A block takes NT*Q quads of a token (all HQ of them where PARTS is false: then the row of
+// f that it sums is the row that it holds).  With PARTS the blocks of a token each sum
+// the whole row: for few tokens, and for rows that would not leave room for x.
+template <int S, int NT, int Q, bool PARTS>
+__global__ __launch_bounds__(NT) void post_norm_kernel(PostNorm p, int HQ, int parts, float eps) {
+  constexpr int NW = NT / 64;
+  const int part = PARTS ? blockIdx.x % parts : 0;
+  const size_t t = PARTS ? blockIdx.x / parts : blockIdx.x;
+  const int q0 = part * NT * Q + threadIdx.x;
+  float pk[S], ck[S][S];
+#pragma unroll
+  for (int k = 0; k < S; ++k) pk[k] = p.post[t * S + k];
+#pragma unroll
+  for (int j = 0; j < S; ++j)
+#pragma unroll
+    for (int k = 0; k < S; ++k) ck[j][k] = p.comb[t * S * S + j * S + k];
+  uintx4 fv[Q], gv[Q];
+  float4 xv[Q][S];
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const int q = q0 + NT * i;
+    fv[i] = gv[i] = uintx4{0u, 0u, 0u, 0u};
+    if (q < HQ) fv[i] = load_raw(p.f, nullptr, p.f_kind, t, HQ, 0, q);
+  }
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const int q = q0 + NT * i;
+    if (q < HQ) {
+#pragma unroll
+      for (int j = 0; j < S; ++j) xv[i][j] = nt_load4(p.x + ((t * S + j) * HQ + q) * 4);
+      if (p.gate) gv[i] = load_raw(p.gate, nullptr, p.gate_kind, p.gate_rows ? t : 0, HQ, 0, q);
+    }
+  }
+  float ss = 0.f;
+  if constexpr (PARTS) {
+    for (int q = threadIdx.x; q < HQ; q += NT)
+      ss = sq4(raw_values(load_raw(p.f, nullptr, p.f_kind, t, HQ, 0, q), p.f_kind), ss);
+  } else {
+#pragma unroll
+    for (int i = 0; i < Q; ++i) ss = sq4(raw_values(fv[i], p.f_kind), ss);
+  }
+  ss = wave_total(ss);
+  if constexpr (NW > 1) {
+    __shared__ float sums[NW];
+    if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = ss;
+    __syncthreads();
+    ss = sums[0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) ss += sums[w];
+  }
+  const float r = rms_inverse(ss, 4 * HQ, eps);
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const int q = q0 + NT * i;
+    if (q >= HQ) break;
+    const float4 h = branch_out(raw_values(fv[i], p.f_kind), r,
+                                reinterpret_cast<const float4*>(p.nw)[q], gv[i], p);
+    mix_store<S>(pk, ck, xv[i], h, p.x_out, t, HQ, q);
+  }
+}
+
+namespace {
+template <int S, int NT, int Q, bool PARTS>
+void launch_post_norm_at(const PostNorm& p, int T, int HQ, float eps, hipStream_t st) {
+  const int parts = PARTS ? (HQ + NT * Q - 1) / (NT * Q) : 1;
+  hipLaunchKernelGGL((post_norm_kernel<S, NT, Q, PARTS>), dim3((unsigned)T * parts), dim3(NT), 0,
+                     st, p, HQ, parts, eps);
+}
+template <int S>
+void launch_post_norm_s(const PostNorm& p, int T, int HQ, float eps, hipStream_t st) {
+  if (HQ <= 64)
+    launch_post_norm_at<S, 64, 1, false>(p, T, HQ, eps, st);
+  else if (HQ <= 256)
+    launch_post_norm_at<S, 256, 1, false>(p, T, HQ, eps, st);
+  else if (T <= 128)
+    launch_post_norm_at<S, 256, 1, true>(p, T, HQ, eps, st);
+  else if (HQ <= 1024)
+    launch_post_norm_at<S, 512, 2, false>(p, T, HQ, eps, st);
+  else if (HQ <= 2048)
+    launch_post_norm_at<S, 1024, 2, false>(p, T, HQ, eps, st);
+  else
+    launch_post_norm_at<S, 1024, 2, true>(p, T, HQ, eps, st);
+}
+}  // namespace
+
+hipError_t launch_post_norm(const PostNorm& p, int T, int S, int H, float eps, hipStream_t st) {
+  switch (S) {
+#define MHC_S(SS)                                  \
+  case SS:                                         \
+    launch_post_norm_s<SS>(p, T, H / 4, eps, st);   \
+    break;
+    MHC_S(1) MHC_S(2) MHC_S(3) MHC_S(4) MHC_S(5) MHC_S(6) MHC_S(7) MHC_S(8)
+#undef MHC_S
+    default:
+      return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace mhc

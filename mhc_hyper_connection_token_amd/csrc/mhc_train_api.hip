@@ -6,9 +6,14 @@
 #include "mhc_checks.h"
 #include "mhc_kernels.h"
 
+using mhc::blocks_of;
+using mhc::check_apart;
 using mhc::check_ptr;
+using mhc::check_ptrs;
 using mhc::check_shape;
-using mhc::overlaps;
+using mhc::kept_span;
+using mhc::Pair;
+using mhc::pair_span;
 using mhc::Span;
 using mhc::span;
 
@@ -17,50 +22,12 @@ namespace {
 constexpr long kMaxF8Blocks = 1L << 28;  // bounds the launch grids
 constexpr int kMaxF8Cols = 1 << 28;
 
-size_t blocks_of(size_t n) { return (n + 127) / 128; }
-
 int check_matrix(int rows, int cols) {
   if (rows < 0 || cols < 1) return MHC_EINVAL;
   if (cols % 4 != 0) return MHC_EALIGN;
   if (cols > kMaxF8Cols || (long)rows * (long)blocks_of(cols) > kMaxF8Blocks)
     return MHC_EUNSUPPORTED;
   return MHC_OK;
-}
-
-// The spans of a codes / scales pair; empty ones for a null pointer.
-struct Pair {
-  Span codes, scales;
-};
-Pair pair_span(const void* codes, const void* scales, size_t rows, size_t cols, bool square) {
-  if (!codes) return Pair{span(nullptr, 0), span(nullptr, 0)};
-  const size_t kb = blocks_of(cols);
-  return Pair{span(codes, rows * kb * 128),
-              span(scales, (square ? blocks_of(rows) : rows) * kb)};
-}
-
-// Each of out[] apart from every in[] and from the other outputs.
-int check_apart(const Span* out, int no, const Span* in, int ni) {
-  for (int i = 0; i < no; ++i) {
-    for (int k = 0; k < ni; ++k)
-      if (overlaps(out[i], in[k])) return MHC_EOVERLAP;
-    for (int k = i + 1; k < no; ++k)
-      if (overlaps(out[i], out[k])) return MHC_EOVERLAP;
-  }
-  return MHC_OK;
-}
-
-int check_ptrs(const void* const* ptrs, int n) {
-  for (int i = 0; i < n; ++i)
-    if (!ptrs[i]) return MHC_EINVAL;
-  for (int i = 0; i < n; ++i)
-    if (int rc = check_ptr(ptrs[i])) return rc;
-  return MHC_OK;
-}
-
-// Span of [rows][H] kept in fp32, or as codes where scales are given.
-Pair kept_span(const void* p, const unsigned char* scales, size_t rows, size_t H) {
-  if (scales) return pair_span(p, scales, rows, H, false);
-  return Pair{span(p, rows * H * 4), span(nullptr, 0)};
 }
 
 int status(hipError_t e) { return e == hipSuccess ? MHC_OK : MHC_EHIP; }
