@@ -7,9 +7,10 @@
 //   int8 codes with a scale per 32 columns: v_mfma_i32_16x16x32_i8, exact per block of 32.
 // The sums of a, which the zero points multiply, come from the same instruction with a
 // column operand of ones: they lie where the products lie.
-#include "mhc_q4.h"
+#include <type_traits>
 
 #include "mhc_kernels.h"
+#include "mhc_q4.h"
 
 namespace mhc {
 
@@ -47,27 +48,6 @@ __device__ __forceinline__ Octet<A> load_octet(const unsigned char* p, bool in) 
   return o;
 }
 
-// The top eight significant bits of eight fp32 values as bf16, and what they leave.
-__device__ __forceinline__ bf16x8 take_plane(floatx4 (&v)[2]) {
-  unsigned u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const unsigned lo = __float_as_uint(v[i >> 1][2 * (i & 1)]);
-    const unsigned hi = __float_as_uint(v[i >> 1][2 * (i & 1) + 1]);
-    u[i] = __builtin_amdgcn_perm(hi, lo, 0x07060302);
-    v[i >> 1][2 * (i & 1)] -= __uint_as_float(lo & 0xffff0000u);
-    v[i >> 1][2 * (i & 1) + 1] -= __uint_as_float(hi & 0xffff0000u);
-  }
-  bf16x8 r;
-  __builtin_memcpy(&r, u, 16);
-  return r;
-}
-
-template <int A>
-constexpr int planes() {
-  return A == kActF32 ? 3 : 1;
-}
-
 struct Q4Args {
   const unsigned char* a;
   const float* ad;  // scales of int8 activations, [M][K/32]
@@ -78,176 +58,787 @@ struct Q4Args {
   int M, N, K, KG, f16, bf16_out;
 };
 
+
+__device__ __forceinline__ void octet_values(const Octet<kActF32>& o, float* v) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = o.v[e >> 2][e & 3];
+}
+__device__ __forceinline__ void octet_values(const Octet<kActBF16>& o, float* v) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = __uint_as_float((unsigned)o.v[e] << 16);
+    v[2 * e + 1] = __uint_as_float((unsigned)o.v[e] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ void store_one(const Q4Args& p, size_t at, float v) {
+  if (p.bf16_out)
+    static_cast<__hip_bfloat16*>(p.out)[at] = __float2bfloat16(v);
+  else
+    static_cast<float*>(p.out)[at] = v;
+}
+
 }  // namespace
 
-// 16*MT rows of a and 16*NF columns n a block; its W waves take chunks of U times 128
-// columns of the depth in turn, and their sums are added in wave order through LDS.
-template <int A, int GS, int MT, int NF, int W, int U>
-__global__ __launch_bounds__(64 * W) void q4_matmul_kernel(Q4Args p) {
-  constexpr int PL = planes<A>(), GB = 1 << GS;  // blocks of 32 a group
-  __shared__ floatx4 part[W][MT * NF][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 16 * NF, m0 = blockIdx.y * 16 * MT;
-  const int KB = p.K / kQ4Block, SB = (p.K + 127) / 128;
-  // rows past the end read the last row; their results are not stored
-  const unsigned char *crow[NF], *arow[MT];
-  size_t srow[NF];
+// ---------------------------------------------------------------- one row
+// A lane holds the activations of 32 columns (an octet in each of a superblock's four
+// blocks) and meets the rows of the weight with them, 16 bytes of each: R rows at a time,
+// `iters` times, the next R on their way.  A wave's 64 lanes cover 2048 columns; the block's
+// W waves are KS slices of the depth times W / KS runs of R * iters rows, whose sums meet in
+// LDS.
+constexpr int kVectorRows = 64;  // rows of a wave at most
+
+template <int A, int GS, int R, int W>
+__global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int iters) {
+  constexpr int GB = 1 << GS, NG = 4 / GB;  // blocks of 32 a group, groups in a superblock
+  __shared__ float part[W][kVectorRows];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int KB = p.K / kQ4Block, SB = (p.K + 127) / 128, g = lane & 3;
+  const int slice = wave % KS, runs = W / KS, rows = R * iters;
+  const int n0 = (blockIdx.x * runs + wave / KS) * rows;
+  const size_t pitch = (size_t)SB * 64;
+  const bool whole = p.K % 128 == 0;
+  for (int s0 = slice * 16; s0 < SB; s0 += KS * 16) {
+    // lanes past the end read the last superblock, times zeros
+    const int s = min(s0 + (lane >> 2), SB - 1);
+    const bool in = s0 + (lane >> 2) < SB;
+    const unsigned code_at = s * 64u + g * 16u;
+    intx4 cn[R];
+    unsigned short bits[R][NG];
+    unsigned char zero[R][NG];
+    auto fetch = [&](int n) {  // rows past the end: the last one, whose sums are not stored
 #pragma unroll
-  for (int j = 0; j < NF; ++j) {
-    const size_t n = min(n0 + 16 * j + r, p.N - 1);
-    crow[j] = p.codes + n * SB * 64 + 16 * g;
-    srow[j] = n * p.KG;
-  }
+      for (int i = 0; i < R; ++i)
+        cn[i] = __builtin_nontemporal_load(reinterpret_cast<const intx4*>(
+            p.codes + (size_t)min(n + i, p.N - 1) * pitch + code_at));
+      if (whole) {  // all groups are there, and aligned to their number
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-    arow[i] = p.a + (min(m0 + 16 * i + r, p.M - 1) * (size_t)p.K + 8 * g) * act_size<A>();
-  floatx4 acc[MT][NF];
+        for (int i = 0; i < R; ++i)
+          __builtin_memcpy(
+              bits[i],
+              __builtin_assume_aligned(
+                  p.scales + (size_t)min(n + i, p.N - 1) * p.KG + (unsigned)(s * NG), 2 * NG),
+              2 * NG);
+      } else {
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-    for (int j = 0; j < NF; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
-  for (int s0 = wave * U; s0 < SB; s0 += W * U) {
-    intx4 cv[U][NF];
-    float sv[U][NF][4 / GB], zv[U][NF][4 / GB];
-    Octet<A> av[U][MT][4];
-    float dv[A == kActQ8 ? U : 1][MT][4][4];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int s = min(s0 + u, SB - 1);
-#pragma unroll
-      for (int j = 0; j < NF; ++j) {
-        cv[u][j] = *reinterpret_cast<const intx4*>(crow[j] + (size_t)s * 64);
-#pragma unroll
-        for (int b = 0; b < 4; b += GB) {
-          const size_t k = srow[j] + min((4 * s + b) >> GS, p.KG - 1);
-          sv[u][j][b / GB] = q4_scale(p.scales[k], p.f16);
-          zv[u][j][b / GB] = p.zeros ? (float)p.zeros[k] : 8.f;
-        }
+          for (int k = 0; k < NG; ++k)
+            bits[i][k] =
+                p.scales[(size_t)min(n + i, p.N - 1) * p.KG + (unsigned)min(s * NG + k, p.KG - 1)];
       }
-      // a block past the end: zeros
+      if (p.zeros) {
+        if (whole) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+          for (int i = 0; i < R; ++i)
+            __builtin_memcpy(
+                zero[i],
+                __builtin_assume_aligned(
+                    p.zeros + (size_t)min(n + i, p.N - 1) * p.KG + (unsigned)(s * NG), NG),
+                NG);
+        } else {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int k = 4 * (s0 + u) + b;
-          av[u][i][b] = load_octet<A>(arow[i] + (size_t)k * kQ4Block * act_size<A>(), k < KB);
-          if constexpr (A == kActQ8)
+          for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-              dv[u][i][b][v] =
-                  p.ad[(size_t)min(m0 + 16 * i + 4 * g + v, p.M - 1) * KB + min(k, KB - 1)];
+            for (int k = 0; k < NG; ++k)
+              zero[i][k] = p.zeros[(size_t)min(n + i, p.N - 1) * p.KG +
+                                   (unsigned)min(s * NG + k, p.KG - 1)];
         }
-    }
+      } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      floatx4 sum[MT][NF], ones[MT];
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+          for (int k = 0; k < NG; ++k) zero[i][k] = 8;
+      }
+    };
+    // the activations first: loads are waited for in the order they were asked for in
+    intx2 aq[4];
+    float av[4][8], ad[4], as[NG];
+    int qs[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const bool here = in && 4 * s + b < KB;
+      const Octet<A> o = load_octet<A>(
+          p.a + (size_t)((4 * s + b) * kQ4Block + 8 * g) * act_size<A>(), here);
+      if constexpr (A == kActQ8) {
+        aq[b] = o.v;
+        ad[b] = here ? p.ad[4 * s + b] : 0.f;
+      } else {
+        octet_values(o, av[b]);
+      }
+    }
+    fetch(n0);
+    if constexpr (A == kActQ8) {
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        if (b % GB == 0) {
+        qs[b] = __builtin_amdgcn_sdot4(aq[b][0], 0x01010101, 0, false);
+        qs[b] = __builtin_amdgcn_sdot4(aq[b][1], 0x01010101, qs[b], false);
+      }
+    } else {
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            ones[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < NG; ++k) {
+        as[k] = 0.f;
 #pragma unroll
-            for (int j = 0; j < NF; ++j) sum[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
-          }
-        }
-        if constexpr (A == kActQ8) {
-          const long one = 0x0101010101010101L;
-          long cx[NF];
+        for (int b = k * GB; b < (k + 1) * GB; ++b)
 #pragma unroll
-          for (int j = 0; j < NF; ++j)
-            cx[j] = (long)(unsigned)q4_low(cv[u][j][b]) | ((long)q4_high(cv[u][j][b]) << 32);
+          for (int e = 0; e < 8; ++e) as[k] += av[b][e];
+      }
+    }
+    for (int it = 0; it < iters; ++it) {
+      intx4 cv[R];
+      float sv[R][NG], zv[R][NG];
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            long ax;
-            __builtin_memcpy(&ax, &av[u][i][b].v, 8);
-            const intx4 none{0, 0, 0, 0};
-            const intx4 q = __builtin_amdgcn_mfma_i32_16x16x32_i8(ax, one, none, 0, 0, 0);
+      for (int i = 0; i < R; ++i) {
+        cv[i] = cn[i];
 #pragma unroll
-            for (int j = 0; j < NF; ++j) {
-              const intx4 t = __builtin_amdgcn_mfma_i32_16x16x32_i8(ax, cx[j], none, 0, 0, 0);
-              const int z = (int)zv[u][j][b / GB];
-#pragma unroll
-              for (int v = 0; v < 4; ++v)
-                sum[i][j][v] = fmaf((float)(t[v] - z * q[v]), dv[u][i][b][v], sum[i][j][v]);
-            }
-          }
-        } else {
-          bf16x8 cx[NF], one;
-#pragma unroll
-          for (int v = 0; v < 8; ++v) one[v] = (__bf16)1.0f;
-#pragma unroll
-          for (int j = 0; j < NF; ++j) cx[j] = q4_to_bf16(cv[u][j][b]);
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int l = 0; l < PL; ++l) {
-              bf16x8 ax;
-              if constexpr (A == kActF32)
-                ax = take_plane(av[u][i][b].v);
-              else
-                __builtin_memcpy(&ax, &av[u][i][b].v, 16);
-              ones[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ax, one, ones[i], 0, 0, 0);
-#pragma unroll
-              for (int j = 0; j < NF; ++j)
-                sum[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ax, cx[j], sum[i][j], 0, 0, 0);
-            }
-        }
-        if (b % GB == GB - 1) {
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int j = 0; j < NF; ++j)
-#pragma unroll
-              for (int v = 0; v < 4; ++v) {
-                const float t = A == kActQ8 ? sum[i][j][v]
-                                            : fmaf(-zv[u][j][b / GB], ones[i][v], sum[i][j][v]);
-                acc[i][j][v] = fmaf(sv[u][j][b / GB], t, acc[i][j][v]);
-              }
+        for (int k = 0; k < NG; ++k) {
+          sv[i][k] = q4_scale(bits[i][k], p.f16);
+          zv[i][k] = (float)zero[i][k];
         }
       }
+      if (it + 1 < iters) fetch(n0 + R * (it + 1));
+      float acc[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        acc[i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < NG; ++k) {
+          float t;
+          if constexpr (A == kActQ8) {
+            t = 0.f;
+#pragma unroll
+            for (int b = k * GB; b < (k + 1) * GB; ++b) {
+              int v = -(int)zv[i][k] * qs[b];
+              v = __builtin_amdgcn_sdot4(aq[b][0], q4_low(cv[i][b]), v, false);
+              v = __builtin_amdgcn_sdot4(aq[b][1], q4_high(cv[i][b]), v, false);
+              t = fmaf((float)v, ad[b], t);
+            }
+            acc[i] = fmaf(sv[i][k], t, acc[i]);
+          } else {
+            // codes come as multiples of 2^-9 (mhc_q4.h): so does the zero point, and the
+            // scale makes up for it
+            t = -(zv[i][k] * 0.001953125f) * as[k];
+#pragma unroll
+            for (int b = k * GB; b < (k + 1) * GB; ++b) {
+              const int lo = q4_low(cv[i][b]), hi = q4_high(cv[i][b]);
+              const floatx2 c[4] = {__builtin_amdgcn_cvt_pk_f32_fp8(lo, false),
+                                    __builtin_amdgcn_cvt_pk_f32_fp8(lo, true),
+                                    __builtin_amdgcn_cvt_pk_f32_fp8(hi, false),
+                                    __builtin_amdgcn_cvt_pk_f32_fp8(hi, true)};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) t = fmaf(c[e >> 1][e & 1], av[b][e], t);
+            }
+            acc[i] = fmaf(sv[i][k] * 512.f, t, acc[i]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) acc[i] = sum_wave(acc[i]);
+      if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          float* to = &part[wave][R * it + i];
+          *to = s0 == slice * 16 ? acc[i] : *to + acc[i];
+        }
     }
   }
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NF; ++j) part[wave][i * NF + j][lane] = acc[i][j];
   __syncthreads();
-  for (int i = threadIdx.x; i < MT * NF * 64; i += 64 * W) {
-    const int l = i & 63, f = i >> 6;
-    floatx4 s = part[0][f][l];
+  // (a slice past the end of the depth has no sums)
+  const int full = min(KS, (SB + 15) / 16);
+  for (int i = threadIdx.x; i < runs * rows; i += 64 * W) {
+    const int run = i / rows, row = i - run * rows, n = (blockIdx.x * runs + run) * rows + row;
+    float v = part[run * KS][row];
+    for (int k = 1; k < full; ++k) v += part[run * KS + k][row];
+    if (n < p.N) store_one(p, n, v);
+  }
+}
+
+// ---------------------------------------------------------------- up to 16 rows
+// A block takes 16*NF columns n, the depth in stages of one superblock (128 columns) a
+// wave; the waves' sums are added in order at the end.  A stage lies in LDS: the
+// codes, the scales and zero points as floats, and the activations as the instructions take
+// them (fp32 as its three planes).  It comes by way of registers, the weight from two stages
+// ahead on, in whole lines (a wave's load is 1 KB of one row).  Sixteen rows read straight
+// into the instructions' layout instead are sixteen lines a load, for the two bytes of a
+// scale as well, and every wave loads the activations again.
+// Within a row of codes the 16-byte unit i lies at place i ^ (row % 16), and a row of
+// activations is 16 bytes longer than it needs, so that sixteen rows read at one unit meet
+// all banks.
+// FEW (at most four rows): row r of the instruction is row r / 4 of a, and a lane ends with
+// one sum, of row lane / 16.  With fp32 activations the rows 4 m, + 1, + 2 are the three
+// planes of row m, so one instruction does what takes three from five rows on.
+template <int A, int GS, bool FEW, int NF, int W>
+struct RowsLayout {
+  static constexpr int NG = 4 >> GS;                       // groups in a superblock
+  static constexpr int CODES = 16 * NF * 64 * W;  // bytes of a stage
+  static constexpr int SCALES = 16 * NF * W * NG * 8;
+  static constexpr int PITCH = 128 * W * (A == kActQ8 ? 1 : 2) + 16;  // of a row of a
+  static constexpr int DPITCH = 4 * W + 4;        // floats, of a row of its scales
+  static int bytes(int M) {
+    return CODES + SCALES + M * (PITCH * (A == kActF32 ? 3 : 1) + (A == kActQ8 ? DPITCH * 4 : 0));
+  }
+};
+
+template <int A, int GS, bool FEW, int NF, int W>
+__global__ __launch_bounds__(64 * W) void q4_rows_kernel(Q4Args p) {
+  using L = RowsLayout<A, GS, FEW, NF, W>;
+  constexpr int NT = 64 * W, NG = L::NG;
+  constexpr int GB = 1 << GS;                       // blocks of 32 a group
+  constexpr int MV = FEW ? 1 : 4;                   // sums a lane ends with, per tile
+  constexpr int PL = A == kActF32 && !FEW ? 3 : 1;  // instructions a tile and block
+  constexpr int UR = 4 * W, UA = 8 * W * act_size<A>();  // 16-byte units of a row, of codes and a
+  constexpr int RA = FEW ? 4 : 16;
+  constexpr int NS = (16 * NF * W * NG + NT - 1) / NT, NA = (RA * UA + NT - 1) / NT;
+  static_assert(NF * W * 16 * UR * 4 >= NF * MV * W * 64, "the sums fit where the codes were");
+  extern __shared__ __align__(16) unsigned char lds[];
+  float2* const scales = reinterpret_cast<float2*>(lds + L::CODES);
+  unsigned char* const acts = lds + L::CODES + L::SCALES;
+  float* const dacts = reinterpret_cast<float*>(acts + p.M * L::PITCH);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * 16 * NF;
+  const int KB = p.K / kQ4Block, SB = (p.K + 127) / 128;
+
+  // Rows past the end read the last row; their results are not stored.
+  intx4 cn[2][NF], an[NA];
+  unsigned short sn[2][NS];
+  unsigned char zn[2][NS];
+  float dn = 0.f;
+  auto fetch_a = [&](int sb) {  // zeros past the end
 #pragma unroll
-    for (int w = 1; w < W; ++w) s += part[w][f][l];
-    const int n = n0 + 16 * (f % NF) + (l & 15);
+    for (int i = 0; i < NA; ++i) {
+      const int id = threadIdx.x + NT * i, m = id / UA, c = id % UA;
+      const int col = 128 * sb + c * (16 / act_size<A>());
+      an[i] = intx4{0, 0, 0, 0};
+      if (m < p.M && col < p.K)
+        an[i] = *reinterpret_cast<const intx4*>(p.a + ((size_t)m * p.K + col) * act_size<A>());
+    }
+    if constexpr (A == kActQ8) {
+      const int m = threadIdx.x / (4 * W), k = 4 * sb + threadIdx.x % (4 * W);
+      dn = m < p.M && k < KB ? p.ad[(size_t)m * KB + k] : 0.f;
+    }
+  };
+  auto fetch_w = [&](int sb, auto turn) {  // a superblock past the end: the last one, times zeros
+    constexpr int T = decltype(turn)::value;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int m = m0 + 16 * (f / NF) + 4 * (l >> 4) + v;
-      if (m < p.M && n < p.N) {
-        const size_t at = (size_t)m * p.N + n;
-        if (p.bf16_out)
-          static_cast<__hip_bfloat16*>(p.out)[at] = __float2bfloat16(s[v]);
-        else
-          static_cast<float*>(p.out)[at] = s[v];
+    for (int i = 0; i < NF; ++i) {
+      const int row = (NT * i + threadIdx.x) / UR, unit = threadIdx.x % UR;
+      const unsigned char* base = p.codes + (size_t)min(n0 + row, p.N - 1) * SB * 64;
+      const unsigned at = min(sb + (unit >> 2), SB - 1) * 64u + (unit & 3) * 16u;
+      cn[T][i] = __builtin_nontemporal_load(reinterpret_cast<const intx4*>(base + at));
+    }
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int id = threadIdx.x + NT * i, row = id / (W * NG), k = id % (W * NG);
+      sn[T][i] = p.scales[(size_t)min(n0 + row, p.N - 1) * p.KG + min(sb * NG + k, p.KG - 1)];
+    }
+    if (p.zeros) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const int id = threadIdx.x + NT * i, row = id / (W * NG), k = id % (W * NG);
+        zn[T][i] = p.zeros[(size_t)min(n0 + row, p.N - 1) * p.KG + min(sb * NG + k, p.KG - 1)];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) zn[T][i] = 8;
+    }
+  };
+  auto place = [&](auto turn) {
+    constexpr int T = decltype(turn)::value;
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      const int row = (NT * i + threadIdx.x) / UR, unit = threadIdx.x % UR;
+      reinterpret_cast<intx4*>(lds)[row * UR + (unit ^ (row & 15))] = cn[T][i];
+    }
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int id = threadIdx.x + NT * i, row = id / (W * NG), k = id % (W * NG);
+      if (16 * NF * W * NG % NT == 0 || row < 16 * NF)
+        scales[k * 16 * NF + row] = make_float2(q4_scale(sn[T][i], p.f16), (float)zn[T][i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      const int id = threadIdx.x + NT * i, m = id / UA, c = id % UA;
+      if (m >= p.M) continue;
+      if constexpr (A == kActF32) {
+        float v[4];
+        __builtin_memcpy(v, &an[i], 16);
+#pragma unroll
+        for (int l = 0; l < 3; ++l) {  // the top eight significant bits, and what they leave
+          unsigned u[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const unsigned lo = __float_as_uint(v[2 * h]), hi = __float_as_uint(v[2 * h + 1]);
+            u[h] = __builtin_amdgcn_perm(hi, lo, 0x07060302);
+            v[2 * h] -= __uint_as_float(lo & 0xffff0000u);
+            v[2 * h + 1] -= __uint_as_float(hi & 0xffff0000u);
+          }
+          __builtin_memcpy(
+              __builtin_assume_aligned(acts + (3 * m + l) * L::PITCH + 8 * c, 8), u, 8);
+        }
+      } else {
+        __builtin_memcpy(__builtin_assume_aligned(acts + m * L::PITCH + 16 * c, 16), &an[i], 16);
       }
     }
+    if constexpr (A == kActQ8) {
+      const int m = threadIdx.x / (4 * W);
+      if (m < p.M) dacts[m * L::DPITCH + threadIdx.x % (4 * W)] = dn;
+    }
+  };
+
+  const int am = min(FEW ? r >> 2 : r, p.M - 1);
+  float acc[NF][MV];
+#pragma unroll
+  for (int j = 0; j < NF; ++j)
+#pragma unroll
+    for (int v = 0; v < MV; ++v) acc[j][v] = 0.f;
+
+  auto multiply = [&] {
+    intx4 cv[NF];
+#pragma unroll
+    for (int j = 0; j < NF; ++j)
+      cv[j] = reinterpret_cast<const intx4*>(lds)[(16 * j + r) * UR + ((4 * wave + g) ^ r)];
+    float4 dv[MV];
+    if constexpr (A == kActQ8)
+#pragma unroll
+      for (int v = 0; v < MV; ++v)
+        dv[v] = *reinterpret_cast<const float4*>(
+            dacts + min(FEW ? g : 4 * g + v, p.M - 1) * L::DPITCH + 4 * wave);
+    floatx4 sum[NF], ones;
+    float2 sz[NF];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      if (b % GB == 0) {
+        ones = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+          sum[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+          sz[j] = scales[(wave * NG + b / GB) * 16 * NF + 16 * j + r];
+        }
+      }
+      if constexpr (A == kActQ8) {
+        long ax;
+        __builtin_memcpy(&ax,
+                         __builtin_assume_aligned(
+                             acts + am * L::PITCH + 128 * wave + 32 * b + 8 * g, 8), 8);
+        const intx4 none{0, 0, 0, 0};
+        const intx4 q =
+            __builtin_amdgcn_mfma_i32_16x16x32_i8(ax, 0x0101010101010101L, none, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+          const long cx = (long)(unsigned)q4_low(cv[j][b]) | ((long)q4_high(cv[j][b]) << 32);
+          const intx4 t = __builtin_amdgcn_mfma_i32_16x16x32_i8(ax, cx, none, 0, 0, 0);
+          const int z = (int)sz[j].y;
+#pragma unroll
+          for (int v = 0; v < MV; ++v)
+            sum[j][v] = fmaf((float)(t[v] - z * q[v]),
+                             b == 0 ? dv[v].x : b == 1 ? dv[v].y : b == 2 ? dv[v].z : dv[v].w,
+                             sum[j][v]);
+        }
+      } else {
+        bf16x8 one, ax[PL];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) one[v] = (__bf16)1.0f;
+#pragma unroll
+        for (int l = 0; l < PL; ++l) {
+          const int row = A == kActBF16 ? am : FEW ? 3 * am + min(r & 3, 2) : 3 * am + l;
+          __builtin_memcpy(&ax[l],
+                           __builtin_assume_aligned(
+                               acts + row * L::PITCH + 256 * wave + 64 * b + 16 * g, 16), 16);
+          ones = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ax[l], one, ones, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+          const bf16x8 cx = q4_to_bf16(cv[j][b]);
+#pragma unroll
+          for (int l = 0; l < PL; ++l)
+            sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ax[l], cx, sum[j], 0, 0, 0);
+        }
+      }
+      if (b % GB == GB - 1) {
+        if (A == kActF32 && FEW) ones[0] += ones[1] + ones[2];
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+          if (A == kActF32 && FEW) sum[j][0] += sum[j][1] + sum[j][2];
+#pragma unroll
+          for (int v = 0; v < MV; ++v) {
+            const float t = A == kActQ8 ? sum[j][v] : fmaf(-sz[j].y, ones[v], sum[j][v]);
+            acc[j][v] = fmaf(sz[j].x, t, acc[j][v]);
+          }
+        }
+      }
+    }
+  };
+  auto step = [&](int sb, auto turn) {
+    place(turn);
+    __syncthreads();
+    // asked for in the order of use, which is the order that loads are waited for in
+    if (sb + W < SB) fetch_a(sb + W);
+    if (sb + 2 * W < SB) fetch_w(sb + 2 * W, turn);
+    if (sb + wave < SB) multiply();
+    __syncthreads();
+  };
+  constexpr std::integral_constant<int, 0> even{};
+  constexpr std::integral_constant<int, 1> odd{};
+  fetch_w(0, even);
+  fetch_a(0);
+  if (W < SB) fetch_w(W, odd);
+  for (int sb = 0; sb < SB; sb += 2 * W) {
+    step(sb, even);
+    if (sb + W < SB) step(sb + W, odd);
+  }
+  float* sums = reinterpret_cast<float*>(lds);  // no longer than the codes were
+#pragma unroll
+  for (int j = 0; j < NF; ++j)
+#pragma unroll
+    for (int v = 0; v < MV; ++v) sums[(wave * NF * MV + j * MV + v) * 64 + lane] = acc[j][v];
+  __syncthreads();
+  for (int i = threadIdx.x; i < NF * MV * 64; i += NT) {
+    const int l = i & 63, f = i >> 6;
+    float s = sums[i];
+#pragma unroll
+    for (int w = 1; w < W; ++w) s += sums[w * NF * MV * 64 + i];
+    const int n = n0 + 16 * (f / MV) + (l & 15), m = FEW ? l >> 4 : 4 * (l >> 4) + f % MV;
+    if (m < p.M && n < p.N) store_one(p, (size_t)m * p.N + n, s);
+  }
+}
+
+// ---------------------------------------------------------------- tiles
+// A block takes BM = 32*FM*WM rows of a and BN = 32*FN*WN columns n; WM x WN waves, each with
+// FM x FN tiles of v_mfma_f32_32x32x16_bf16, times KG groups of such waves that take the
+// superblocks (128 columns) of the depth in turn and are added in order at the end.  A stage
+// (a superblock for each group of waves) comes by way of registers into one of two buffers in
+// LDS while the one before is multiplied, one barrier a stage.
+// In LDS: the codes; the activations as bf16 (fp32 ones and int8 codes times their scale as
+// three planes), with the sums of each group of columns, which the zero points multiply; the
+// scales and zero points as floats.  A group's products start from minus zero point times
+// sum and end times the scale in the sums that are kept, in fp32.
+// The 16-byte units of a row are placed so that sixteen rows read at one unit meet all banks.
+template <int A, int GS, int FM, int FN, int WM, int WN, int KG>
+struct TileLayout {
+  static constexpr int PL = A == kActBF16 ? 1 : 3, NG = 4 >> GS;
+  static constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
+  static constexpr int CODES = BN * 64, ACTS = PL * BM * 256;  // bytes of a superblock
+  static constexpr int SUMS = BM * NG * 4, SCALES = BN * NG * 8;
+  static constexpr int PART = CODES + ACTS + SUMS + SCALES, STAGE = KG * PART;
+  static constexpr int LAST = (KG - 1) * WM * WN * FM * FN * 4096;  // the groups' sums
+  static constexpr int BUFS = 2 * STAGE <= 160 * 1024 ? 2 : 1;
+  static constexpr int BYTES = BUFS * STAGE > LAST ? BUFS * STAGE : LAST;
+};
+
+// Sum over aligned groups of N neighbouring lanes, N up to 32, in every lane.
+template <int N>
+__device__ __forceinline__ float sum_lanes(float v) {
+  if (N >= 2) v += dpp<0xB1>(v);
+  if (N >= 4) v += dpp<0x4E>(v);
+  if (N >= 8) v += dpp<0x141>(v);
+  if (N >= 16) v += dpp<0x128>(v);
+  return N >= 32 ? swap16_sum(v) : v;
+}
+
+template <int A, int GS, int FM, int FN, int WM, int WN, int KG>
+__global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, int MT, int NT) {
+  using L = TileLayout<A, GS, FM, FN, WM, WN, KG>;
+  constexpr int W = WM * WN * KG, TH = 64 * W, PL = L::PL, NG = L::NG, GB = 1 << GS;
+  constexpr int BM = L::BM, BN = L::BN;
+  constexpr int UA = 8 * act_size<A>();  // 16-byte units of a row of a, of a superblock
+  constexpr int NA = KG * BM * UA / TH, NB = (KG * BN * 4 + TH - 1) / TH;
+  constexpr int NS = (KG * BN * NG + TH - 1) / TH;
+  static_assert(KG * BM * UA % TH == 0, "whole loads");
+  extern __shared__ __align__(16) unsigned char lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 31, h = lane >> 5;
+  const int wm = wave % WM, wn = wave / WM % WN, kg = wave / (WM * WN);
+  const int KB = p.K / kQ4Block, SB = (p.K + 127) / 128;
+
+  // Blocks go to the eight dies in turn: give each die a run of tiles, rows first, so that
+  // the tiles that read the same columns of the weight share its L2.
+  const int tiles = MT * NT;
+  int id = blockIdx.x;
+  {
+    const int per = tiles / 8, rest = tiles % 8, die = id % 8, at = id / 8;
+    id = die * per + min(die, rest) + at;
+  }
+  const int m0 = id % MT * BM, n0 = id / MT * BN;
+
+  intx4 an[NA], bn[NB];
+  float dn[A == kActQ8 ? NA : 1];
+  unsigned short sn[NS];
+  unsigned char zn[NS];
+  // superblock sb + (the group); rows past the end read the last row, and are not stored
+  auto fetch = [&](int sb) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      const int at = threadIdx.x + TH * i, row = at / UA, c = at % UA;
+      const int m = min(m0 + row % BM, p.M - 1);
+      const int col = 128 * (sb + row / BM) + c * (16 / act_size<A>());
+      an[i] = intx4{0, 0, 0, 0};
+      if (col < p.K)
+        an[i] = *reinterpret_cast<const intx4*>(p.a + ((size_t)m * p.K + col) * act_size<A>());
+      if constexpr (A == kActQ8) dn[i] = p.ad[(size_t)m * KB + min(col / kQ4Block, KB - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int at = threadIdx.x + TH * i, row = at / 4;
+      const int n = min(n0 + row % BN, p.N - 1), s = min(sb + row / BN, SB - 1);
+      bn[i] = *reinterpret_cast<const intx4*>(p.codes + ((size_t)n * SB + s) * 64 + (at & 3) * 16);
+    }
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int at = threadIdx.x + TH * i, row = at / NG, k = at % NG;
+      const size_t g = (size_t)min(n0 + row % BN, p.N - 1) * p.KG +
+                       min((sb + row / BN) * NG + k, p.KG - 1);
+      sn[i] = p.scales[g];
+      zn[i] = 8;
+      if (p.zeros) zn[i] = p.zeros[g];
+    }
+  };
+  auto place = [&](unsigned char* to) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      const int at = threadIdx.x + TH * i, row = at / UA, c = at % UA, m = row % BM;
+      unsigned char* part = to + row / BM * L::PART;
+      unsigned char* acts = part + L::CODES;
+      float total = 0.f;
+      if constexpr (A == kActBF16) {
+        reinterpret_cast<intx4*>(acts)[m * 16 + (c ^ (m & 15))] = an[i];
+        float v[8];
+        octet_values(Octet<kActBF16>{an[i]}, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) total += v[e];
+      } else {
+        constexpr int NV = A == kActF32 ? 4 : 16;  // columns of a unit
+        float v[NV];
+        if constexpr (A == kActF32) {
+          __builtin_memcpy(v, &an[i], 16);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            v[e] = (float)((signed char)(an[i][e >> 2] >> (8 * (e & 3)))) * dn[i];
+        }
+#pragma unroll
+        for (int e = 0; e < NV; ++e) total += v[e];
+#pragma unroll
+        for (int l = 0; l < 3; ++l) {  // the top eight significant bits, and what they leave
+          unsigned u[NV / 2];
+#pragma unroll
+          for (int e = 0; e < NV / 2; ++e) {
+            const unsigned lo = __float_as_uint(v[2 * e]), hi = __float_as_uint(v[2 * e + 1]);
+            u[e] = __builtin_amdgcn_perm(hi, lo, 0x07060302);
+            v[2 * e] -= __uint_as_float(lo & 0xffff0000u);
+            v[2 * e + 1] -= __uint_as_float(hi & 0xffff0000u);
+          }
+          unsigned char* plane = acts + (l * BM + m) * 256;
+          if constexpr (A == kActF32) {
+            __builtin_memcpy(__builtin_assume_aligned(
+                                 plane + ((c >> 1) ^ (m & 15)) * 16 + (c & 1) * 8, 8), u, 8);
+          } else {
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+              __builtin_memcpy(
+                  __builtin_assume_aligned(plane + ((2 * c + o) ^ (m & 15)) * 16, 16), u + 4 * o,
+                  16);
+          }
+        }
+      }
+      total = sum_lanes<UA / NG>(total);
+      if (c % (UA / NG) == 0)
+        reinterpret_cast<float*>(acts + L::ACTS)[c / (UA / NG) * BM + m] = -total;
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int at = threadIdx.x + TH * i, row = at / 4, n = row % BN;
+      if (KG * BN * 4 % TH == 0 || row < KG * BN)
+        reinterpret_cast<intx4*>(to + row / BN * L::PART)[n * 4 + ((at & 3) ^ ((n >> 2) & 3))] =
+            bn[i];
+    }
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int at = threadIdx.x + TH * i, row = at / NG, k = at % NG;
+      if (KG * BN * NG % TH == 0 || row < KG * BN)
+        reinterpret_cast<float2*>(to + row / BN * L::PART + L::CODES + L::ACTS +
+                                  L::SUMS)[k * BN + row % BN] =
+            make_float2(q4_scale(sn[i], p.f16), (float)zn[i]);
+    }
+  };
+
+  floatx16 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+
+  auto multiply = [&](const unsigned char* part) {
+    const unsigned char* acts = part + L::CODES;
+    const float* sums = reinterpret_cast<const float*>(acts + L::ACTS);
+    const float2* scales = reinterpret_cast<const float2*>(acts + L::ACTS + L::SUMS);
+    intx4 cv[FN][2];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int n = (wn * FN + j) * 32 + r;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        cv[j][u] = reinterpret_cast<const intx4*>(part)[n * 4 + ((2 * u + h) ^ ((n >> 2) & 3))];
+    }
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+      float2 sz[FN];
+      bf16x8 bx[FN][2 * GB];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        sz[j] = scales[k * BN + (wn * FN + j) * 32 + r];
+#pragma unroll
+        for (int b = 0; b < 2 * GB; ++b) bx[j][b] = q4_to_bf16(cv[j][b & 1][k * GB + (b >> 1)]);
+      }
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int m = (wm * FM + i) * 32 + r;
+        floatx16 c, t[FN];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const floatx4 s = *reinterpret_cast<const floatx4*>(
+              sums + k * BM + (wm * FM + i) * 32 + 8 * v + 4 * h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[4 * v + e] = s[e];
+        }
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) t[j][v] = sz[j].y * c[v];
+#pragma unroll
+        for (int l = 0; l < PL; ++l)
+#pragma unroll
+          for (int b = 0; b < 2 * GB; ++b) {
+            const int unit = 4 * (k * GB + (b >> 1)) + 2 * (b & 1) + h;
+            bf16x8 ax;
+            __builtin_memcpy(&ax,
+                             __builtin_assume_aligned(
+                                 acts + ((l * BM + m) * 16 + (unit ^ (m & 15))) * 16, 16), 16);
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+              t[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ax, bx[j][b], t[j], 0, 0, 0);
+          }
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) acc[i][j][v] = fmaf(sz[j].x, t[j][v], acc[i][j][v]);
+      }
+    }
+  };
+
+  fetch(0);
+  int turn = 0;
+  for (int sb = 0; sb < SB; sb += KG, turn ^= L::BUFS - 1) {
+    unsigned char* stage = lds + turn * L::STAGE;
+    if (L::BUFS == 1 && sb > 0) __syncthreads();
+    place(stage);
+    __syncthreads();  // (of two buffers, the one written next was read before this)
+    if (sb + KG < SB) fetch(sb + KG);
+    if (KG == 1 || sb + kg < SB) multiply(stage + kg * L::PART);
+  }
+  if constexpr (KG > 1) {
+    float4* last = reinterpret_cast<float4*>(lds);
+    __syncthreads();
+    if (kg > 0) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            last[(((wave - WM * WN) * FM + i) * FN + j) * 256 + v * 64 + lane] =
+                make_float4(acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2],
+                            acc[i][j][4 * v + 3]);
+    }
+    __syncthreads();
+    if (kg > 0) return;
+#pragma unroll
+    for (int k = 1; k < KG; ++k)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float4 o =
+                last[((((k - 1) * WM * WN + wave) * FM + i) * FN + j) * 256 + v * 64 + lane];
+            acc[i][j][4 * v] += o.x;
+            acc[i][j][4 * v + 1] += o.y;
+            acc[i][j][4 * v + 2] += o.z;
+            acc[i][j][4 * v + 3] += o.w;
+          }
+  }
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int n = n0 + (wn * FN + j) * 32 + r;
+    if (n >= p.N) continue;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int m = m0 + (wm * FM + i) * 32 + 8 * (v >> 2) + 4 * h + (v & 3);
+        if (m < p.M) store_one(p, (size_t)m * p.N + n, acc[i][j][v]);
+      }
   }
 }
 
 namespace {
-template <int A, int GS, int MT, int NF, int W, int U>
-void launch_q4_at(const Q4Args& p, hipStream_t st) {
-  hipLaunchKernelGGL((q4_matmul_kernel<A, GS, MT, NF, W, U>),
-                     dim3((p.N + 16 * NF - 1) / (16 * NF), (p.M + 16 * MT - 1) / (16 * MT)),
-                     dim3(64 * W), 0, st, p);
+template <int A, int GS, int FM, int FN, int WM, int WN, int KG>
+void launch_q4_tile(const Q4Args& p, hipStream_t st) {
+  using L = TileLayout<A, GS, FM, FN, WM, WN, KG>;
+  const int MT = (p.M + L::BM - 1) / L::BM, NT = (p.N + L::BN - 1) / L::BN, lds = L::BYTES;
+  hipLaunchKernelGGL((q4_tile_kernel<A, GS, FM, FN, WM, WN, KG>), dim3((unsigned)(MT * NT)),
+                     dim3(64 * WM * WN * KG), lds, st, p, MT, NT);
+}
+template <int A, int GS, bool FEW, int NF, int W>
+void launch_q4_rows(const Q4Args& p, hipStream_t st) {
+  const int lds = RowsLayout<A, GS, FEW, NF, W>::bytes(p.M);
+  hipLaunchKernelGGL((q4_rows_kernel<A, GS, FEW, NF, W>), dim3((p.N + 16 * NF - 1) / (16 * NF)),
+                     dim3(64 * W), lds, st, p);
+}
+template <int A, int GS, bool FEW>
+void launch_q4_few(const Q4Args& p, hipStream_t st) {
+  constexpr int W = A == kActF32 && !FEW ? 8 : 16;  // 16 rows' planes of 16 superblocks: 197 KB
+  if (p.N <= 4096)
+    launch_q4_rows<A, GS, FEW, 1, W>(p, st);
+  else if (p.N <= 8192)
+    launch_q4_rows<A, GS, FEW, 2, W>(p, st);
+  else if (p.N < 16384)
+    launch_q4_rows<A, GS, FEW, 2, 8>(p, st);
+  else
+    launch_q4_rows<A, GS, FEW, 4, 8>(p, st);
+}
+template <int A, int GS, int R, int W>
+void launch_q4_vector(const Q4Args& p, hipStream_t st) {
+  int KS = 1;  // slices: as many as there are, up to the block's waves
+  while (KS < W && KS * 2048 < p.K) KS *= 2;
+  // one round of 16 waves a unit
+  const int most = kVectorRows / R;
+  const long want = ((long)p.N * KS + 4096L * R - 1) / (4096L * R);
+  const int iters = want < 1 ? 1 : want > most ? most : (int)want;
+  const int rows = W / KS * R * iters;
+  hipLaunchKernelGGL((q4_vector_kernel<A, GS, R, W>), dim3((p.N + rows - 1) / rows),
+                     dim3(64 * W), 0, st, p, KS, iters);
 }
 template <int A, int GS>
 void launch_q4_g(const Q4Args& p, hipStream_t st) {
-  if (p.M > 16)
-    launch_q4_at<A, GS, 2, 2, 8, 1>(p, st);
-  else if (p.N >= 8192)
-    launch_q4_at<A, GS, 1, 2, 8, 1>(p, st);
+  if (p.M == 1)
+    launch_q4_vector<A, GS, 2, 8>(p, st);
+  else if (p.M <= 4)
+    launch_q4_few<A, GS, true>(p, st);
+  else if (p.M <= 16)
+    launch_q4_few<A, GS, false>(p, st);
+  else if (p.M <= 32)
+    launch_q4_tile<A, GS, 1, 1, 1, 2, 4>(p, st);
+  else if (p.M <= 64)
+    launch_q4_tile<A, GS, 2, 1, 1, 4, 2>(p, st);
   else
-    launch_q4_at<A, GS, 1, 1, 8, 2>(p, st);
+    launch_q4_tile<A, GS, 2, 1, 2, 4, 1>(p, st);
 }
 template <int A>
 void launch_q4_a(const Q4Args& p, int group, hipStream_t st) {
