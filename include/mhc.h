@@ -562,7 +562,8 @@ int mhc_site_post_norm_bwd(const float* g, const void* x, const unsigned char* x
  *   a [M][K], a_type   MHC_F32 or MHC_BF16 with a_scales NULL; or MHC_I8 with a_scales
  *     [M][K/32], value a * a_scales: the q and d of mhc_site_pre_zq8
  *   Products are exact and summed in fp32 in an order fixed by the shape (int8: exactly
- *   within 32 columns); a part of an fp32 value that is under 2^-126 may count as zero.  A
+ *   within 32 columns for M <= 16, else of a * a_scales rounded to fp32); a part of an fp32
+ *   value that is under 2^-126 may count as zero.  A
  *   row of a with an infinity or a NaN gives a row that is not finite; other rows do not
  *   see it.
  *

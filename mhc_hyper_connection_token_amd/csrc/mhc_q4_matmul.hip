@@ -40,14 +40,6 @@ constexpr int act_size() {
   return A == kActF32 ? 4 : A == kActBF16 ? 2 : 1;
 }
 
-template <int A>
-__device__ __forceinline__ Octet<A> load_octet(const unsigned char* p, bool in) {
-  Octet<A> o;
-  __builtin_memset(&o, 0, sizeof(o));
-  if (in) o = *reinterpret_cast<const Octet<A>*>(p);
-  return o;
-}
-
 struct Q4Args {
   const unsigned char* a;
   const float* ad;  // scales of int8 activations, [M][K/32]
@@ -88,7 +80,7 @@ __device__ __forceinline__ void store_one(const Q4Args& p, size_t at, float v) {
 // LDS.
 constexpr int kVectorRows = 64;  // rows of a wave at most
 
-template <int A, int GS, int R, int W>
+template <int A, int GS, bool ZEROS, int R, int W>
 __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int iters) {
   constexpr int GB = 1 << GS, NG = 4 / GB;  // blocks of 32 a group, groups in a superblock
   __shared__ float part[W][kVectorRows];
@@ -120,16 +112,7 @@ __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int
               __builtin_assume_aligned(
                   p.scales + (size_t)min(n + i, p.N - 1) * p.KG + (unsigned)(s * NG), 2 * NG),
               2 * NG);
-      } else {
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-          for (int k = 0; k < NG; ++k)
-            bits[i][k] =
-                p.scales[(size_t)min(n + i, p.N - 1) * p.KG + (unsigned)min(s * NG + k, p.KG - 1)];
-      }
-      if (p.zeros) {
-        if (whole) {
+        if constexpr (ZEROS)
 #pragma unroll
           for (int i = 0; i < R; ++i)
             __builtin_memcpy(
@@ -137,38 +120,41 @@ __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int
                 __builtin_assume_aligned(
                     p.zeros + (size_t)min(n + i, p.N - 1) * p.KG + (unsigned)(s * NG), NG),
                 NG);
-        } else {
-#pragma unroll
-          for (int i = 0; i < R; ++i)
-#pragma unroll
-            for (int k = 0; k < NG; ++k)
-              zero[i][k] = p.zeros[(size_t)min(n + i, p.N - 1) * p.KG +
-                                   (unsigned)min(s * NG + k, p.KG - 1)];
-        }
       } else {
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
-          for (int k = 0; k < NG; ++k) zero[i][k] = 8;
+          for (int k = 0; k < NG; ++k) {
+            const size_t at =
+                (size_t)min(n + i, p.N - 1) * p.KG + (unsigned)min(s * NG + k, p.KG - 1);
+            bits[i][k] = p.scales[at];
+            if constexpr (ZEROS) zero[i][k] = p.zeros[at];
+          }
       }
     };
     // the activations first: loads are waited for in the order they were asked for in
+    Octet<A> ao[4];
     intx2 aq[4];
     float av[4][8], ad[4], as[NG];
     int qs[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      const bool here = in && 4 * s + b < KB;
-      const Octet<A> o = load_octet<A>(
-          p.a + (size_t)((4 * s + b) * kQ4Block + 8 * g) * act_size<A>(), here);
-      if constexpr (A == kActQ8) {
-        aq[b] = o.v;
-        ad[b] = here ? p.ad[4 * s + b] : 0.f;
-      } else {
-        octet_values(o, av[b]);
-      }
+      const int k = min(4 * s + b, KB - 1);
+      ao[b] = *reinterpret_cast<const Octet<A>*>(
+          p.a + (unsigned)(k * kQ4Block + 8 * g) * (unsigned)act_size<A>());
+      if constexpr (A == kActQ8) ad[b] = p.ad[k];
     }
     fetch(n0);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      if (!in || 4 * s + b >= KB) __builtin_memset(&ao[b], 0, sizeof(ao[b]));
+      if constexpr (A == kActQ8) {
+        aq[b] = ao[b].v;
+        if (!in || 4 * s + b >= KB) ad[b] = 0.f;
+      } else {
+        octet_values(ao[b], av[b]);
+      }
+    }
     if constexpr (A == kActQ8) {
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
@@ -194,7 +180,7 @@ __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
           sv[i][k] = q4_scale(bits[i][k], p.f16);
-          zv[i][k] = (float)zero[i][k];
+          zv[i][k] = ZEROS ? (float)zero[i][k] : 8.f;
         }
       }
       if (it + 1 < iters) fetch(n0 + R * (it + 1));
@@ -306,47 +292,60 @@ __global__ __launch_bounds__(64 * W) void q4_rows_kernel(Q4Args p) {
   unsigned short sn[2][NS];
   unsigned char zn[2][NS];
   float dn = 0.f;
-  auto fetch_a = [&](int sb) {  // zeros past the end
+  // Where a thread's loads begin: 64-bit products cost too much to be formed a stage.  No
+  // register that is loaded into gets a value of its own in between, which would wait for the
+  // load: past the end of the depth the last columns are read, and zeros take their place in
+  // LDS.
+  const unsigned char *ap[NA], *bp[NF];
+  size_t sp[NS];
+#pragma unroll
+  for (int i = 0; i < NA; ++i)
+    ap[i] = p.a + (size_t)((threadIdx.x + NT * i) / UA) * p.K * act_size<A>();
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+    bp[i] = p.codes + (size_t)min(n0 + (int)(NT * i + threadIdx.x) / UR, p.N - 1) * SB * 64 +
+            (threadIdx.x & 3) * 16;
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+    sp[i] = (size_t)min(n0 + (int)(threadIdx.x + NT * i) / (W * NG), p.N - 1) * p.KG;
+  auto fetch_a = [&](int sb) {
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
-      const int id = threadIdx.x + NT * i, m = id / UA, c = id % UA;
-      const int col = 128 * sb + c * (16 / act_size<A>());
-      an[i] = intx4{0, 0, 0, 0};
-      if (m < p.M && col < p.K)
-        an[i] = *reinterpret_cast<const intx4*>(p.a + ((size_t)m * p.K + col) * act_size<A>());
+      const int col = 128 * sb + (threadIdx.x + NT * i) % UA * (16 / act_size<A>());
+      if ((NT * i + 64 * wave) / UA < p.M)  // (whole waves)
+        an[i] = *reinterpret_cast<const intx4*>(
+            ap[i] + (unsigned)(min(col, p.K - 16 / act_size<A>()) * act_size<A>()));
     }
-    if constexpr (A == kActQ8) {
-      const int m = threadIdx.x / (4 * W), k = 4 * sb + threadIdx.x % (4 * W);
-      dn = m < p.M && k < KB ? p.ad[(size_t)m * KB + k] : 0.f;
-    }
+    if constexpr (A == kActQ8)
+      dn = p.ad[(size_t)min((int)threadIdx.x / (4 * W), p.M - 1) * KB +
+                min(4 * sb + (int)threadIdx.x % (4 * W), KB - 1)];
   };
   auto fetch_w = [&](int sb, auto turn) {  // a superblock past the end: the last one, times zeros
     constexpr int T = decltype(turn)::value;
 #pragma unroll
     for (int i = 0; i < NF; ++i) {
-      const int row = (NT * i + threadIdx.x) / UR, unit = threadIdx.x % UR;
-      const unsigned char* base = p.codes + (size_t)min(n0 + row, p.N - 1) * SB * 64;
-      const unsigned at = min(sb + (unit >> 2), SB - 1) * 64u + (unit & 3) * 16u;
-      cn[T][i] = __builtin_nontemporal_load(reinterpret_cast<const intx4*>(base + at));
+      const unsigned at = min(sb + (int)(threadIdx.x % UR) / 4, SB - 1) * 64u;
+      cn[T][i] = __builtin_nontemporal_load(reinterpret_cast<const intx4*>(bp[i] + at));
     }
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const int id = threadIdx.x + NT * i, row = id / (W * NG), k = id % (W * NG);
-      sn[T][i] = p.scales[(size_t)min(n0 + row, p.N - 1) * p.KG + min(sb * NG + k, p.KG - 1)];
-    }
-    if (p.zeros) {
+    for (int i = 0; i < NS; ++i)
+      sn[T][i] = p.scales[sp[i] + (unsigned)min(sb * NG + (int)((threadIdx.x + NT * i) % (W * NG)),
+                                                p.KG - 1)];
+    if (p.zeros)
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        const int id = threadIdx.x + NT * i, row = id / (W * NG), k = id % (W * NG);
-        zn[T][i] = p.zeros[(size_t)min(n0 + row, p.N - 1) * p.KG + min(sb * NG + k, p.KG - 1)];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NS; ++i) zn[T][i] = 8;
-    }
+      for (int i = 0; i < NS; ++i)
+        zn[T][i] = p.zeros[sp[i] + (unsigned)min(
+                                       sb * NG + (int)((threadIdx.x + NT * i) % (W * NG)),
+                                       p.KG - 1)];
   };
-  auto place = [&](auto turn) {
+  auto place = [&](int sb, auto turn) {
     constexpr int T = decltype(turn)::value;
+    if ((sb + W) * 128 > p.K) {  // the last stage, where it is short
+#pragma unroll
+      for (int i = 0; i < NA; ++i)
+        if (128 * sb + (int)(threadIdx.x + NT * i) % UA * (16 / act_size<A>()) >= p.K)
+          an[i] = intx4{0, 0, 0, 0};
+    }
 #pragma unroll
     for (int i = 0; i < NF; ++i) {
       const int row = (NT * i + threadIdx.x) / UR, unit = threadIdx.x % UR;
@@ -356,12 +355,13 @@ __global__ __launch_bounds__(64 * W) void q4_rows_kernel(Q4Args p) {
     for (int i = 0; i < NS; ++i) {
       const int id = threadIdx.x + NT * i, row = id / (W * NG), k = id % (W * NG);
       if (16 * NF * W * NG % NT == 0 || row < 16 * NF)
-        scales[k * 16 * NF + row] = make_float2(q4_scale(sn[T][i], p.f16), (float)zn[T][i]);
+        scales[k * 16 * NF + row] =
+            make_float2(q4_scale(sn[T][i], p.f16), p.zeros ? (float)zn[T][i] : 8.f);
     }
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
-      const int id = threadIdx.x + NT * i, m = id / UA, c = id % UA;
-      if (m >= p.M) continue;
+      const int m = (NT * i + 64 * wave) / UA, c = (threadIdx.x + NT * i) % UA;
+      if (m >= p.M) break;
       if constexpr (A == kActF32) {
         float v[4];
         __builtin_memcpy(v, &an[i], 16);
@@ -472,7 +472,7 @@ __global__ __launch_bounds__(64 * W) void q4_rows_kernel(Q4Args p) {
     }
   };
   auto step = [&](int sb, auto turn) {
-    place(turn);
+    place(sb, turn);
     __syncthreads();
     // asked for in the order of use, which is the order that loads are waited for in
     if (sb + W < SB) fetch_a(sb + W);
@@ -546,6 +546,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
   constexpr int UA = 8 * act_size<A>();  // 16-byte units of a row of a, of a superblock
   constexpr int NA = KG * BM * UA / TH, NB = (KG * BN * 4 + TH - 1) / TH;
   constexpr int NS = (KG * BN * NG + TH - 1) / TH;
+  constexpr int AHEAD = A == kActBF16 ? 2 : 1;  // stages on their way (registers allow)
   static_assert(KG * BM * UA % TH == 0, "whole loads");
   extern __shared__ __align__(16) unsigned char lds[];
   const int lane = threadIdx.x & 63;
@@ -564,39 +565,60 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
   }
   const int m0 = id % MT * BM, n0 = id / MT * BN;
 
-  intx4 an[NA], bn[NB];
-  float dn[A == kActQ8 ? NA : 1];
-  unsigned short sn[NS];
-  unsigned char zn[NS];
-  // superblock sb + (the group); rows past the end read the last row, and are not stored
-  auto fetch = [&](int sb) {
+  intx4 an[AHEAD][NA], bn[AHEAD][NB];
+  float dn[AHEAD][A == kActQ8 ? NA : 1];
+  unsigned short sn[AHEAD][NS];
+  unsigned char zn[AHEAD][NS];
+  // Where a thread's loads begin (64-bit products cost too much to be formed a stage); rows past
+  // the end read the last row, and are not stored.  As above, past the end of the depth the
+  // last columns are read, and zeros take their place in LDS.
+  const unsigned char *ap[NA], *bp[NB];
+  size_t sp[NS];
+#pragma unroll
+  for (int i = 0; i < NA; ++i)
+    ap[i] = p.a + (size_t)min(m0 + (int)(threadIdx.x + TH * i) / UA % BM, p.M - 1) * p.K *
+                      act_size<A>();
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+    bp[i] = p.codes + (size_t)min(n0 + (int)(threadIdx.x + TH * i) / 4 % BN, p.N - 1) * SB * 64 +
+            (threadIdx.x & 3) * 16;
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+    sp[i] = (size_t)min(n0 + (int)(threadIdx.x + TH * i) / NG % BN, p.N - 1) * p.KG;
+  auto fetch = [&](int sb, auto turn) {
+    constexpr int T = decltype(turn)::value;
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
-      const int at = threadIdx.x + TH * i, row = at / UA, c = at % UA;
-      const int m = min(m0 + row % BM, p.M - 1);
-      const int col = 128 * (sb + row / BM) + c * (16 / act_size<A>());
-      an[i] = intx4{0, 0, 0, 0};
-      if (col < p.K)
-        an[i] = *reinterpret_cast<const intx4*>(p.a + ((size_t)m * p.K + col) * act_size<A>());
-      if constexpr (A == kActQ8) dn[i] = p.ad[(size_t)m * KB + min(col / kQ4Block, KB - 1)];
+      const int at = threadIdx.x + TH * i;
+      const int col = 128 * (sb + at / UA / BM) + at % UA * (16 / act_size<A>());
+      an[T][i] = *reinterpret_cast<const intx4*>(
+          ap[i] + (unsigned)(min(col, p.K - 16 / act_size<A>()) * act_size<A>()));
+      if constexpr (A == kActQ8)
+        dn[T][i] = p.ad[(size_t)(ap[i] - p.a) / kQ4Block + min(col / kQ4Block, KB - 1)];
     }
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      const int at = threadIdx.x + TH * i, row = at / 4;
-      const int n = min(n0 + row % BN, p.N - 1), s = min(sb + row / BN, SB - 1);
-      bn[i] = *reinterpret_cast<const intx4*>(p.codes + ((size_t)n * SB + s) * 64 + (at & 3) * 16);
+      const int s = min(sb + (int)(threadIdx.x + TH * i) / 4 / BN, SB - 1);
+      bn[T][i] = *reinterpret_cast<const intx4*>(bp[i] + (unsigned)(s * 64));
     }
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-      const int at = threadIdx.x + TH * i, row = at / NG, k = at % NG;
-      const size_t g = (size_t)min(n0 + row % BN, p.N - 1) * p.KG +
-                       min((sb + row / BN) * NG + k, p.KG - 1);
-      sn[i] = p.scales[g];
-      zn[i] = 8;
-      if (p.zeros) zn[i] = p.zeros[g];
+      const int at = threadIdx.x + TH * i;
+      const size_t g = sp[i] + (unsigned)min((sb + at / NG / BN) * NG + at % NG, p.KG - 1);
+      sn[T][i] = p.scales[g];
+      if (p.zeros) zn[T][i] = p.zeros[g];
     }
   };
-  auto place = [&](unsigned char* to) {
+  auto place = [&](unsigned char* to, int sb, auto turn) {
+    constexpr int T = decltype(turn)::value;
+    if ((sb + KG) * 128 > p.K) {  // the last stage, where it is short
+#pragma unroll
+      for (int i = 0; i < NA; ++i) {
+        const int at = threadIdx.x + TH * i;
+        if (128 * (sb + at / UA / BM) + at % UA * (16 / act_size<A>()) >= p.K)
+          an[T][i] = intx4{0, 0, 0, 0};
+      }
+    }
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
       const int at = threadIdx.x + TH * i, row = at / UA, c = at % UA, m = row % BM;
@@ -604,20 +626,24 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
       unsigned char* acts = part + L::CODES;
       float total = 0.f;
       if constexpr (A == kActBF16) {
-        reinterpret_cast<intx4*>(acts)[m * 16 + (c ^ (m & 15))] = an[i];
-        float v[8];
-        octet_values(Octet<kActBF16>{an[i]}, v);
+        reinterpret_cast<intx4*>(acts)[m * 16 + (c ^ (m & 15))] = an[T][i];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) total += v[e];
+        for (int e = 0; e < 4; ++e) {
+          bf16x2 v, one;
+          const int u = an[T][i][e], ones = 0x3f803f80;
+          __builtin_memcpy(&v, &u, 4);
+          __builtin_memcpy(&one, &ones, 4);
+          total = __builtin_amdgcn_fdot2_f32_bf16(v, one, total, false);
+        }
       } else {
         constexpr int NV = A == kActF32 ? 4 : 16;  // columns of a unit
         float v[NV];
         if constexpr (A == kActF32) {
-          __builtin_memcpy(v, &an[i], 16);
+          __builtin_memcpy(v, &an[T][i], 16);
         } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            v[e] = (float)((signed char)(an[i][e >> 2] >> (8 * (e & 3)))) * dn[i];
+            v[e] = (float)((signed char)(an[T][i][e >> 2] >> (8 * (e & 3)))) * dn[T][i];
         }
 #pragma unroll
         for (int e = 0; e < NV; ++e) total += v[e];
@@ -653,7 +679,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
       const int at = threadIdx.x + TH * i, row = at / 4, n = row % BN;
       if (KG * BN * 4 % TH == 0 || row < KG * BN)
         reinterpret_cast<intx4*>(to + row / BN * L::PART)[n * 4 + ((at & 3) ^ ((n >> 2) & 3))] =
-            bn[i];
+            bn[T][i];
     }
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
@@ -661,7 +687,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
       if (KG * BN * NG % TH == 0 || row < KG * BN)
         reinterpret_cast<float2*>(to + row / BN * L::PART + L::CODES + L::ACTS +
                                   L::SUMS)[k * BN + row % BN] =
-            make_float2(q4_scale(sn[i], p.f16), (float)zn[i]);
+            make_float2(q4_scale(sn[T][i], p.f16), p.zeros ? (float)zn[T][i] : 8.f);
     }
   };
 
@@ -677,52 +703,65 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
     const unsigned char* acts = part + L::CODES;
     const float* sums = reinterpret_cast<const float*>(acts + L::ACTS);
     const float2* scales = reinterpret_cast<const float2*>(acts + L::ACTS + L::SUMS);
-    intx4 cv[FN][2];
+    // Steps of one plane of one row tile in one group; what the next one needs of the
+    // activations is read while this one is multiplied (one plane: the registers allow it).
+    constexpr int STEPS = FM * PL, EARLY = PL == 1 ? 1 : 0;
+    bf16x8 ax[1 + EARLY][2 * GB];
+    auto read = [&](int k, int step, int to) {
+      const int m = (wm * FM + step / PL) * 32 + r;
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int n = (wn * FN + j) * 32 + r;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        cv[j][u] = reinterpret_cast<const intx4*>(part)[n * 4 + ((2 * u + h) ^ ((n >> 2) & 3))];
-    }
-#pragma unroll
+      for (int b = 0; b < 2 * GB; ++b) {
+        const int unit = 4 * (k * GB + (b >> 1)) + 2 * (b & 1) + h;
+        __builtin_memcpy(&ax[to][b],
+                         __builtin_assume_aligned(
+                             acts + ((step % PL * BM + m) * 16 + (unit ^ (m & 15))) * 16, 16),
+                         16);
+      }
+    };
+#pragma unroll(GS == 0 ? 1 : NG)
     for (int k = 0; k < NG; ++k) {
+      if (EARLY) read(k, 0, 0);
       float2 sz[FN];
       bf16x8 bx[FN][2 * GB];
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        sz[j] = scales[k * BN + (wn * FN + j) * 32 + r];
+        const int n = (wn * FN + j) * 32 + r;
+        sz[j] = scales[k * BN + n];
 #pragma unroll
-        for (int b = 0; b < 2 * GB; ++b) bx[j][b] = q4_to_bf16(cv[j][b & 1][k * GB + (b >> 1)]);
+        for (int u = 0; u < 2; ++u) {
+          int c[GB];  // an octet of each of the group's blocks
+          __builtin_memcpy(
+              c,
+              __builtin_assume_aligned(
+                  part + (n * 4 + ((2 * u + h) ^ ((n >> 2) & 3))) * 16 + k * GB * 4, 4 * GB),
+              4 * GB);
+#pragma unroll
+          for (int b = 0; b < GB; ++b) bx[j][2 * b + u] = q4_to_bf16(c[b]);
+        }
       }
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        const int m = (wm * FM + i) * 32 + r;
-        floatx16 c, t[FN];
+        floatx16 t[FN];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const floatx4 s = *reinterpret_cast<const floatx4*>(
+          const floatx4 c = *reinterpret_cast<const floatx4*>(
               sums + k * BM + (wm * FM + i) * 32 + 8 * v + 4 * h);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) c[4 * v + e] = s[e];
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[j][4 * v + e] = sz[j].y * c[e];
         }
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
+        for (int l = 0; l < PL; ++l) {
+          const int step = i * PL + l;
+          if (step + EARLY < STEPS) read(k, step + EARLY, (step + EARLY) & EARLY);
 #pragma unroll
-          for (int v = 0; v < 16; ++v) t[j][v] = sz[j].y * c[v];
-#pragma unroll
-        for (int l = 0; l < PL; ++l)
-#pragma unroll
-          for (int b = 0; b < 2 * GB; ++b) {
-            const int unit = 4 * (k * GB + (b >> 1)) + 2 * (b & 1) + h;
-            bf16x8 ax;
-            __builtin_memcpy(&ax,
-                             __builtin_assume_aligned(
-                                 acts + ((l * BM + m) * 16 + (unit ^ (m & 15))) * 16, 16), 16);
+          for (int b = 0; b < 2 * GB; ++b)
 #pragma unroll
             for (int j = 0; j < FN; ++j)
-              t[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ax, bx[j][b], t[j], 0, 0, 0);
-          }
+              t[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ax[step & EARLY][b], bx[j][b], t[j],
+                                                              0, 0, 0);
+        }
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
@@ -731,15 +770,26 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
     }
   };
 
-  fetch(0);
-  int turn = 0;
-  for (int sb = 0; sb < SB; sb += KG, turn ^= L::BUFS - 1) {
-    unsigned char* stage = lds + turn * L::STAGE;
+  auto step = [&](int sb, auto turn) {
+    constexpr int T = decltype(turn)::value;
+    unsigned char* stage = lds + T % L::BUFS * L::STAGE;
     if (L::BUFS == 1 && sb > 0) __syncthreads();
-    place(stage);
+    place(stage, sb, std::integral_constant<int, T % AHEAD>{});
     __syncthreads();  // (of two buffers, the one written next was read before this)
-    if (sb + KG < SB) fetch(sb + KG);
+    if (sb + AHEAD * KG < SB) fetch(sb + AHEAD * KG, std::integral_constant<int, T % AHEAD>{});
     if (KG == 1 || sb + kg < SB) multiply(stage + kg * L::PART);
+  };
+  constexpr std::integral_constant<int, 0> even{};
+  constexpr std::integral_constant<int, 1> odd{};
+  fetch(0, even);
+  if (AHEAD > 1 && KG < SB) fetch(KG, std::integral_constant<int, 1 % AHEAD>{});
+  if constexpr (AHEAD == 1 && L::BUFS == 1) {
+    for (int sb = 0; sb < SB; sb += KG) step(sb, even);
+  } else {
+    for (int sb = 0; sb < SB; sb += 2 * KG) {
+      step(sb, even);
+      if (sb + KG < SB) step(sb + KG, odd);
+    }
   }
   if constexpr (KG > 1) {
     float4* last = reinterpret_cast<float4*>(lds);
@@ -822,8 +872,37 @@ void launch_q4_vector(const Q4Args& p, hipStream_t st) {
   const long want = ((long)p.N * KS + 4096L * R - 1) / (4096L * R);
   const int iters = want < 1 ? 1 : want > most ? most : (int)want;
   const int rows = W / KS * R * iters;
-  hipLaunchKernelGGL((q4_vector_kernel<A, GS, R, W>), dim3((p.N + rows - 1) / rows),
-                     dim3(64 * W), 0, st, p, KS, iters);
+  const dim3 grid((p.N + rows - 1) / rows);
+  if (p.zeros)
+    hipLaunchKernelGGL((q4_vector_kernel<A, GS, true, R, W>), grid, dim3(64 * W), 0, st, p, KS,
+                       iters);
+  else
+    hipLaunchKernelGGL((q4_vector_kernel<A, GS, false, R, W>), grid, dim3(64 * W), 0, st, p, KS,
+                       iters);
+}
+// Tiles by the rounds of 256 blocks they take: the smallest that need one, with several groups
+// of waves on each; us in 32 x 64 / 32 x 128 / 64 x 128 / 128 x 128: 48 x 7168 x 7168 26 / 35 /
+// 50 / 83, 64 x 16384 x 4096 30 / 23 / 32 / 49, 100 x 7168 x 7168 46 / 35 / 51 / 88, 128 x
+// 16384 x 4096 56 / 41 / 34 / 52, 512 x 4096 x 4096 56 / 39 / 33 / 52; past one round 333 x
+// 7168 x 7168 116 / 116 / 105 / 95, 512 x 16384 x 4096 212 / 146 / 117 / 103.  With three
+// planes a tile's cost goes with its size, and small ones waste less of the last round: 333 x
+// 7168 x 7168 in 32 x 128 and 128 x 128 172 and 225, 512 x 8192 x 4096 (groups of 32) 187 and
+// 153.
+template <int A, int GS>
+void launch_q4_tiles(const Q4Args& p, hipStream_t st) {
+  auto blocks = [&](long bm, long bn) {
+    return ((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn);
+  };
+  auto rounds = [&](long bm, long bn) { return (blocks(bm, bn) + 255) / 256; };
+  if (blocks(32, 64) <= 256)
+    launch_q4_tile<A, GS, 1, 1, 1, 2, 4>(p, st);
+  else if (blocks(32, 128) <= 256 ||
+           (A != kActBF16 && 5 * rounds(32, 128) <= 16 * rounds(128, 128)))
+    launch_q4_tile<A, GS, 1, 1, 1, 4, 2>(p, st);
+  else if (blocks(64, 128) <= 256)
+    launch_q4_tile<A, GS, 2, 1, 1, 4, 2>(p, st);
+  else
+    launch_q4_tile<A, GS, 2, 1, 2, 4, 1>(p, st);
 }
 template <int A, int GS>
 void launch_q4_g(const Q4Args& p, hipStream_t st) {
@@ -833,12 +912,8 @@ void launch_q4_g(const Q4Args& p, hipStream_t st) {
     launch_q4_few<A, GS, true>(p, st);
   else if (p.M <= 16)
     launch_q4_few<A, GS, false>(p, st);
-  else if (p.M <= 32)
-    launch_q4_tile<A, GS, 1, 1, 1, 2, 4>(p, st);
-  else if (p.M <= 64)
-    launch_q4_tile<A, GS, 2, 1, 1, 4, 2>(p, st);
   else
-    launch_q4_tile<A, GS, 2, 1, 2, 4, 1>(p, st);
+    launch_q4_tiles<A, GS>(p, st);
 }
 template <int A>
 void launch_q4_a(const Q4Args& p, int group, hipStream_t st) {

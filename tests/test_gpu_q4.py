@@ -111,12 +111,13 @@ def _bound(kind, K, group, a, size, w):
     """Products are exact.  A matrix instruction adds 32 of them to its sum with at most 33
     roundings, a group has group/32 of them for each plane of a; the group's two sums are put
     together in 2 and added to the others in K/group more and one for each of 16 waves.  int8
-    blocks are exact: one rounding a block, then as above."""
-    planes = 3 if kind == "f32" else 1
+    blocks of up to 16 rows are exact: one rounding a block, then as above; past that their
+    values are rounded once and then go as fp32 does."""
+    planes = 1 if kind == "bf16" else 3
     kg = -(-K // group)
-    if kind == "q8":
+    if kind == "q8" and a.shape[0] <= 16:
         return (group // 32 + 3 + kg + 18) * ULP * (a.abs() @ w.abs().t())
-    n = 33 * group // 32 * planes + 4 + kg + 18
+    n = 33 * group // 32 * planes + 5 + kg + 18
     return n * ULP * (a.abs() @ size.t())
 
 
