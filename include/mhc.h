@@ -509,11 +509,12 @@ int mhc_site_pre_bwd(const void* x, const unsigned char* x_scales, const float* 
  *   dgate   [gate_rows][H] fp32 out, NULL without a gate
  *   work, work_bytes   device scratch of the caller, at least mhc_norm_bwd_work_bytes
  *     bytes (MHC_EINVAL if less); in use until the call's work is done
- * hidden <= 16384 (MHC_EUNSUPPORTED above).  T = 0 does nothing but to zero the sums over
+ * hidden <= 8192 (MHC_EUNSUPPORTED above).  T = 0 does nothing but to zero the sums over
  * tokens.  Sums are fp32, those over tokens added in an order fixed by the shape: equal
  * inputs give equal bits.  A token's squares must stay within fp32.
  *
- * mhc_norm_bwd_work_bytes: 0 for T < 1 or a hidden that the calls reject.
+ * mhc_norm_bwd_work_bytes: 0 for T < 1 or a hidden that the calls reject, and where the
+ *   calls need none (a few short rows; work may be NULL then).
  */
 enum { MHC_GATE_PLAIN = 0, MHC_GATE_SIGMOID = 1, MHC_GATE_SILU = 2 };
 

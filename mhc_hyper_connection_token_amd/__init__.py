@@ -834,13 +834,13 @@ def branch_norm(y, nw, eps: float = 1e-5, *, dtype=None, out=None, stream=None):
         raise ValueError("the norm is float32 or bfloat16")
     f32 = torch.float32
     py, pn = _gpu(y, "y", f32), _gpu(nw, "nw", f32, (H,))
+    bf16 = dtype != f32
     if out is None:
-        out = torch.empty((T, H), device=y.device, dtype=dtype)
+        out = y.new_empty((T, H), dtype=dtype) if bf16 else y.new_empty((T, H))
         po = out.data_ptr()
     else:
         po = _gpu(out, "out", dtype, (T, H))
-    _call("mhc_branch_norm", y.get_device(),
-          (py, pn, T, H, float(eps), po, int(dtype == torch.bfloat16)), (nw, out))
+    _call("mhc_branch_norm", y.get_device(), (py, pn, T, H, eps, po, bf16), (nw, out))
     return out
 
 
@@ -849,11 +849,28 @@ def norm_bwd_work_bytes(T: int, hidden: int) -> int:
     return int(load_library().mhc_norm_bwd_work_bytes(T, hidden))
 
 
-def _norm_work(work, T, H, device):
+def _norm_work(work, T, H, like):
+    """The scratch of a call, its address and size; none where none is needed or given."""
     import torch
     if work is None:
-        work = torch.empty(norm_bwd_work_bytes(T, H), device=device, dtype=torch.uint8)
-    return work, _gpu(work, "work", torch.uint8)
+        need = load_library().mhc_norm_bwd_work_bytes(T, H)
+        if need == 0:
+            return None, None, 0
+        work = like.new_empty(need, dtype=torch.uint8)
+        return work, work.data_ptr(), need
+    return work, _gpu(work, "work", torch.uint8), work.numel()
+
+
+def _new_or(out, names, shapes, like):
+    """The float32 outputs of a call, new ones (of `like`, float32) or as given, checked, and
+    their addresses."""
+    if out is None:
+        out = tuple([like.new_empty(s) for s in shapes])
+        return out, [o.data_ptr() for o in out]
+    if len(out) != len(shapes):
+        raise ValueError(f"out must hold {len(shapes)} tensors")
+    f32 = like.dtype
+    return out, [_gpu(o, n, f32, s) for o, n, s in zip(out, names, shapes)]
 
 
 def branch_norm_bwd(dz, y, nw, eps: float = 1e-5, *, out=None, work=None, stream=None):
@@ -870,11 +887,11 @@ def branch_norm_bwd(dz, y, nw, eps: float = 1e-5, *, out=None, work=None, stream
     f32 = torch.float32
     pz, z_bf16 = _typed(dz, "dz")
     py, pys, ty = _kept(y, "y", (T,), H)
-    out, po = _outputs(out, ("dy", "dnw"), ((T, H), (H,)), (f32, f32), dz.device)
-    work, pw = _norm_work(work, T, H, dz.device)
+    pn = _gpu(nw, "nw", f32, (H,))
+    out, po = _new_or(out, ("dy", "dnw"), ((T, H), (H,)), nw)
+    work, pw, nbytes = _norm_work(work, T, H, nw)
     _call("mhc_branch_norm_bwd", dz.get_device(),
-          (pz, z_bf16, py, pys, _gpu(nw, "nw", f32, (H,)), T, H, float(eps), *po, pw,
-           work.numel()), (*ty, nw, *out, work))
+          (pz, z_bf16, py, pys, pn, T, H, eps, *po, pw, nbytes), (*ty, nw, *out, work))
     return out
 
 
@@ -894,15 +911,15 @@ def site_post_norm(x, f, nw, post, comb, eps: float = 1e-5, *, gate=None, gate_a
     T, S, H = x.shape
     f32 = torch.float32
     px = _gpu(x, "x", f32)
+    args = (px, *_typed(f, "f", (T, H)), _gpu(nw, "nw", f32, (H,)), *_gate(gate, gate_act, T, H),
+            alpha, _gpu(post, "post", f32, (T, S)), _gpu(comb, "comb", f32, (T, S, S)), T, S, H,
+            eps)
     if out is None:
-        out = torch.empty((T, S, H), device=x.device, dtype=f32)
+        out = x.new_empty((T, S, H))
         po = out.data_ptr()
     else:
         po = _gpu(out, "out", f32, (T, S, H))
-    _call("mhc_site_post_norm", x.get_device(),
-          (px, *_typed(f, "f", (T, H)), _gpu(nw, "nw", f32, (H,)), *_gate(gate, gate_act, T, H),
-           float(alpha), _gpu(post, "post", f32, (T, S)), _gpu(comb, "comb", f32, (T, S, S)), T,
-           S, H, float(eps), po), (f, nw, gate, post, comb, out))
+    _call("mhc_site_post_norm", x.get_device(), (*args, po), (f, nw, gate, post, comb, out))
     return out
 
 
@@ -937,14 +954,13 @@ def site_post_norm_bwd(g, x, f, nw, post, comb, eps: float = 1e-5, *, gate=None,
         if len(out) != 6 or out[5] is not None:
             raise ValueError("out must hold 5 tensors and None, the gradient of no gate")
         out = out[:5]
-    out, po = _outputs(out, names, shapes, (f32,) * len(shapes), g.device)
+    args = (pg, px, pxs, pf, f_bf16, pfs, _gpu(nw, "nw", f32, (H,)), *how, alpha,
+            _gpu(post, "post", f32, (T, S)), _gpu(comb, "comb", f32, (T, S, S)), T, S, H, eps)
+    out, po = _new_or(out, names, shapes, g)
     if gate is None:
         out, po = (*out, None), [*po, None]
-    work, pw = _norm_work(work, T, H, g.device)
-    _call("mhc_site_post_norm_bwd", g.get_device(),
-          (pg, px, pxs, pf, f_bf16, pfs, _gpu(nw, "nw", f32, (H,)), *how, float(alpha),
-           _gpu(post, "post", f32, (T, S)), _gpu(comb, "comb", f32, (T, S, S)), T, S, H,
-           float(eps), *po, pw, work.numel()),
+    work, pw, nbytes = _norm_work(work, T, H, g)
+    _call("mhc_site_post_norm_bwd", g.get_device(), (*args, *po, pw, nbytes),
           (*tx, *tf, nw, gate, post, comb, *out, work))
     return out
 
@@ -990,16 +1006,26 @@ def _q4_weight(codes, scales, zeros, K):
         raise ValueError("K must be a multiple of 32")
     N, kg = scales.shape
     # the group size that gives this many groups (where two do, there is one group)
-    group = next((g for g in (128, 64, 32) if -(-K // g) == kg), None)
-    if group is None:
+    if kg == (K + 127) // 128:
+        group = 128
+    elif kg == (K + 63) // 64:
+        group = 64
+    elif kg == K // 32:
+        group = 32
+    else:
         raise ValueError(f"scales has {kg} groups a row: none of 32, 64 and 128 columns gives "
                          f"that at K = {K}")
-    if scales.dtype not in (torch.bfloat16, torch.float16):
+    dtype = scales.dtype
+    if dtype == torch.bfloat16:
+        kind = 1
+    elif dtype == torch.float16:
+        kind = 2
+    else:
         raise ValueError("scales must be bfloat16 or float16")
     pc = _gpu(codes, "codes", torch.uint8, (N, _blocks(K) * 64))
-    ps = _gpu(scales, "scales", scales.dtype)
+    ps = _gpu(scales, "scales", dtype)
     pz = None if zeros is None else _gpu(zeros, "zeros", torch.uint8, (N, kg))
-    return pc, ps, 1 if scales.dtype == torch.bfloat16 else 2, pz, N, group
+    return pc, ps, kind, pz, N, group
 
 
 def q4_encode(w, *, group: int = 128, zeros: bool = False, out=None, stream=None):
@@ -1066,12 +1092,12 @@ def q4_matmul(a, codes, scales, zeros=None, *, dtype=None, out=None, stream=None
     else:
         (pa, a_type), pd, others = _typed(a, "a"), None, (codes, scales, zeros)
     if out is None:
-        out = torch.empty((M, N), device=q.device, dtype=dtype)
+        out = q.new_empty((M, N), dtype=dtype)
         po = out.data_ptr()
     else:
         po = _gpu(out, "out", dtype, (M, N))
     _call("mhc_q4_matmul", q.get_device(),
-          (pa, a_type, pd, pc, ps, kind, pz, M, N, K, group, po, int(dtype == torch.bfloat16)),
+          (pa, a_type, pd, pc, ps, kind, pz, M, N, K, group, po, dtype == torch.bfloat16),
           (*others, out))
     return out
 

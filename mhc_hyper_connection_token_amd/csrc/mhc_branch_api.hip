@@ -17,7 +17,7 @@ using mhc::span;
 
 namespace {
 
-constexpr int kMaxNormHidden = 16384;  // a row that a block's registers hold
+constexpr int kMaxNormHidden = 8192;  // a row that a block's registers hold
 constexpr int kMaxQ4Rows = 1 << 24;    // these three bound the launch grids
 constexpr int kMaxQ4Cols = 1 << 20;
 constexpr int kMaxQ4Tokens = 1 << 20;
@@ -99,10 +99,10 @@ int mhc_branch_norm_bwd_check(const void* dz, int dz_type, const void* y,
   if (!real_type(dz_type) || !dnw) return MHC_EINVAL;
   if ((rc = check_ptr(dnw))) return rc;
   if (T == 0) return MHC_OK;
-  const void* ptrs[] = {dz, y, nw, dy, work};
-  if ((rc = check_ptrs(ptrs, 5))) return rc;
-  if (y_scales && (rc = check_ptr(y_scales))) return rc;
   const size_t H = hidden, n = T * H, need = mhc_norm_bwd_work_bytes(T, hidden);
+  const void* ptrs[] = {dz, y, nw, dy, work};
+  if ((rc = check_ptrs(ptrs, need ? 5 : 4))) return rc;
+  if (y_scales && (rc = check_ptr(y_scales))) return rc;
   if (work_bytes < need) return MHC_EINVAL;
   const Pair py = kept_span(y, y_scales, T, H);
   const Span in[] = {span(dz, n * type_size(dz_type)), py.codes, py.scales, span(nw, H * 4)};
@@ -176,11 +176,11 @@ int mhc_site_post_norm_bwd_check(const float* g, const void* x, const unsigned c
   if ((rc = check_ptr(dnw)) || (dgate && (rc = check_ptr(dgate)))) return rc;
   const Span sums[] = {span(dnw, H * 4), span(dgate, dgate ? gate_rows * H * 4 : 0)};
   if (T == 0) return check_apart(sums, 2, nullptr, 0);
+  const size_t need = mhc_norm_bwd_work_bytes(T, hidden);
   const void* ptrs[] = {g, x, f, nw, post, comb, dx, df, dpost, dcomb, work};
-  if ((rc = check_ptrs(ptrs, 11))) return rc;
+  if ((rc = check_ptrs(ptrs, need ? 11 : 10))) return rc;
   if (x_scales && (rc = check_ptr(x_scales))) return rc;
   if (f_scales && (rc = check_ptr(f_scales))) return rc;
-  const size_t need = mhc_norm_bwd_work_bytes(T, hidden);
   if (work_bytes < need) return MHC_EINVAL;
   const Pair px = kept_span(x, x_scales, Tz * S, H), pf = kept_span(f, f_scales, Tz, H);
   const Span in[] = {span(g, Tz * S * H * 4), px.codes, px.scales,

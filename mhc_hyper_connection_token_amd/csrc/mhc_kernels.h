@@ -195,6 +195,7 @@ struct PostNorm {
   float* x_out;
   float alpha;
   int f_kind, gate_kind, gate_rows, gate_act;
+  int stream = 0;  // stores that do not stay in the cache; set at the launch
 };
 hipError_t launch_post_norm(const PostNorm& p, int T, int S, int H, float eps, hipStream_t st);
 
@@ -209,6 +210,7 @@ struct NormBwd {
   float* dy;
   float* dnw;
   int dz_kind;
+  int stream = 0;  // as above
 };
 struct PostNormBwd {
   const float* g;
@@ -228,6 +230,7 @@ struct PostNormBwd {
   float* dgate;
   float alpha;
   int f_kind, gate_kind, gate_rows, gate_act;
+  int stream = 0;  // as above
 };
 size_t norm_bwd_work_bytes(int T, int H, int sums);
 hipError_t launch_norm_bwd(const NormBwd& p, int T, int H, float eps, void* work, hipStream_t st);

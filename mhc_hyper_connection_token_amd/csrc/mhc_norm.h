@@ -6,35 +6,57 @@
 
 namespace mhc {
 
-typedef unsigned uintx4 __attribute__((ext_vector_type(4)));
-
-// Four entries of a row as they lie in memory: fp32, bf16, or e4m3 codes with their
-// scale byte.  The type is the same for a whole launch, so the branch is uniform, and
-// nothing in it waits for the load: the values are made where they are used.
+// Four entries of a row as they lie in memory: fp32, bf16, or e4m3 codes with their scale
+// byte.  (The type is a template's: loads of one that is known at run time end up behind
+// branches, each of which waits for the loads before it.)
 enum Kind { kF32 = 0, kBF16 = 1, kF8 = 2 };
 
-__device__ __forceinline__ uintx4 load_raw(const void* p, const unsigned char* s, int kind,
-                                           size_t row, int HQ, int KB, int q) {
-  uintx4 v{0u, 0u, 0u, 0u};
-  if (kind == kF32) {
-    v = __builtin_nontemporal_load(static_cast<const uintx4*>(p) + row * HQ + q);
-  } else if (kind == kBF16) {
-    const uintx2 h = __builtin_nontemporal_load(static_cast<const uintx2*>(p) + row * HQ + q);
-    v[0] = h[0];
-    v[1] = h[1];
+template <int KIND>
+struct Raw;
+template <>
+struct Raw<kF32> {
+  floatx4 v;
+};
+template <>
+struct Raw<kBF16> {
+  uintx2 v;
+};
+template <>
+struct Raw<kF8> {
+  unsigned v, scale;
+};
+
+// Quad q of row `row` of [rows][4 * HQ]; s and KB: the scale bytes of 8-bit blocks.
+template <int KIND>
+__device__ __forceinline__ Raw<KIND> load_raw(const void* p, const unsigned char* s, size_t row,
+                                              int HQ, int KB, int q) {
+  Raw<KIND> r;
+  if constexpr (KIND == kF32) {
+    r.v = __builtin_nontemporal_load(static_cast<const floatx4*>(p) + row * HQ + q);
+  } else if constexpr (KIND == kBF16) {
+    r.v = __builtin_nontemporal_load(static_cast<const uintx2*>(p) + row * HQ + q);
   } else {
-    v[0] = __builtin_nontemporal_load(static_cast<const unsigned*>(p) + row * KB * 32 + q);
-    v[1] = s[row * KB + (q >> 5)];
+    r.v = __builtin_nontemporal_load(static_cast<const unsigned*>(p) + row * KB * 32 + q);
+    r.scale = s[row * KB + (q >> 5)];
   }
-  return v;
+  return r;
 }
-__device__ __forceinline__ float4 raw_values(uintx4 v, int kind) {
-  if (kind == kF8) return f8_unpack(v[0], f8_scale(v[1]));
-  const bool h = kind == kBF16;
-  return make_float4(__uint_as_float(h ? v[0] << 16 : v[0]),
-                     __uint_as_float(h ? v[0] & 0xffff0000u : v[1]),
-                     __uint_as_float(h ? v[1] << 16 : v[2]),
-                     __uint_as_float(h ? v[1] & 0xffff0000u : v[3]));
+__device__ __forceinline__ float4 raw_values(Raw<kF32> r) {
+  return make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+}
+__device__ __forceinline__ float4 raw_values(Raw<kBF16> r) {
+  return make_float4(__uint_as_float(r.v[0] << 16), __uint_as_float(r.v[0] & 0xffff0000u),
+                     __uint_as_float(r.v[1] << 16), __uint_as_float(r.v[1] & 0xffff0000u));
+}
+__device__ __forceinline__ float4 raw_values(Raw<kF8> r) {
+  return f8_unpack(r.v, f8_scale(r.scale));
+}
+
+// A gate: none, or one of the kinds.
+enum Gate { kNoGate = 0, kGateF32 = 1, kGateBF16 = 2 };
+template <int GATE>
+constexpr int gate_kind() {
+  return GATE == kGateBF16 ? kBF16 : kF32;
 }
 
 // The factor a(g) of a gate and its slope a'(g).  With t = exp(-|g|) and d = 1/(1+t),
@@ -73,7 +95,20 @@ __device__ __forceinline__ float4 fma4(float4 a, float4 b, float4 c) {
   return make_float4(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y), fmaf(a.z, b.z, c.z),
                      fmaf(a.w, b.w, c.w));
 }
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
 __device__ __forceinline__ float4 zero4() { return make_float4(0.f, 0.f, 0.f, 0.f); }
+
+// What the memory-side cache can hold of the outputs until the next kernel reads them; past
+// its size stores that stay in it only displace (measured at the post mix's gradient).
+constexpr size_t kCacheBytes = size_t(256) << 20;
+__device__ __forceinline__ void store_out(float* p, float4 v, int stream) {
+  if (stream)
+    nt_store4(p, v);
+  else
+    *reinterpret_cast<float4*>(p) = v;
+}
 
 __device__ __forceinline__ float wave_total(float v) {  // sum_wave, in every lane
   return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(sum_wave(v))));

@@ -19,9 +19,9 @@ __device__ __forceinline__ float to_bf16(float v) {  // the value, rounded to ne
 }  // namespace
 
 // Codes of padding columns (past K, up to a multiple of 128) are zero.
-template <int G>
-__global__ __launch_bounds__(256) void q4_encode_kernel(const void* __restrict__ w, int kind,
-                                                        int N, int K, int KG,
+template <int G, int KIND>
+__global__ __launch_bounds__(256) void q4_encode_kernel(const void* __restrict__ w, int N,
+                                                        int K, int KG,
                                                         unsigned char* __restrict__ codes,
                                                         __hip_bfloat16* __restrict__ scales,
                                                         unsigned char* __restrict__ zeros) {
@@ -35,7 +35,7 @@ __global__ __launch_bounds__(256) void q4_encode_kernel(const void* __restrict__
     const int q = in ? (int)(at - n * PQ) : 0;
     const bool real = in && q * 4 < K;
     float4 v = zero4();
-    if (real) v = raw_values(load_raw(w, nullptr, kind, n, K / 4, 0, q), kind);
+    if (real) v = raw_values(load_raw<KIND>(w, nullptr, n, K / 4, 0, q));
     const float x[4] = {v.x, v.y, v.z, v.w};
     float lo = 0.f, hi = 0.f;
 #pragma unroll
@@ -108,21 +108,31 @@ unsigned blocks_for(size_t threads) {
 }
 }  // namespace
 
+namespace {
+template <int G>
+void launch_q4_encode_g(const void* w, bool bf16, int N, int K, unsigned char* codes,
+                        __hip_bfloat16* scales, unsigned char* zeros, hipStream_t st) {
+  const int KG = (K + G - 1) / G;
+  const dim3 grid(blocks_for((size_t)N * ((K + 127) / 128 * 32)));
+  if (bf16)
+    hipLaunchKernelGGL((q4_encode_kernel<G, kBF16>), grid, dim3(256), 0, st, w, N, K, KG, codes,
+                       scales, zeros);
+  else
+    hipLaunchKernelGGL((q4_encode_kernel<G, kF32>), grid, dim3(256), 0, st, w, N, K, KG, codes,
+                       scales, zeros);
+}
+}  // namespace
+
 hipError_t launch_q4_encode(const void* w, bool bf16, int N, int K, int group,
                             unsigned char* codes, void* scales, unsigned char* zeros,
                             hipStream_t st) {
-  const int KG = (K + group - 1) / group, kind = bf16 ? kBF16 : kF32;
-  const dim3 grid(blocks_for((size_t)N * ((K + 127) / 128 * 32)));
   __hip_bfloat16* s = static_cast<__hip_bfloat16*>(scales);
   if (group == 32)
-    hipLaunchKernelGGL(q4_encode_kernel<32>, grid, dim3(256), 0, st, w, kind, N, K, KG, codes, s,
-                       zeros);
+    launch_q4_encode_g<32>(w, bf16, N, K, codes, s, zeros, st);
   else if (group == 64)
-    hipLaunchKernelGGL(q4_encode_kernel<64>, grid, dim3(256), 0, st, w, kind, N, K, KG, codes, s,
-                       zeros);
+    launch_q4_encode_g<64>(w, bf16, N, K, codes, s, zeros, st);
   else
-    hipLaunchKernelGGL(q4_encode_kernel<128>, grid, dim3(256), 0, st, w, kind, N, K, KG, codes,
-                       s, zeros);
+    launch_q4_encode_g<128>(w, bf16, N, K, codes, s, zeros, st);
   return hipGetLastError();
 }
 

@@ -718,7 +718,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
                          16);
       }
     };
-#pragma unroll(GS == 0 ? 1 : NG)
+    constexpr int ROLL = GS == 0 ? 1 : NG;
+#pragma unroll ROLL
     for (int k = 0; k < NG; ++k) {
       if (EARLY) read(k, 0, 0);
       float2 sz[FN];

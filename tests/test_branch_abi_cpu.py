@@ -25,8 +25,8 @@ def norm(**kw):
 
 @pytest.mark.parametrize("kw,code", [
     ({}, OK), (dict(z_type=1), OK), (dict(T=0, y=None, nw=None, z=None), OK),
-    (dict(H=16384), OK), (dict(H=16388), EUNSUP), (dict(T=1 << 23), EUNSUP),
-    (dict(T=1 << 18, H=8192), EUNSUP), (dict(T=-1), EINVAL), (dict(H=0), EINVAL),
+    (dict(H=8192), OK), (dict(H=8196), EUNSUP), (dict(T=1 << 23), EUNSUP),
+    (dict(T=1 << 19, H=4096), EUNSUP), (dict(T=-1), EINVAL), (dict(H=0), EINVAL),
     (dict(H=262), EALIGN), (dict(z_type=2), EINVAL), (dict(z_type=-1), EINVAL),
     (dict(eps=0.0), EINVAL), (dict(eps=-1e-5), EINVAL), (dict(eps=NAN), EINVAL),
     (dict(eps=INF), EINVAL), (dict(nw=None), EINVAL), (dict(y=A[0] + 8), EALIGN),
@@ -45,7 +45,7 @@ def norm_bwd(**kw):
 @pytest.mark.parametrize("kw,code", [
     ({}, OK), (dict(dz_type=1), OK), (dict(ys=A[6]), OK),
     (dict(T=0, dz=None, y=None, work=None, nbytes=0), OK), (dict(T=0, dnw=None), EINVAL),
-    (dict(dz_type=2), EINVAL), (dict(H=16388), EUNSUP), (dict(H=258), EALIGN),
+    (dict(dz_type=2), EINVAL), (dict(H=8196), EUNSUP), (dict(H=258), EALIGN),
     (dict(eps=0.0), EINVAL), (dict(dy=None), EINVAL), (dict(work=None), EINVAL),
     (dict(nbytes=mhc.norm_bwd_work_bytes(9, 260) - 1), EINVAL), (dict(work=A[5] + 4), EALIGN),
     (dict(ys=A[6] + 1), EALIGN), (dict(dy=A[0]), EOVERLAP), (dict(dy=A[1]), EOVERLAP),
@@ -67,7 +67,7 @@ def post(**kw):
     (dict(T=0, x=None, rows=1), OK), (dict(alpha=NAN), EINVAL), (dict(alpha=-INF), EINVAL),
     (dict(gate=None, alpha=NAN), EINVAL), (dict(f_type=2), EINVAL), (dict(gate_type=2), EINVAL),
     (dict(act=3), EINVAL), (dict(act=-1), EINVAL), (dict(rows=2), EINVAL), (dict(rows=0), EINVAL),
-    (dict(gate=A[3] + 4), EALIGN), (dict(S=9), EUNSUP), (dict(H=16388), EUNSUP),
+    (dict(gate=A[3] + 4), EALIGN), (dict(S=9), EUNSUP), (dict(H=8196), EUNSUP),
     (dict(H=262), EALIGN), (dict(eps=NAN), EINVAL), (dict(comb=None), EINVAL),
     (dict(out=A[0]), EOVERLAP), (dict(out=A[1]), EOVERLAP), (dict(out=A[3] + 9 * 1040 - 16), EOVERLAP),
     (dict(out=A[3] + 9 * 1040), OK), (dict(out=A[3] + 1040, rows=1), OK)])
@@ -90,7 +90,7 @@ def post_bwd(**kw):
     (dict(T=0, rows=1, g=None, dx=None, work=None, nbytes=0), OK),
     (dict(T=0, rows=1, dgate=None), EINVAL), (dict(T=0, rows=0, dgate=None), OK),
     (dict(T=0, dnw=None), EINVAL), (dict(dnw=None), EINVAL), (dict(dcomb=None), EINVAL),
-    (dict(nbytes=64), EINVAL), (dict(S=9), EUNSUP), (dict(H=16388), EUNSUP),
+    (dict(nbytes=64), EINVAL), (dict(S=9), EUNSUP), (dict(H=8196), EUNSUP),
     (dict(xs=A[14] + 8), EALIGN), (dict(dgate=A[12] + 8), EALIGN), (dict(dx=A[0]), EOVERLAP),
     (dict(df=A[2]), EOVERLAP), (dict(dgate=A[4]), EOVERLAP), (dict(dnw=A[3]), EOVERLAP),
     (dict(dgate=A[11]), EOVERLAP), (dict(work=A[8]), EOVERLAP),
@@ -138,7 +138,7 @@ def test_q4_matmul_check(kw, code):
 def test_calls_refuse_before_any_gpu_work(lib):
     assert lib.mhc_branch_norm(A[0], A[1], 4, 6, 1e-5, A[2], 0, None) == EALIGN
     assert lib.mhc_branch_norm(A[0], A[1], 0, 8, 1e-5, A[2], 0, None) == OK
-    assert lib.mhc_branch_norm_bwd(A[0], 0, A[1], None, A[2], 4, 8, 1e-5, A[3], A[4], A[5], 8,
+    assert lib.mhc_branch_norm_bwd(A[0], 0, A[1], None, A[2], 9, 8, 1e-5, A[3], A[4], A[5], 8,
                                    None) == EINVAL
     assert lib.mhc_site_post_norm(A[0], A[1], 0, A[2], None, 0, 1, 0, 1.0, A[3], A[4], 4, 4, 128,
                                   0.0, A[5], None) == EINVAL
@@ -152,8 +152,10 @@ def test_calls_refuse_before_any_gpu_work(lib):
 def test_work_bytes():
     assert mhc.norm_bwd_work_bytes(0, 4096) == 0
     assert mhc.norm_bwd_work_bytes(4, 4098) == 0
-    assert mhc.norm_bwd_work_bytes(4, 16388) == 0
-    assert 0 < mhc.norm_bwd_work_bytes(1, 4) <= mhc.norm_bwd_work_bytes(5000, 4)
+    assert mhc.norm_bwd_work_bytes(4, 8196) == 0
+    assert mhc.norm_bwd_work_bytes(4, 1024) == 0  # a few short rows need none
+    assert 0 < mhc.norm_bwd_work_bytes(5, 4) <= mhc.norm_bwd_work_bytes(5000, 4)
+    assert norm_bwd(T=4, work=None, nbytes=0) == OK and post_bwd(T=4, rows=4, work=None, nbytes=0) == OK
     # less than the row's own tensor at the production site
     assert mhc.norm_bwd_work_bytes(4096, 4096) < 4096 * 4096 * 4
 
