@@ -840,7 +840,7 @@ def branch_norm(y, nw, eps: float = 1e-5, *, dtype=None, out=None, stream=None):
         po = out.data_ptr()
     else:
         po = _gpu(out, "out", dtype, (T, H))
-    _call("mhc_branch_norm", y.get_device(), (py, pn, T, H, eps, po, bf16), (nw, out))
+    _call("mhc_branch_norm", y.get_device(), (py, pn, T, H, float(eps), po, bf16), (nw, out))
     return out
 
 
@@ -891,7 +891,8 @@ def branch_norm_bwd(dz, y, nw, eps: float = 1e-5, *, out=None, work=None, stream
     out, po = _new_or(out, ("dy", "dnw"), ((T, H), (H,)), nw)
     work, pw, nbytes = _norm_work(work, T, H, nw)
     _call("mhc_branch_norm_bwd", dz.get_device(),
-          (pz, z_bf16, py, pys, pn, T, H, eps, *po, pw, nbytes), (*ty, nw, *out, work))
+          (pz, z_bf16, py, pys, pn, T, H, float(eps), *po, pw, nbytes),
+          (*ty, nw, *out, work))
     return out
 
 
@@ -912,8 +913,8 @@ def site_post_norm(x, f, nw, post, comb, eps: float = 1e-5, *, gate=None, gate_a
     f32 = torch.float32
     px = _gpu(x, "x", f32)
     args = (px, *_typed(f, "f", (T, H)), _gpu(nw, "nw", f32, (H,)), *_gate(gate, gate_act, T, H),
-            alpha, _gpu(post, "post", f32, (T, S)), _gpu(comb, "comb", f32, (T, S, S)), T, S, H,
-            eps)
+            float(alpha), _gpu(post, "post", f32, (T, S)), _gpu(comb, "comb", f32, (T, S, S)),
+            T, S, H, float(eps))
     if out is None:
         out = x.new_empty((T, S, H))
         po = out.data_ptr()
@@ -954,8 +955,9 @@ def site_post_norm_bwd(g, x, f, nw, post, comb, eps: float = 1e-5, *, gate=None,
         if len(out) != 6 or out[5] is not None:
             raise ValueError("out must hold 5 tensors and None, the gradient of no gate")
         out = out[:5]
-    args = (pg, px, pxs, pf, f_bf16, pfs, _gpu(nw, "nw", f32, (H,)), *how, alpha,
-            _gpu(post, "post", f32, (T, S)), _gpu(comb, "comb", f32, (T, S, S)), T, S, H, eps)
+    args = (pg, px, pxs, pf, f_bf16, pfs, _gpu(nw, "nw", f32, (H,)), *how, float(alpha),
+            _gpu(post, "post", f32, (T, S)), _gpu(comb, "comb", f32, (T, S, S)), T, S, H,
+            float(eps))
     out, po = _new_or(out, names, shapes, g)
     if gate is None:
         out, po = (*out, None), [*po, None]

@@ -104,7 +104,13 @@ def _act(M, K, kind, seed):
 SHAPES = [(1, 1, 32), (1, 16, 32), (2, 5, 96), (1, 100, 4096), (3, 33, 160), (8, 130, 1056),
           (1, 4099, 256), (5, 9000, 64), (16, 33, 128), (17, 64, 256), (40, 70, 384),
           (64, 129, 2080), (100, 257, 512), (333, 48, 1024), (130, 520, 224), (1, 64, 16384),
-          (2, 8200, 512), (7, 16400, 128), (300, 700, 96), (65, 4100, 128)]
+          (2, 8200, 512), (7, 16400, 128), (300, 700, 96), (65, 4100, 128),
+          # one row: more rows of the weight than one turn of the waves, more depth than theirs
+          (1, 30000, 64), (1, 70, 20000),
+          # up to 16 rows: each width of a block, several stages and a short last one
+          (4, 6000, 2080), (3, 16400, 2208), (9, 5000, 4128), (16, 8200, 1056), (16, 16390, 1120),
+          # each tile: 32 x 128, 64 x 128, 128 x 128 (bf16), 128 x 128 (planes)
+          (40, 9000, 160), (120, 16000, 416), (130, 20000, 288), (128, 32700, 96)]
 
 
 def _bound(kind, K, group, a, size, w):
