@@ -3,7 +3,10 @@
 //   site_post_norm  h[t,i] = alpha * a(gate) * f[t,i] * r_t * nw[i]   (r_t of f)
 //                   x'[t,k,i] = post[t,k] * h[t,i] + sum_j comb[t,j,k] * x[t,j,i]
 // Both are one pass over memory: a token's row stays in the registers of the threads
-// that sum its squares until r_t is known.  HBM-bound.
+// that sum its squares until r_t is known.  HBM-bound (a large copy runs at 6.6 TB/s):
+// branch_norm of 4096 x 4096 to bf16 20 us, 5.0 TB/s; the post mix of 4096 tokens of 4 x 4096
+// with a bf16 branch and gate 99 us, 6.1 TB/s, of 1024 of 8 x 7168 96 us, 5.2; one token 3.0 us
+// a launch, latency.
 #include "mhc_norm.h"
 
 namespace mhc {

@@ -2,11 +2,14 @@
 //   out[m,n] = sum_g scale[n,g] * (sum_{k in g} a[m,k] code[n,k] - zero[n,g] sum_{k in g} a[m,k])
 // so that the matrix instructions multiply the codes themselves, which are exact in any type,
 // and a scale is applied once to a group's sum, in fp32.
-//   fp32 activations: three bf16 planes that add up to the value, each a product of its own;
-//   bf16 activations: as they are;  both on v_mfma_f32_16x16x32_bf16, summed in fp32;
-//   int8 codes with a scale per 32 columns: v_mfma_i32_16x16x32_i8, exact per block of 32.
-// The sums of a, which the zero points multiply, come from the same instruction with a
-// column operand of ones: they lie where the products lie.
+// Three kernels by the number of rows M of a:
+//   1        the vector ALU, lanes along the depth: nothing of the weight is staged;
+//   2 .. 16  v_mfma_f32_16x16x32_bf16 (int8 activations: v_mfma_i32_16x16x32_i8, exact per
+//            block of 32), the depth split over a block's waves;
+//   more     tiles of v_mfma_f32_32x32x16_bf16.
+// fp32 activations go into the matrix instructions as three bf16 planes that add up to the
+// value.  Few rows are bound by reading the weight once; their floor is what a plain read of
+// the same bytes takes, 3.5 us for 8.4 MB, 6.9 for 33.5, 16.5 for 100.
 #include <type_traits>
 
 #include "mhc_kernels.h"
@@ -77,7 +80,11 @@ __device__ __forceinline__ void store_one(const Q4Args& p, size_t at, float v) {
 // blocks) and meets the rows of the weight with them, 16 bytes of each: R rows at a time,
 // `iters` times, the next R on their way.  A wave's 64 lanes cover 2048 columns; the block's
 // W waves are KS slices of the depth times W / KS runs of R * iters rows, whose sums meet in
-// LDS.
+// LDS.  us at 4096 x 4096, 16384 x 4096 and 28672 x 7168 (int8; bf16; bf16): 4.4, 9.5, 23.7
+// (4.5 TB/s); fp32 10.4 at the second, 13.7 with 64-column groups and zero points.  Without the
+// products the loads alone take 8.9 and 21.3: what is left above the floor is the conversion
+// and the products (2 instructions a weight in fp32) that the loads do not hide, and the
+// first loads' latency.  R = 2, 4, 8: 9.6, 10.1, 11.6 at 16384 x 4096 in bf16.
 constexpr int kVectorRows = 64;  // rows of a wave at most
 
 template <int A, int GS, bool ZEROS, int R, int W>
@@ -248,6 +255,9 @@ __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int
 // ahead on, in whole lines (a wave's load is 1 KB of one row).  Sixteen rows read straight
 // into the instructions' layout instead are sixteen lines a load, for the two bytes of a
 // scale as well, and every wave loads the activations again.
+// us at 2, 8 and 16 rows of 16384 x 4096: bf16 10.7 (3 rows), 11.7, 12.5; fp32 11.1, 15.3,
+// 18.4; int8 10.7, 13.2, 13.6; with the activations read by every wave 16.6 at 8 rows in
+// bf16.  What is left above the floor: two barriers a stage of 1024 columns, 700 clocks each.
 // Within a row of codes the 16-byte unit i lies at place i ^ (row % 16), and a row of
 // activations is 16 bytes longer than it needs, so that sixteen rows read at one unit meet
 // all banks.
@@ -509,13 +519,19 @@ __global__ __launch_bounds__(64 * W) void q4_rows_kernel(Q4Args p) {
 // A block takes BM = 32*FM*WM rows of a and BN = 32*FN*WN columns n; WM x WN waves, each with
 // FM x FN tiles of v_mfma_f32_32x32x16_bf16, times KG groups of such waves that take the
 // superblocks (128 columns) of the depth in turn and are added in order at the end.  A stage
-// (a superblock for each group of waves) comes by way of registers into one of two buffers in
-// LDS while the one before is multiplied, one barrier a stage.
+// (a superblock for each group of waves) is asked for while the one before is multiplied and
+// goes by way of registers into LDS: into one of two buffers, one barrier a stage, or, where
+// two do not fit, into the one that every wave has done with.
 // In LDS: the codes; the activations as bf16 (fp32 ones and int8 codes times their scale as
 // three planes), with the sums of each group of columns, which the zero points multiply; the
 // scales and zero points as floats.  A group's products start from minus zero point times
 // sum and end times the scale in the sums that are kept, in fp32.
 // The 16-byte units of a row are placed so that sixteen rows read at one unit meet all banks.
+// What bounds it: a stage of a 128 x 128 tile in bf16 takes 4000 clocks of its unit, of which
+// the matrix instructions fill 1030, the vector ones (staging and sums 700, conversion to bf16
+// and scaling the rest) 1680 and LDS 1240; two waves a SIMD, all its registers allow, leave a
+// third of the time to waits.  Memory is not it: with two stages on their way instead of one
+// 97 and 98 us at 333 x 7168 x 7168.
 template <int A, int GS, int FM, int FN, int WM, int WN, int KG>
 struct TileLayout {
   static constexpr int PL = A == kActBF16 ? 1 : 3, NG = 4 >> GS;
@@ -546,7 +562,6 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
   constexpr int UA = 8 * act_size<A>();  // 16-byte units of a row of a, of a superblock
   constexpr int NA = KG * BM * UA / TH, NB = (KG * BN * 4 + TH - 1) / TH;
   constexpr int NS = (KG * BN * NG + TH - 1) / TH;
-  constexpr int AHEAD = A == kActBF16 ? 2 : 1;  // stages on their way (registers allow)
   static_assert(KG * BM * UA % TH == 0, "whole loads");
   extern __shared__ __align__(16) unsigned char lds[];
   const int lane = threadIdx.x & 63;
@@ -565,10 +580,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
   }
   const int m0 = id % MT * BM, n0 = id / MT * BN;
 
-  intx4 an[AHEAD][NA], bn[AHEAD][NB];
-  float dn[AHEAD][A == kActQ8 ? NA : 1];
-  unsigned short sn[AHEAD][NS];
-  unsigned char zn[AHEAD][NS];
+  intx4 an[NA], bn[NB];
+  float dn[A == kActQ8 ? NA : 1];
+  unsigned short sn[NS];
+  unsigned char zn[NS];
   // Where a thread's loads begin (64-bit products cost too much to be formed a stage); rows past
   // the end read the last row, and are not stored.  As above, past the end of the depth the
   // last columns are read, and zeros take their place in LDS.
@@ -585,38 +600,36 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
 #pragma unroll
   for (int i = 0; i < NS; ++i)
     sp[i] = (size_t)min(n0 + (int)(threadIdx.x + TH * i) / NG % BN, p.N - 1) * p.KG;
-  auto fetch = [&](int sb, auto turn) {
-    constexpr int T = decltype(turn)::value;
+  auto fetch = [&](int sb) {
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
       const int at = threadIdx.x + TH * i;
       const int col = 128 * (sb + at / UA / BM) + at % UA * (16 / act_size<A>());
-      an[T][i] = *reinterpret_cast<const intx4*>(
+      an[i] = *reinterpret_cast<const intx4*>(
           ap[i] + (unsigned)(min(col, p.K - 16 / act_size<A>()) * act_size<A>()));
       if constexpr (A == kActQ8)
-        dn[T][i] = p.ad[(size_t)(ap[i] - p.a) / kQ4Block + min(col / kQ4Block, KB - 1)];
+        dn[i] = p.ad[(size_t)(ap[i] - p.a) / kQ4Block + min(col / kQ4Block, KB - 1)];
     }
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       const int s = min(sb + (int)(threadIdx.x + TH * i) / 4 / BN, SB - 1);
-      bn[T][i] = *reinterpret_cast<const intx4*>(bp[i] + (unsigned)(s * 64));
+      bn[i] = *reinterpret_cast<const intx4*>(bp[i] + (unsigned)(s * 64));
     }
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const int at = threadIdx.x + TH * i;
       const size_t g = sp[i] + (unsigned)min((sb + at / NG / BN) * NG + at % NG, p.KG - 1);
-      sn[T][i] = p.scales[g];
-      if (p.zeros) zn[T][i] = p.zeros[g];
+      sn[i] = p.scales[g];
+      if (p.zeros) zn[i] = p.zeros[g];
     }
   };
-  auto place = [&](unsigned char* to, int sb, auto turn) {
-    constexpr int T = decltype(turn)::value;
+  auto place = [&](unsigned char* to, int sb) {
     if ((sb + KG) * 128 > p.K) {  // the last stage, where it is short
 #pragma unroll
       for (int i = 0; i < NA; ++i) {
         const int at = threadIdx.x + TH * i;
         if (128 * (sb + at / UA / BM) + at % UA * (16 / act_size<A>()) >= p.K)
-          an[T][i] = intx4{0, 0, 0, 0};
+          an[i] = intx4{0, 0, 0, 0};
       }
     }
 #pragma unroll
@@ -626,11 +639,11 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
       unsigned char* acts = part + L::CODES;
       float total = 0.f;
       if constexpr (A == kActBF16) {
-        reinterpret_cast<intx4*>(acts)[m * 16 + (c ^ (m & 15))] = an[T][i];
+        reinterpret_cast<intx4*>(acts)[m * 16 + (c ^ (m & 15))] = an[i];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           bf16x2 v, one;
-          const int u = an[T][i][e], ones = 0x3f803f80;
+          const int u = an[i][e], ones = 0x3f803f80;
           __builtin_memcpy(&v, &u, 4);
           __builtin_memcpy(&one, &ones, 4);
           total = __builtin_amdgcn_fdot2_f32_bf16(v, one, total, false);
@@ -639,11 +652,11 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
         constexpr int NV = A == kActF32 ? 4 : 16;  // columns of a unit
         float v[NV];
         if constexpr (A == kActF32) {
-          __builtin_memcpy(v, &an[T][i], 16);
+          __builtin_memcpy(v, &an[i], 16);
         } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            v[e] = (float)((signed char)(an[T][i][e >> 2] >> (8 * (e & 3)))) * dn[T][i];
+            v[e] = (float)((signed char)(an[i][e >> 2] >> (8 * (e & 3)))) * dn[i];
         }
 #pragma unroll
         for (int e = 0; e < NV; ++e) total += v[e];
@@ -679,7 +692,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
       const int at = threadIdx.x + TH * i, row = at / 4, n = row % BN;
       if (KG * BN * 4 % TH == 0 || row < KG * BN)
         reinterpret_cast<intx4*>(to + row / BN * L::PART)[n * 4 + ((at & 3) ^ ((n >> 2) & 3))] =
-            bn[T][i];
+            bn[i];
     }
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
@@ -687,7 +700,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
       if (KG * BN * NG % TH == 0 || row < KG * BN)
         reinterpret_cast<float2*>(to + row / BN * L::PART + L::CODES + L::ACTS +
                                   L::SUMS)[k * BN + row % BN] =
-            make_float2(q4_scale(sn[T][i], p.f16), p.zeros ? (float)zn[T][i] : 8.f);
+            make_float2(q4_scale(sn[i], p.f16), p.zeros ? (float)zn[i] : 8.f);
     }
   };
 
@@ -703,25 +716,9 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
     const unsigned char* acts = part + L::CODES;
     const float* sums = reinterpret_cast<const float*>(acts + L::ACTS);
     const float2* scales = reinterpret_cast<const float2*>(acts + L::ACTS + L::SUMS);
-    // Steps of one plane of one row tile in one group; what the next one needs of the
-    // activations is read while this one is multiplied (one plane: the registers allow it).
-    constexpr int STEPS = FM * PL, EARLY = PL == 1 ? 1 : 0;
-    bf16x8 ax[1 + EARLY][2 * GB];
-    auto read = [&](int k, int step, int to) {
-      const int m = (wm * FM + step / PL) * 32 + r;
-#pragma unroll
-      for (int b = 0; b < 2 * GB; ++b) {
-        const int unit = 4 * (k * GB + (b >> 1)) + 2 * (b & 1) + h;
-        __builtin_memcpy(&ax[to][b],
-                         __builtin_assume_aligned(
-                             acts + ((step % PL * BM + m) * 16 + (unit ^ (m & 15))) * 16, 16),
-                         16);
-      }
-    };
     constexpr int ROLL = GS == 0 ? 1 : NG;
 #pragma unroll ROLL
     for (int k = 0; k < NG; ++k) {
-      if (EARLY) read(k, 0, 0);
       float2 sz[FN];
       bf16x8 bx[FN][2 * GB];
 #pragma unroll
@@ -740,9 +737,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
           for (int b = 0; b < GB; ++b) bx[j][2 * b + u] = q4_to_bf16(c[b]);
         }
       }
+      // the tiles take turns, so that no product waits for the one before it
+      floatx16 t[FM][FN];
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        floatx16 t[FN];
+      for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const floatx4 c = *reinterpret_cast<const floatx4*>(
@@ -750,47 +748,47 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
 #pragma unroll
           for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t[j][4 * v + e] = sz[j].y * c[e];
+            for (int e = 0; e < 4; ++e) t[i][j][4 * v + e] = sz[j].y * c[e];
         }
 #pragma unroll
-        for (int l = 0; l < PL; ++l) {
-          const int step = i * PL + l;
-          if (step + EARLY < STEPS) read(k, step + EARLY, (step + EARLY) & EARLY);
+      for (int l = 0; l < PL; ++l) {
+        bf16x8 ax[FM][2 * GB];
 #pragma unroll
-          for (int b = 0; b < 2 * GB; ++b)
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int b = 0; b < 2 * GB; ++b) {
+            const int m = (wm * FM + i) * 32 + r, unit = 4 * (k * GB + (b >> 1)) + 2 * (b & 1) + h;
+            __builtin_memcpy(&ax[i][b],
+                             __builtin_assume_aligned(
+                                 acts + ((l * BM + m) * 16 + (unit ^ (m & 15))) * 16, 16), 16);
+          }
+#pragma unroll
+        for (int b = 0; b < 2 * GB; ++b)
+#pragma unroll
+          for (int i = 0; i < FM; ++i)
 #pragma unroll
             for (int j = 0; j < FN; ++j)
-              t[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ax[step & EARLY][b], bx[j][b], t[j],
-                                                              0, 0, 0);
-        }
+              t[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ax[i][b], bx[j][b], t[i][j], 0, 0,
+                                                                 0);
+      }
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-          for (int v = 0; v < 16; ++v) acc[i][j][v] = fmaf(sz[j].x, t[j][v], acc[i][j][v]);
-      }
+          for (int v = 0; v < 16; ++v) acc[i][j][v] = fmaf(sz[j].x, t[i][j][v], acc[i][j][v]);
     }
   };
 
-  auto step = [&](int sb, auto turn) {
-    constexpr int T = decltype(turn)::value;
-    unsigned char* stage = lds + T % L::BUFS * L::STAGE;
+  fetch(0);
+  int turn = 0;
+  for (int sb = 0; sb < SB; sb += KG, turn ^= L::BUFS - 1) {
+    unsigned char* stage = lds + turn * L::STAGE;
     if (L::BUFS == 1 && sb > 0) __syncthreads();
-    place(stage, sb, std::integral_constant<int, T % AHEAD>{});
+    place(stage, sb);
     __syncthreads();  // (of two buffers, the one written next was read before this)
-    if (sb + AHEAD * KG < SB) fetch(sb + AHEAD * KG, std::integral_constant<int, T % AHEAD>{});
+    if (sb + KG < SB) fetch(sb + KG);
     if (KG == 1 || sb + kg < SB) multiply(stage + kg * L::PART);
-  };
-  constexpr std::integral_constant<int, 0> even{};
-  constexpr std::integral_constant<int, 1> odd{};
-  fetch(0, even);
-  if (AHEAD > 1 && KG < SB) fetch(KG, std::integral_constant<int, 1 % AHEAD>{});
-  if constexpr (AHEAD == 1 && L::BUFS == 1) {
-    for (int sb = 0; sb < SB; sb += KG) step(sb, even);
-  } else {
-    for (int sb = 0; sb < SB; sb += 2 * KG) {
-      step(sb, even);
-      if (sb + KG < SB) step(sb + KG, odd);
-    }
   }
   if constexpr (KG > 1) {
     float4* last = reinterpret_cast<float4*>(lds);
@@ -884,11 +882,10 @@ void launch_q4_vector(const Q4Args& p, hipStream_t st) {
 // Tiles by the rounds of 256 blocks they take: the smallest that need one, with several groups
 // of waves on each; us in 32 x 64 / 32 x 128 / 64 x 128 / 128 x 128: 48 x 7168 x 7168 26 / 35 /
 // 50 / 83, 64 x 16384 x 4096 30 / 23 / 32 / 49, 100 x 7168 x 7168 46 / 35 / 51 / 88, 128 x
-// 16384 x 4096 56 / 41 / 34 / 52, 512 x 4096 x 4096 56 / 39 / 33 / 52; past one round 333 x
-// 7168 x 7168 116 / 116 / 105 / 95, 512 x 16384 x 4096 212 / 146 / 117 / 103.  With three
-// planes a tile's cost goes with its size, and small ones waste less of the last round: 333 x
-// 7168 x 7168 in 32 x 128 and 128 x 128 172 and 225, 512 x 8192 x 4096 (groups of 32) 187 and
-// 153.
+// 16384 x 4096 56 / 41 / 34 / 52, 512 x 4096 x 4096 56 / 39 / 33 / 52.  Past one round a tile's
+// cost goes with its size, nearly, and small ones waste less of the last round: 32 x 128 and
+// 128 x 128 take 91 and 97 us at 333 x 7168 x 7168 (172 and 225 in fp32), 115 and 103 at 512 x
+// 16384 x 4096, 187 and 154 at 512 x 8192 x 4096 in fp32 with groups of 32.
 template <int A, int GS>
 void launch_q4_tiles(const Q4Args& p, hipStream_t st) {
   auto blocks = [&](long bm, long bn) {
@@ -897,11 +894,12 @@ void launch_q4_tiles(const Q4Args& p, hipStream_t st) {
   auto rounds = [&](long bm, long bn) { return (blocks(bm, bn) + 255) / 256; };
   if (blocks(32, 64) <= 256)
     launch_q4_tile<A, GS, 1, 1, 1, 2, 4>(p, st);
-  else if (blocks(32, 128) <= 256 ||
-           (A != kActBF16 && 5 * rounds(32, 128) <= 16 * rounds(128, 128)))
+  else if (blocks(32, 128) <= 256)
     launch_q4_tile<A, GS, 1, 1, 1, 4, 2>(p, st);
   else if (blocks(64, 128) <= 256)
     launch_q4_tile<A, GS, 2, 1, 1, 4, 2>(p, st);
+  else if (5 * rounds(32, 128) <= 16 * rounds(128, 128))
+    launch_q4_tile<A, GS, 1, 1, 1, 4, 2>(p, st);
   else
     launch_q4_tile<A, GS, 2, 1, 2, 4, 1>(p, st);
 }
