@@ -210,7 +210,7 @@ __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int
             acc[i] = fmaf(sv[i][k], t, acc[i]);
           } else {
             // codes come as multiples of 2^-9 (mhc_q4.h): so does the zero point, and the
-            // scale makes up for it
+            // sum is made up for it (a scale may be the type's largest)
             t = -(zv[i][k] * 0.001953125f) * as[k];
 #pragma unroll
             for (int b = k * GB; b < (k + 1) * GB; ++b) {
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int
 #pragma unroll
               for (int e = 0; e < 8; ++e) t = fmaf(c[e >> 1][e & 1], av[b][e], t);
             }
-            acc[i] = fmaf(sv[i][k] * 512.f, t, acc[i]);
+            acc[i] = fmaf(sv[i][k], t * 512.f, acc[i]);
           }
         }
       }

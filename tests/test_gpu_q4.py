@@ -171,6 +171,25 @@ def test_whole_numbers_are_exact(mhc, M, N, K, kind):
             np.testing.assert_array_equal(got.double().cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16", "q8"])
+@pytest.mark.parametrize("M", [1, 4, 12, 40])
+@pytest.mark.parametrize("ea,es", [(-110, 120), (-100, 127), (100, -126)])
+def test_scales_at_the_ends_of_their_range(mhc, kind, M, ea, es):
+    """Whole numbers times powers of two: exact in any order."""
+    print(f"[case] q4_matmul M={M} {kind} a 2^{ea} scales 2^{es}", flush=True)
+    g = np.random.default_rng(M)
+    c = g.integers(0, 16, (70, 256)).astype(np.uint8)
+    c[3], c[5, 64:128] = 8, 8  # a group, and a row, of zeros
+    n = g.integers(-4, 5, (M, 256)).astype(np.float32)
+    scales = torch.full((70, 4), 2.0 ** es, dtype=torch.bfloat16).cuda()
+    v = torch.from_numpy(n)
+    a = (v.to(torch.int8).cuda(), torch.full((M, 8), 2.0 ** ea).cuda()) if kind == "q8" else \
+        (v * 2.0 ** ea).to(torch.bfloat16 if kind == "bf16" else torch.float32).cuda()
+    got = mhc.q4_matmul(a, torch.from_numpy(bf.pack(c)).cuda(), scales).double().cpu()
+    want = torch.from_numpy(n.astype(np.float64) @ (c.astype(np.float64) - 8).T)
+    assert torch.equal(got, want * 2.0 ** (ea + es))
+
+
 def test_one_column_at_a_time(mhc):
     """A unit activation picks a weight's column: every column's place and group."""
     print("[case] columns", flush=True)
