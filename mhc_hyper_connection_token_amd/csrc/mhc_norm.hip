@@ -4,7 +4,7 @@
 //                   x'[t,k,i] = post[t,k] * h[t,i] + sum_j comb[t,j,k] * x[t,j,i]
 // Both are one pass over memory: a token's row stays in the registers of the threads
 // that sum its squares until r_t is known.  HBM-bound (a large copy runs at 6.6 TB/s):
-// branch_norm of 4096 x 4096 to bf16 20 us, 5.0 TB/s; the post mix of 4096 tokens of 4 x 4096
+// branch_norm of 4096 x 4096 to bf16 18.5 us, 5.4 TB/s; the post mix of 4096 tokens of 4 x 4096
 // with a bf16 branch and gate 99 us, 6.1 TB/s, of 1024 of 8 x 7168 96 us, 5.2; one token 3.0 us
 // a launch, latency.
 #include "mhc_norm.h"
@@ -73,6 +73,10 @@ hipError_t launch_branch_norm(const float* y, const float* nw, int T, int H, flo
     launch_branch_norm_at<1, 1>(y, nw, T, HQ, eps, z, bf16, st);
   else if (HQ <= 256)
     launch_branch_norm_at<1, 4>(y, nw, T, HQ, eps, z, bf16, st);
+  else if (HQ <= 1024 && T >= 1024)
+    // more of a row in each thread, where tokens fill the chip: 4096 x 4096 to bf16 18.5 us,
+    // with four waves 20.3; one token 3.2 and 2.6
+    launch_branch_norm_at<2, 8>(y, nw, T, HQ, eps, z, bf16, st);
   else if (HQ <= 1024)
     launch_branch_norm_at<4, 4>(y, nw, T, HQ, eps, z, bf16, st);
   else

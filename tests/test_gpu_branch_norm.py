@@ -48,7 +48,8 @@ def _same(a, b):
 
 
 NORM_SHAPES = [(1, 4), (3, 128), (5, 256), (7, 260), (37, 1028), (1, 4096), (9, 4100), (2, 7168),
-               (3, 8192), (1500, 132), (1100, 1024), (4, 8188)]
+               (3, 8192), (1500, 132), (1100, 1024), (4, 8188), (1023, 1028), (1024, 1028),
+               (1030, 4096)]
 
 
 @pytest.mark.parametrize("T,H", NORM_SHAPES)
