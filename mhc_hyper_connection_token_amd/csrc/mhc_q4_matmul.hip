@@ -73,6 +73,17 @@ __device__ __forceinline__ void store_one(const Q4Args& p, size_t at, float v) {
     static_cast<float*>(p.out)[at] = v;
 }
 
+// N bytes at an address that is a multiple of N, zero-extended to whole dwords.
+template <int N>
+__device__ __forceinline__ void load_bits(unsigned* to, const void* from) {
+  if constexpr (N == 1)
+    *to = *static_cast<const unsigned char*>(from);
+  else if constexpr (N == 2)
+    *to = *static_cast<const unsigned short*>(from);
+  else
+    __builtin_memcpy(to, __builtin_assume_aligned(from, N), N);
+}
+
 }  // namespace
 
 // ---------------------------------------------------------------- one row
@@ -81,7 +92,7 @@ __device__ __forceinline__ void store_one(const Q4Args& p, size_t at, float v) {
 // `iters` times, the next R on their way.  A wave's 64 lanes cover 2048 columns; the block's
 // W waves are KS slices of the depth times W / KS runs of R * iters rows, whose sums meet in
 // LDS.  us at 4096 x 4096, 16384 x 4096 and 28672 x 7168 (int8; bf16; bf16): 4.4, 9.5, 23.7
-// (4.5 TB/s); fp32 10.4 at the second, 13.7 with 64-column groups and zero points.  Without the
+// (4.5 TB/s); fp32 10.4 at the second, 11.5 with 64-column groups and zero points.  Without the
 // products the loads alone take 8.9 and 21.3: what is left above the floor is the conversion
 // and the products (2 instructions a weight in fp32) that the loads do not hide, and the
 // first loads' latency.  R = 2, 4, 8: 9.6, 10.1, 11.6 at 16384 x 4096 in bf16.
@@ -104,39 +115,35 @@ __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int
     const bool in = s0 + (lane >> 2) < SB;
     const unsigned code_at = s * 64u + g * 16u;
     intx4 cn[R];
-    unsigned short bits[R][NG];
-    unsigned char zero[R][NG];
+    // a row's scales and zero points as they were loaded: taken apart here, where two paths
+    // meet, they would be waited for
+    unsigned bits[R][(NG + 1) / 2], zero[R];
     auto fetch = [&](int n) {  // rows past the end: the last one, whose sums are not stored
 #pragma unroll
       for (int i = 0; i < R; ++i)
         cn[i] = __builtin_nontemporal_load(reinterpret_cast<const intx4*>(
             p.codes + (size_t)min(n + i, p.N - 1) * pitch + code_at));
-      if (whole) {  // all groups are there, and aligned to their number
+      if (NG == 1 || whole) {  // all groups are there, and aligned to their number
 #pragma unroll
-        for (int i = 0; i < R; ++i)
-          __builtin_memcpy(
-              bits[i],
-              __builtin_assume_aligned(
-                  p.scales + (size_t)min(n + i, p.N - 1) * p.KG + (unsigned)(s * NG), 2 * NG),
-              2 * NG);
-        if constexpr (ZEROS)
-#pragma unroll
-          for (int i = 0; i < R; ++i)
-            __builtin_memcpy(
-                zero[i],
-                __builtin_assume_aligned(
-                    p.zeros + (size_t)min(n + i, p.N - 1) * p.KG + (unsigned)(s * NG), NG),
-                NG);
+        for (int i = 0; i < R; ++i) {
+          const size_t at = (size_t)min(n + i, p.N - 1) * p.KG + (unsigned)(s * NG);
+          load_bits<2 * NG>(bits[i], p.scales + at);
+          if constexpr (ZEROS) load_bits<NG>(&zero[i], p.zeros + at);
+        }
       } else {
 #pragma unroll
-        for (int i = 0; i < R; ++i)
+        for (int i = 0; i < R; ++i) {
+#pragma unroll
+          for (int k = 0; k < (NG + 1) / 2; ++k) bits[i][k] = 0;
+          zero[i] = 0;
 #pragma unroll
           for (int k = 0; k < NG; ++k) {
             const size_t at =
                 (size_t)min(n + i, p.N - 1) * p.KG + (unsigned)min(s * NG + k, p.KG - 1);
-            bits[i][k] = p.scales[at];
-            if constexpr (ZEROS) zero[i][k] = p.zeros[at];
+            bits[i][k / 2] |= (unsigned)p.scales[at] << (16 * (k % 2));
+            if constexpr (ZEROS) zero[i] |= (unsigned)p.zeros[at] << (8 * k);
           }
+        }
       }
     };
     // the activations first: loads are waited for in the order they were asked for in
@@ -186,8 +193,8 @@ __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int
         cv[i] = cn[i];
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
-          sv[i][k] = q4_scale(bits[i][k], p.f16);
-          zv[i][k] = ZEROS ? (float)zero[i][k] : 8.f;
+          sv[i][k] = q4_scale((unsigned short)(bits[i][k / 2] >> (16 * (k % 2))), p.f16);
+          zv[i][k] = ZEROS ? (float)(zero[i] >> (8 * k) & 255) : 8.f;
         }
       }
       if (it + 1 < iters) fetch(n0 + R * (it + 1));
