@@ -267,7 +267,8 @@ def run(state):
         return mhc.branch_norm(s["y"], s["nw"], EPS, dtype=s["z"])
     if op == "norm_bwd":
         return mhc.branch_norm_bwd(s["dz"], s["y"], s["nw"], EPS)
-    how = dict(gate=s["gate"], gate_act=s["gate_act"], alpha=s["alpha"])
+    how = dict(gate=s["gate"], gate_act=s["gate_act"] if s["gate"] is not None else None,
+               alpha=s["alpha"])
     if op == "post":
         return mhc.site_post_norm(s["x"], s["f"], s["nw"], s["post"], s["comb"], EPS, **how)
     out = mhc.site_post_norm_bwd(s["g"], s["x"], s["f"], s["nw"], s["post"], s["comb"], EPS,
