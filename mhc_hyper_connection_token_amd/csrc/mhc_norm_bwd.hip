@@ -21,11 +21,12 @@ namespace mhc {
 namespace {
 // Parts of a sum over tokens, blocks of the first launch: eight waves for each unit.  More
 // parts are more to write and to read again: 1001 tokens of 7168 22 us with 256 of eight
-// waves, 25 with 512, 33 with 1024; 8192 of 256 14 us with 1024 of one wave, 22 with 256.
+// waves, 25 with 512, 33 with 1024; 8192 of 256 16 us with 1024 of one wave, 17
+// with 2048, 22 with 256.
 // A few short rows are one block's: it writes the sums themselves, without the second launch.
 int parts_of(int T, int H) {
   if (H <= kOneWaveHidden && T <= 4) return T < 1 ? T : 1;
-  const int most = H <= kOneWaveHidden ? 2048 : 256;
+  const int most = H <= kOneWaveHidden ? 1024 : 256;
   return T < most ? T : most;
 }
 }  // namespace
