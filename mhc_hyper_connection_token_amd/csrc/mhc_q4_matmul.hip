@@ -10,6 +10,7 @@
 // fp32 activations go into the matrix instructions as three bf16 planes that add up to the
 // value.  Few rows are bound by reading the weight once; their floor is what a plain read of
 // the same bytes takes, 3.5 us for 8.4 MB, 6.9 for 33.5, 16.5 for 100.
+#include <algorithm>
 #include <type_traits>
 
 #include "mhc_kernels.h"
@@ -795,7 +796,11 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
     place(stage, sb);
     __syncthreads();  // (of two buffers, the one written next was read before this)
     if (sb + KG < SB) fetch(sb + KG);
+    // Waves that multiply go before waves that stage: 333 x 7168 x 7168 in int8 166 -> 150 us,
+    // the other types and sizes up to 3 % (100 x 28672 x 7168 in bf16 94.4 -> 91.8).
+    __builtin_amdgcn_s_setprio(1);
     if (KG == 1 || sb + kg < SB) multiply(stage + kg * L::PART);
+    __builtin_amdgcn_s_setprio(0);
   }
   if constexpr (KG > 1) {
     float4* last = reinterpret_cast<float4*>(lds);
@@ -890,22 +895,27 @@ void launch_q4_vector(const Q4Args& p, hipStream_t st) {
 // of waves on each; us in 32 x 64 / 32 x 128 / 64 x 128 / 128 x 128: 48 x 7168 x 7168 26 / 35 /
 // 50 / 83, 64 x 16384 x 4096 30 / 23 / 32 / 49, 100 x 7168 x 7168 46 / 35 / 51 / 88, 128 x
 // 16384 x 4096 56 / 41 / 34 / 52, 512 x 4096 x 4096 56 / 39 / 33 / 52.  Past one round a tile's
-// cost goes with its size, nearly, and small ones waste less of the last round: 32 x 128 and
-// 128 x 128 take 91 and 97 us at 333 x 7168 x 7168 (172 and 225 in fp32), 115 and 103 at 512 x
-// 16384 x 4096, 187 and 154 at 512 x 8192 x 4096 in fp32 with groups of 32.
+// cost goes with its size, nearly, and small ones waste less of the last round: 32 x 128, 96 x
+// 128 and 128 x 128 take 96, 75 and 96 us at 333 x 7168 x 7168, 121, 123 and 105 at 512 x 16384 x
+// 4096, 46, 44 and 52 at 288 x 9000 x 4096.  In fp32 (three planes of 96 rows do not fit twice)
+// 181, 238 and 190 at the first; the two ends 187 and 157 at 512 x 8192 x 4096, groups of 32.
+// Where the rule is off: 384 x 8192 x 4096, groups of 64, 70 instead of 65.
 template <int A, int GS>
 void launch_q4_tiles(const Q4Args& p, hipStream_t st) {
   auto blocks = [&](long bm, long bn) {
     return ((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn);
   };
   auto rounds = [&](long bm, long bn) { return (blocks(bm, bn) + 255) / 256; };
+  const long least = std::min(5 * rounds(32, 128), 16 * rounds(128, 128));
   if (blocks(32, 64) <= 256)
     launch_q4_tile<A, GS, 1, 1, 1, 2, 4>(p, st);
   else if (blocks(32, 128) <= 256)
     launch_q4_tile<A, GS, 1, 1, 1, 4, 2>(p, st);
   else if (blocks(64, 128) <= 256)
     launch_q4_tile<A, GS, 2, 1, 1, 4, 2>(p, st);
-  else if (5 * rounds(32, 128) <= 16 * rounds(128, 128))
+  else if (A == kActBF16 && 12 * rounds(96, 128) < least) {
+    if constexpr (A == kActBF16) launch_q4_tile<A, GS, 3, 1, 1, 4, 2>(p, st);
+  } else if (5 * rounds(32, 128) == least)
     launch_q4_tile<A, GS, 1, 1, 1, 4, 2>(p, st);
   else
     launch_q4_tile<A, GS, 2, 1, 2, 4, 1>(p, st);

@@ -109,8 +109,9 @@ SHAPES = [(1, 1, 32), (1, 16, 32), (2, 5, 96), (1, 100, 4096), (3, 33, 160), (8,
           (1, 30000, 64), (1, 70, 20000),
           # up to 16 rows: each width of a block, several stages and a short last one
           (4, 6000, 2080), (3, 16400, 2208), (9, 5000, 4128), (16, 8200, 1056), (16, 16390, 1120),
-          # each tile: 32 x 128, 64 x 128, 128 x 128 (bf16), 128 x 128 (planes)
-          (40, 9000, 160), (120, 16000, 416), (130, 20000, 288), (128, 32700, 96)]
+          # each tile: 32 x 128, 64 x 128, 32 x 128 past one round, 128 x 128, 96 x 128 (bf16)
+          (40, 9000, 160), (120, 16000, 416), (130, 20000, 288), (128, 32700, 96),
+          (90, 30000, 416)]
 
 
 def _bound(kind, K, group, a, size, w):
