@@ -84,12 +84,11 @@ def draw(rng):
 
 
 # ------------------------------------------------------------------ plain forms
-def _weight(codes, scales, zeros, group, K):
-    """Codes [N, P/2], P = K up to 128: of the 64 bytes of 128 columns, byte 16 g + 4 b + e
-    holds column 32 b + 8 g + e in its low half and the column 4 past it in its high half."""
-    b = codes.unflatten(1, (-1, 4, 4, 4)).transpose(2, 3)
-    c = torch.stack([b & 15, b >> 4], 4).flatten(1)[:, :K].float()
-    at = torch.arange(K, device="cuda") // group
+def _weight(codes, scales, zeros, group):
+    """Codes [N, K/2]: byte j of each 16 holds columns j (low half) and 16 + j of 32."""
+    b = codes.unflatten(1, (-1, 16))
+    c = torch.cat([b & 15, b >> 4], 2).flatten(1).float()
+    at = torch.arange(c.shape[1], device="cuda") // group
     z = 8.0 if zeros is None else zeros.float()[:, at]
     return (c - z) * scales.float()[:, at]
 
@@ -98,7 +97,7 @@ def _plain_q4(s):
     a = s["a"]
     if isinstance(a, tuple):
         a = (a[0].float().unflatten(1, (-1, 32)) * a[1].unsqueeze(2)).flatten(1)
-    w = _weight(s["codes"], s["scales"], s["zeros"], s["group"], a.shape[1])
+    w = _weight(s["codes"], s["scales"], s["zeros"], s["group"])
     return torch.matmul(a.float(), w.t()).to(s["out"])
 
 
@@ -202,9 +201,8 @@ def _quantised(rand, N, K, group, zeros, scale):
         scales = (w.abs().amax(2) / 7).to(scale)
         z = torch.full_like(scales, 8.0, dtype=torch.float32)
     c = torch.round(w / scales.float().unsqueeze(2)) + z.unsqueeze(2)
-    c = c.clamp(0, 15).to(torch.uint8).flatten(1)[:, :K]
-    c = torch.nn.functional.pad(c, (0, -K % 128)).unflatten(1, (-1, 4, 4, 2, 4)).transpose(2, 3)
-    codes = (c[..., 0, :] | (c[..., 1, :] << 4)).flatten(1).contiguous()
+    c = c.clamp(0, 15).to(torch.uint8).flatten(1)[:, :K].unflatten(1, (-1, 2, 16))
+    codes = (c[:, :, 0] | (c[:, :, 1] << 4)).flatten(1).contiguous()
     return codes, scales, z.to(torch.uint8) if zeros else None
 
 
@@ -267,8 +265,7 @@ def run(state):
         return mhc.branch_norm(s["y"], s["nw"], EPS, dtype=s["z"])
     if op == "norm_bwd":
         return mhc.branch_norm_bwd(s["dz"], s["y"], s["nw"], EPS)
-    how = dict(gate=s["gate"], gate_act=s["gate_act"] if s["gate"] is not None else None,
-               alpha=s["alpha"])
+    how = dict(gate=s["gate"], gate_act=s["gate_act"], alpha=s["alpha"])
     if op == "post":
         return mhc.site_post_norm(s["x"], s["f"], s["nw"], s["post"], s["comb"], EPS, **how)
     out = mhc.site_post_norm_bwd(s["g"], s["x"], s["f"], s["nw"], s["post"], s["comb"], EPS,
@@ -319,9 +316,11 @@ def _value64(t, H):
 
 def _q4_64(case, s):
     N, K = case["N"], case["K"]
-    col = torch.arange(K, device="cuda")
-    byte = col // 128 * 64 + col % 32 // 8 * 16 + col % 128 // 32 * 4 + col % 4
-    w = (s["codes"][:, byte].long() // (1 + 15 * (col % 8 // 4)) % 16).double()
+    codes = s["codes"].long().reshape(N, K // 32, 16)
+    w = torch.empty(N, K // 32, 32, dtype=torch.float64, device="cuda")
+    w[:, :, :16] = codes % 16
+    w[:, :, 16:] = codes // 16
+    w = w.reshape(N, K)
     wide = s["scales"].double().repeat_interleave(case["group"], 1)[:, :K]
     zero = 8.0 if s["zeros"] is None else \
         s["zeros"].double().repeat_interleave(case["group"], 1)[:, :K]
