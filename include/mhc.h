@@ -545,9 +545,8 @@ int mhc_site_post_norm_bwd(const float* g, const void* x, const unsigned char* x
  *   w[n][k] = scale[n][k/G] * (code[n][k] - zero[n][k/G])
  *   scales [N][KG]   MHC_BF16 or MHC_F16
  *   zeros  [N][KG]   one byte, 0 .. 15; NULL: 8 everywhere
- *   codes  [N][P/2]  0 .. 15, P = K rounded up to 128.  Of the 64 bytes of 128 columns,
- *                    byte 16 g + 4 b + e (g, b, e < 4) holds column 32 b + 8 g + e in its
- *                    low half and the column 4 past it in its high half; zero past K
+ *   codes  [N][K/2]  0 .. 15.  Of the 16 bytes of 32 columns, byte j holds column j in its
+ *                    low half and column 16 + j in its high half
  *
  * mhc_q4_encode: w (MHC_F32 or MHC_BF16) into codes and bf16 scales.  With zeros NULL
  *   scale = max|w| / 7 of the group and the codes are 1 .. 15; else, with lo = min(w, 0)

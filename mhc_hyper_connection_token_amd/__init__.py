@@ -1003,7 +1003,7 @@ def _q4_weight(codes, scales, zeros, K):
     """Addresses of a 4-bit weight, its scale type (C ABI), rows and group size."""
     import torch
     if codes.dim() != 2 or scales.dim() != 2:
-        raise ValueError("codes must be [N, P/2] and scales [N, groups]")
+        raise ValueError("codes must be [N, K/2] and scales [N, groups]")
     if K < 1 or K % 32:
         raise ValueError("K must be a multiple of 32")
     N, kg = scales.shape
@@ -1024,7 +1024,7 @@ def _q4_weight(codes, scales, zeros, K):
         kind = 2
     else:
         raise ValueError("scales must be bfloat16 or float16")
-    pc = _gpu(codes, "codes", torch.uint8, (N, _blocks(K) * 64))
+    pc = _gpu(codes, "codes", torch.uint8, (N, K // 2))
     ps = _gpu(scales, "scales", dtype)
     pz = None if zeros is None else _gpu(zeros, "zeros", torch.uint8, (N, kg))
     return pc, ps, kind, pz, N, group
@@ -1032,9 +1032,9 @@ def _q4_weight(codes, scales, zeros, K):
 
 def q4_encode(w, *, group: int = 128, zeros: bool = False, out=None, stream=None):
     """4-bit groups of a weight w [N, K] (float32 or bfloat16; include/mhc.h, "4-bit groups"):
-    (codes [N, P/2] uint8, scales [N, ceil(K/group)] bfloat16), P = K rounded up to 128; with
-    zeros=True a zero point for each group as well, uint8 like the scales.  group is 32, 64
-    or 128.  `out` may supply the tuple that the call returns."""
+    (codes [N, K/2] uint8, scales [N, ceil(K/group)] bfloat16); with zeros=True a zero point
+    for each group as well, uint8 like the scales.  group is 32, 64 or 128.  Byte j of 16 codes
+    holds column j of 32 in its low half and column 16 + j in its high half.  `out` may supply the tuple that the call returns."""
     import torch
     if not isinstance(w, torch.Tensor):
         raise TypeError("w must be a torch.Tensor")
@@ -1048,7 +1048,7 @@ def q4_encode(w, *, group: int = 128, zeros: bool = False, out=None, stream=None
     N, K = w.shape
     kg = -(-K // group)
     u8 = torch.uint8
-    shapes = ((N, _blocks(K) * 64), (N, kg)) + (((N, kg),) if zeros else ())
+    shapes = ((N, K // 2), (N, kg)) + (((N, kg),) if zeros else ())
     out, po = _outputs(out, ("codes", "scales", "zeros"), shapes,
                        (u8, torch.bfloat16, u8)[:len(shapes)], w.device)
     _call("mhc_q4_encode", w.get_device(),

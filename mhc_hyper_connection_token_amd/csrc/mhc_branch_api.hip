@@ -54,7 +54,7 @@ struct Q4Spans {
 Q4Spans q4_spans(const void* codes, const void* scales, const void* zeros, size_t N, size_t K,
                  size_t group) {
   const size_t groups = N * ((K + group - 1) / group);
-  return Q4Spans{span(codes, N * mhc::blocks_of(K) * 64), span(scales, groups * 2),
+  return Q4Spans{span(codes, N * (K / 2)), span(scales, groups * 2),
                  span(zeros, zeros ? groups : 0)};
 }
 

@@ -2,8 +2,8 @@
 // for, a zero point per group, and back.  Done once per weight.
 //
 // A thread holds four neighbouring columns; a group's G/4 threads are neighbouring lanes
-// and exchange its extremes.  The code dword of an octet of columns is put together by the
-// lane of its lower half.
+// and exchange its extremes.  The code dword of an octet of columns (mhc_q4.h) is put together
+// by the lane of its low halves; the high ones are four lanes on.
 #include "mhc_norm.h"
 #include "mhc_q4.h"
 
@@ -18,14 +18,13 @@ __device__ __forceinline__ float to_bf16(float v) {  // the value, rounded to ne
 }
 }  // namespace
 
-// Codes of padding columns (past K, up to a multiple of 128) are zero.
 template <int G, int KIND>
 __global__ __launch_bounds__(256) void q4_encode_kernel(const void* __restrict__ w, int N,
                                                         int K, int KG,
                                                         unsigned char* __restrict__ codes,
                                                         __hip_bfloat16* __restrict__ scales,
                                                         unsigned char* __restrict__ zeros) {
-  const int PQ = (K + 127) / 128 * 32;  // quads of a row, padding included
+  const int PQ = (K + 127) / 128 * 32;  // quads of a row, up to whole groups
   const size_t total = (size_t)N * PQ;
   // whole waves stay in the loop: the exchange below needs every lane of a group
   for (size_t at = (size_t)blockIdx.x * 256 + threadIdx.x; at - (threadIdx.x & 63) < total;
@@ -61,12 +60,10 @@ __global__ __launch_bounds__(256) void q4_encode_kernel(const void* __restrict__
       const float c = x[i] == x[i] ? fminf(fmaxf(rintf(x[i] / d) + z, least), 15.f) : z;
       mine |= (unsigned)c << (8 * i);
     }
-    if (!real) mine = 0;
-    const unsigned high = __shfl_xor(mine, 1);
-    if (in && !(q & 1)) {
-      const int o = q >> 1, s = o >> 4, b = (o >> 2) & 3, g = o & 3;
-      reinterpret_cast<unsigned*>(codes)[n * (PQ / 2) + s * 16 + g * 4 + b] = mine | (high << 4);
-    }
+    const unsigned high = __shfl_xor(mine, 4);
+    if (real && !(q & 4))
+      reinterpret_cast<unsigned*>(codes)[n * (K / 8) + (q >> 3) * 4 + (q & 3)] =
+          mine | (high << 4);
     if (real && q % (G / 4) == 0) {
       scales[n * KG + q / (G / 4)] = __float2bfloat16(d);
       if (zeros) zeros[n * KG + q / (G / 4)] = (unsigned char)z;
@@ -80,13 +77,13 @@ __global__ __launch_bounds__(256) void q4_decode_kernel(const unsigned char* __r
                                                         const unsigned char* __restrict__ zeros,
                                                         int N, int K, int KG, int gshift,
                                                         float* __restrict__ out) {
-  const int KO = K / 8, PO = (K + 127) / 128 * 16;  // octets of a row, and with padding
+  const int KO = K / 8;  // octets of a row
   const size_t total = (size_t)N * KO;
   for (size_t at = (size_t)blockIdx.x * 256 + threadIdx.x; at < total;
        at += (size_t)gridDim.x * 256) {
     const size_t n = at / KO;
-    const int o = (int)(at - n * KO), s = o >> 4, b = (o >> 2) & 3, g = o & 3;
-    const unsigned c = reinterpret_cast<const unsigned*>(codes)[n * PO + s * 16 + g * 4 + b];
+    const int o = (int)(at - n * KO);
+    const unsigned c = reinterpret_cast<const unsigned*>(codes)[at];
     const size_t k = n * KG + (o >> (2 + gshift));
     const float d = q4_scale(scales[k], f16), z = zeros ? (float)zeros[k] : 8.f;
     float v[8];
@@ -95,9 +92,9 @@ __global__ __launch_bounds__(256) void q4_decode_kernel(const unsigned char* __r
       v[i] = ((float)((c >> (8 * i)) & 15) - z) * d;
       v[4 + i] = ((float)((c >> (8 * i + 4)) & 15) - z) * d;
     }
-    float4* p = reinterpret_cast<float4*>(out + at * 8);
+    float4* p = reinterpret_cast<float4*>(out + n * K + (o >> 2) * 32 + (o & 3) * 4);
     p[0] = make_float4(v[0], v[1], v[2], v[3]);
-    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+    p[4] = make_float4(v[4], v[5], v[6], v[7]);
   }
 }
 

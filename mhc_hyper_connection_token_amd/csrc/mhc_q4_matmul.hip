@@ -18,8 +18,6 @@
 
 namespace mhc {
 
-typedef int intx2 __attribute__((ext_vector_type(2)));
-
 namespace {
 
 enum Act { kActF32 = 0, kActBF16 = 1, kActQ8 = 2 };
@@ -55,10 +53,6 @@ struct Q4Args {
 };
 
 
-__device__ __forceinline__ void octet_values(const Octet<kActF32>& o, float* v) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = o.v[e >> 2][e & 3];
-}
 __device__ __forceinline__ void octet_values(const Octet<kActBF16>& o, float* v) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -74,164 +68,138 @@ __device__ __forceinline__ void store_one(const Q4Args& p, size_t at, float v) {
     static_cast<float*>(p.out)[at] = v;
 }
 
-// N bytes at an address that is a multiple of N, zero-extended to whole dwords.
-template <int N>
-__device__ __forceinline__ void load_bits(unsigned* to, const void* from) {
-  if constexpr (N == 1)
-    *to = *static_cast<const unsigned char*>(from);
-  else if constexpr (N == 2)
-    *to = *static_cast<const unsigned short*>(from);
-  else
-    __builtin_memcpy(to, __builtin_assume_aligned(from, N), N);
-}
-
 }  // namespace
 
 // ---------------------------------------------------------------- one row
-// A lane holds the activations of 32 columns (an octet in each of a superblock's four
-// blocks) and meets the rows of the weight with them, 16 bytes of each: R rows at a time,
-// `iters` times, the next R on their way.  A wave's 64 lanes cover 2048 columns; the block's
-// W waves are KS slices of the depth times W / KS runs of R * iters rows, whose sums meet in
-// LDS.  us at 4096 x 4096, 16384 x 4096 and 28672 x 7168 (int8; bf16; bf16): 4.4, 9.5, 23.7
-// (4.5 TB/s); fp32 10.4 at the second, 11.5 with 64-column groups and zero points.  Without the
-// products the loads alone take 8.9 and 21.3: what is left above the floor is the conversion
-// and the products (2 instructions a weight in fp32) that the loads do not hide, and the
-// first loads' latency.  R = 2, 4, 8: 9.6, 10.1, 11.6 at 16384 x 4096 in bf16.
+// A lane holds the activations of a block of 32 columns and meets the rows of the weight with
+// them, the block's 16 bytes of each: R rows at a time, `iters` times, the next R on their
+// way.  A wave's 64 lanes cover 2048 columns; the block's W waves are KS slices of the depth
+// times W / KS runs of R * iters rows, whose sums meet in LDS.  us at 4096 x 4096, 16384 x 4096
+// and 28672 x 7168 (int8; bf16; bf16): 4.2, 9.3, 24.0 (4.5 TB/s); fp32 10.0 at the second, 10.4
+// with 64-column groups and zero points.
 constexpr int kVectorRows = 64;  // rows of a wave at most
 
 template <int A, int GS, bool ZEROS, int R, int W>
 __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int iters) {
-  constexpr int GB = 1 << GS, NG = 4 / GB;  // blocks of 32 a group, groups in a superblock
   __shared__ float part[W][kVectorRows];
+  __shared__ floatx4 turn[A == kActF32 ? W : 1][A == kActF32 ? 64 * 5 : 1];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int KB = p.K / kQ4Block, SB = (p.K + 127) / 128, g = lane & 3;
+  const int KB = p.K / kQ4Block;
   const int slice = wave % KS, runs = W / KS, rows = R * iters;
   const int n0 = (blockIdx.x * runs + wave / KS) * rows;
-  const size_t pitch = (size_t)SB * 64;
-  const bool whole = p.K % 128 == 0;
-  for (int s0 = slice * 16; s0 < SB; s0 += KS * 16) {
-    // lanes past the end read the last superblock, times zeros
-    const int s = min(s0 + (lane >> 2), SB - 1);
-    const bool in = s0 + (lane >> 2) < SB;
-    const unsigned code_at = s * 64u + g * 16u;
+  const size_t pitch = (size_t)KB * 16;
+  for (int k0 = slice * 64; k0 < KB; k0 += KS * 64) {
+    // lanes past the end read the last block, times zeros
+    const int k = min(k0 + lane, KB - 1);
+    const bool in = k0 + lane < KB;
+    const unsigned code_at = k * 16u, group = k >> GS;
     intx4 cn[R];
-    // a row's scales and zero points as they were loaded: taken apart here, where two paths
-    // meet, they would be waited for
-    unsigned bits[R][(NG + 1) / 2], zero[R];
+    // a row's scale and zero point as they were loaded: converted here, they would be waited for
+    unsigned short sn[R];
+    unsigned char zn[R];
     auto fetch = [&](int n) {  // rows past the end: the last one, whose sums are not stored
 #pragma unroll
       for (int i = 0; i < R; ++i)
         cn[i] = __builtin_nontemporal_load(reinterpret_cast<const intx4*>(
             p.codes + (size_t)min(n + i, p.N - 1) * pitch + code_at));
-      if (NG == 1 || whole) {  // all groups are there, and aligned to their number
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const size_t at = (size_t)min(n + i, p.N - 1) * p.KG + (unsigned)(s * NG);
-          load_bits<2 * NG>(bits[i], p.scales + at);
-          if constexpr (ZEROS) load_bits<NG>(&zero[i], p.zeros + at);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-#pragma unroll
-          for (int k = 0; k < (NG + 1) / 2; ++k) bits[i][k] = 0;
-          zero[i] = 0;
-#pragma unroll
-          for (int k = 0; k < NG; ++k) {
-            const size_t at =
-                (size_t)min(n + i, p.N - 1) * p.KG + (unsigned)min(s * NG + k, p.KG - 1);
-            bits[i][k / 2] |= (unsigned)p.scales[at] << (16 * (k % 2));
-            if constexpr (ZEROS) zero[i] |= (unsigned)p.zeros[at] << (8 * k);
-          }
-        }
+      for (int i = 0; i < R; ++i) {
+        const size_t at = (size_t)min(n + i, p.N - 1) * p.KG + group;
+        sn[i] = p.scales[at];
+        if constexpr (ZEROS) zn[i] = p.zeros[at];
       }
     };
     // the activations first: loads are waited for in the order they were asked for in
-    Octet<A> ao[4];
     intx2 aq[4];
-    float av[4][8], ad[4], as[NG];
-    int qs[4];
+    float av[32], ad = 0.f, as = 0.f;
+    int qs = 0;
+    if constexpr (A == kActF32) {
+      // asked for in whole half blocks, four lanes each, and turned about in LDS (a lane's own
+      // 128 bytes at a time are 64 lines a load: 4.9 -> 6.4 us at 4096 x 4096)
+      floatx4 v[2][4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int k = min(4 * s + b, KB - 1);
-      ao[b] = *reinterpret_cast<const Octet<A>*>(
-          p.a + (unsigned)(k * kQ4Block + 8 * g) * (unsigned)act_size<A>());
-      if constexpr (A == kActQ8) ad[b] = p.ad[k];
-    }
-    fetch(n0);
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      if (!in || 4 * s + b >= KB) __builtin_memset(&ao[b], 0, sizeof(ao[b]));
-      if constexpr (A == kActQ8) {
-        aq[b] = ao[b].v;
-        if (!in || 4 * s + b >= KB) ad[b] = 0.f;
-      } else {
-        octet_values(ao[b], av[b]);
-      }
-    }
-    if constexpr (A == kActQ8) {
+        for (int i = 0; i < 4; ++i)
+          v[h][i] = reinterpret_cast<const floatx4*>(p.a)[min(k0 + 16 * i + (lane >> 2), KB - 1) * 8 +
+                                                         4 * h + (lane & 3)];
+      fetch(n0);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        qs[b] = __builtin_amdgcn_sdot4(aq[b][0], 0x01010101, 0, false);
-        qs[b] = __builtin_amdgcn_sdot4(aq[b][1], 0x01010101, qs[b], false);
+      for (int h = 0; h < 2; ++h) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) turn[wave][(16 * i + (lane >> 2)) * 5 + (lane & 3)] = v[h][i];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const floatx4 u = turn[wave][lane * 5 + i];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) av[16 * h + 4 * i + e] = in ? u[e] : 0.f;
+        }
       }
     } else {
+      Octet<A> ao[4];
 #pragma unroll
-      for (int k = 0; k < NG; ++k) {
-        as[k] = 0.f;
+      for (int o = 0; o < 4; ++o)
+        ao[o] = *reinterpret_cast<const Octet<A>*>(
+            p.a + (unsigned)(k * kQ4Block + 8 * o) * (unsigned)act_size<A>());
+      if constexpr (A == kActQ8) ad = p.ad[k];
+      fetch(n0);
 #pragma unroll
-        for (int b = k * GB; b < (k + 1) * GB; ++b)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) as[k] += av[b][e];
+      for (int o = 0; o < 4; ++o) {
+        if (!in) __builtin_memset(&ao[o], 0, sizeof(ao[o]));
+        if constexpr (A == kActQ8) {
+          aq[o] = ao[o].v;
+          qs = __builtin_amdgcn_sdot4(aq[o][0], 0x01010101, qs, false);
+          qs = __builtin_amdgcn_sdot4(aq[o][1], 0x01010101, qs, false);
+        } else {
+          octet_values(ao[o], av + 8 * o);
+        }
       }
+      if (A == kActQ8 && !in) ad = 0.f;
+    }
+    if constexpr (A != kActQ8) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) as += av[e];
     }
     for (int it = 0; it < iters; ++it) {
       intx4 cv[R];
-      float sv[R][NG], zv[R][NG];
+      float sv[R], zv[R];
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         cv[i] = cn[i];
-#pragma unroll
-        for (int k = 0; k < NG; ++k) {
-          sv[i][k] = q4_scale((unsigned short)(bits[i][k / 2] >> (16 * (k % 2))), p.f16);
-          zv[i][k] = ZEROS ? (float)(zero[i] >> (8 * k) & 255) : 8.f;
-        }
+        sv[i] = q4_scale(sn[i], p.f16);
+        zv[i] = ZEROS ? (float)zn[i] : 8.f;
       }
       if (it + 1 < iters) fetch(n0 + R * (it + 1));
       float acc[R];
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        acc[i] = 0.f;
+        if constexpr (A == kActQ8) {
+          int v = -(int)zv[i] * qs;
 #pragma unroll
-        for (int k = 0; k < NG; ++k) {
-          float t;
-          if constexpr (A == kActQ8) {
-            t = 0.f;
-#pragma unroll
-            for (int b = k * GB; b < (k + 1) * GB; ++b) {
-              int v = -(int)zv[i][k] * qs[b];
-              v = __builtin_amdgcn_sdot4(aq[b][0], q4_low(cv[i][b]), v, false);
-              v = __builtin_amdgcn_sdot4(aq[b][1], q4_high(cv[i][b]), v, false);
-              t = fmaf((float)v, ad[b], t);
-            }
-            acc[i] = fmaf(sv[i][k], t, acc[i]);
-          } else {
-            // codes come as multiples of 2^-9 (mhc_q4.h): so does the zero point, and the
-            // sum is made up for it (a scale may be the type's largest)
-            t = -(zv[i][k] * 0.001953125f) * as[k];
-#pragma unroll
-            for (int b = k * GB; b < (k + 1) * GB; ++b) {
-              const int lo = q4_low(cv[i][b]), hi = q4_high(cv[i][b]);
-              const floatx2 c[4] = {__builtin_amdgcn_cvt_pk_f32_fp8(lo, false),
-                                    __builtin_amdgcn_cvt_pk_f32_fp8(lo, true),
-                                    __builtin_amdgcn_cvt_pk_f32_fp8(hi, false),
-                                    __builtin_amdgcn_cvt_pk_f32_fp8(hi, true)};
-#pragma unroll
-              for (int e = 0; e < 8; ++e) t = fmaf(c[e >> 1][e & 1], av[b][e], t);
-            }
-            acc[i] = fmaf(sv[i][k], t * 512.f, acc[i]);
+          for (int d = 0; d < 4; ++d) {  // columns 4 d .. + 3 and 16 + 4 d .. + 3
+            v = __builtin_amdgcn_sdot4(aq[d >> 1][d & 1], q4_low(cv[i][d]), v, false);
+            v = __builtin_amdgcn_sdot4(aq[2 + (d >> 1)][d & 1], q4_high(cv[i][d]), v, false);
           }
+          acc[i] = sv[i] * ((float)v * ad);
+        } else {
+          // codes come as multiples of 2^-9 (mhc_q4.h): so does the zero point, and the
+          // sum is made up for it (a scale may be the type's largest)
+          float t = -(zv[i] * 0.001953125f) * as;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const int lo = q4_low(cv[i][d]), hi = q4_high(cv[i][d]);
+            const floatx2 c[4] = {__builtin_amdgcn_cvt_pk_f32_fp8(lo, false),
+                                  __builtin_amdgcn_cvt_pk_f32_fp8(lo, true),
+                                  __builtin_amdgcn_cvt_pk_f32_fp8(hi, false),
+                                  __builtin_amdgcn_cvt_pk_f32_fp8(hi, true)};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              t = fmaf(c[e >> 1][e & 1], av[16 * (e >> 2) + 4 * d + (e & 3)], t);
+          }
+          acc[i] = sv[i] * (t * 512.f);
         }
       }
 #pragma unroll
@@ -240,13 +208,13 @@ __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           float* to = &part[wave][R * it + i];
-          *to = s0 == slice * 16 ? acc[i] : *to + acc[i];
+          *to = k0 == slice * 64 ? acc[i] : *to + acc[i];
         }
     }
   }
   __syncthreads();
   // (a slice past the end of the depth has no sums)
-  const int full = min(KS, (SB + 15) / 16);
+  const int full = min(KS, (KB + 63) / 64);
   for (int i = threadIdx.x; i < runs * rows; i += 64 * W) {
     const int run = i / rows, row = i - run * rows, n = (blockIdx.x * runs + run) * rows + row;
     float v = part[run * KS][row];
@@ -266,16 +234,23 @@ __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int
 // us at 2, 8 and 16 rows of 16384 x 4096: bf16 10.7 (3 rows), 11.7, 12.5; fp32 11.1, 15.3,
 // 18.4; int8 10.7, 13.2, 13.6; with the activations read by every wave 16.6 at 8 rows in
 // bf16.  What is left above the floor: two barriers a stage of 1024 columns, 700 clocks each.
-// Within a row of codes the 16-byte unit i lies at place i ^ (row % 16), and a row of
-// activations is 16 bytes longer than it needs, so that sixteen rows read at one unit meet
-// all banks.
+// A row, of codes and of activations, is 16 bytes longer than it needs, so that sixteen rows
+// read at one place meet all banks.
+// Which four octets (mhc_q4.h) an instruction sums: of a superblock's sixteen, lane group g
+// takes octet i of block g in instruction i where a group is the superblock, and octet 2 i + g %
+// 2 of block 2 k + g / 2 in instruction i of group k where it is two blocks.  Where a group is one
+// block, and with int8 activations, whose scales change by block, an instruction sums one block:
+// lane group g takes its dword g, columns 4 g .. + 3 and 16 + 4 g .. + 3, and activations in
+// fp32 and bf16 are put into LDS in that order.  (Octets of one block would be two dwords a lane
+// and block: 8 x 7168 x 7168 in int8 16.1 us, so 12.7.)
 // FEW (at most four rows): row r of the instruction is row r / 4 of a, and a lane ends with
 // one sum, of row lane / 16.  With fp32 activations the rows 4 m, + 1, + 2 are the three
 // planes of row m, so one instruction does what takes three from five rows on.
 template <int A, int GS, bool FEW, int NF, int W>
 struct RowsLayout {
   static constexpr int NG = 4 >> GS;                       // groups in a superblock
-  static constexpr int CODES = 16 * NF * 64 * W;  // bytes of a stage
+  static constexpr int CPITCH = 64 * W + 16;       // of a row of codes
+  static constexpr int CODES = 16 * NF * CPITCH;  // bytes of a stage
   static constexpr int SCALES = 16 * NF * W * NG * 8;
   static constexpr int PITCH = 128 * W * (A == kActQ8 ? 1 : 2) + 16;  // of a row of a
   static constexpr int DPITCH = 4 * W + 4;        // floats, of a row of its scales
@@ -289,6 +264,7 @@ __global__ __launch_bounds__(64 * W) void q4_rows_kernel(Q4Args p) {
   using L = RowsLayout<A, GS, FEW, NF, W>;
   constexpr int NT = 64 * W, NG = L::NG;
   constexpr int GB = 1 << GS;                       // blocks of 32 a group
+  constexpr int IG = A == kActQ8 ? 0 : GS;          // ... that an instruction's octets come from
   constexpr int MV = FEW ? 1 : 4;                   // sums a lane ends with, per tile
   constexpr int PL = A == kActF32 && !FEW ? 3 : 1;  // instructions a tile and block
   constexpr int UR = 4 * W, UA = 8 * W * act_size<A>();  // 16-byte units of a row, of codes and a
@@ -321,8 +297,7 @@ __global__ __launch_bounds__(64 * W) void q4_rows_kernel(Q4Args p) {
     ap[i] = p.a + (size_t)((threadIdx.x + NT * i) / UA) * p.K * act_size<A>();
 #pragma unroll
   for (int i = 0; i < NF; ++i)
-    bp[i] = p.codes + (size_t)min(n0 + (int)(NT * i + threadIdx.x) / UR, p.N - 1) * SB * 64 +
-            (threadIdx.x & 3) * 16;
+    bp[i] = p.codes + (size_t)min(n0 + (int)(NT * i + threadIdx.x) / UR, p.N - 1) * KB * 16;
 #pragma unroll
   for (int i = 0; i < NS; ++i)
     sp[i] = (size_t)min(n0 + (int)(threadIdx.x + NT * i) / (W * NG), p.N - 1) * p.KG;
@@ -338,11 +313,11 @@ __global__ __launch_bounds__(64 * W) void q4_rows_kernel(Q4Args p) {
       dn = p.ad[(size_t)min((int)threadIdx.x / (4 * W), p.M - 1) * KB +
                 min(4 * sb + (int)threadIdx.x % (4 * W), KB - 1)];
   };
-  auto fetch_w = [&](int sb, auto turn) {  // a superblock past the end: the last one, times zeros
+  auto fetch_w = [&](int sb, auto turn) {  // a block past the end: the last one, times zeros
     constexpr int T = decltype(turn)::value;
 #pragma unroll
     for (int i = 0; i < NF; ++i) {
-      const unsigned at = min(sb + (int)(threadIdx.x % UR) / 4, SB - 1) * 64u;
+      const unsigned at = min(4 * sb + (int)(threadIdx.x % UR), KB - 1) * 16u;
       cn[T][i] = __builtin_nontemporal_load(reinterpret_cast<const intx4*>(bp[i] + at));
     }
 #pragma unroll
@@ -367,7 +342,7 @@ __global__ __launch_bounds__(64 * W) void q4_rows_kernel(Q4Args p) {
 #pragma unroll
     for (int i = 0; i < NF; ++i) {
       const int row = (NT * i + threadIdx.x) / UR, unit = threadIdx.x % UR;
-      reinterpret_cast<intx4*>(lds)[row * UR + (unit ^ (row & 15))] = cn[T][i];
+      reinterpret_cast<intx4*>(lds)[row * (L::CPITCH / 16) + unit] = cn[T][i];
     }
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
@@ -393,8 +368,17 @@ __global__ __launch_bounds__(64 * W) void q4_rows_kernel(Q4Args p) {
             v[2 * h] -= __uint_as_float(lo & 0xffff0000u);
             v[2 * h + 1] -= __uint_as_float(hi & 0xffff0000u);
           }
+          const int to = IG == 0 ? (c >> 3) * 64 + (c & 3) * 16 + (c >> 2 & 1) * 8 : 8 * c;
           __builtin_memcpy(
-              __builtin_assume_aligned(acts + (3 * m + l) * L::PITCH + 8 * c, 8), u, 8);
+              __builtin_assume_aligned(acts + (3 * m + l) * L::PITCH + to, 8), u, 8);
+        }
+      } else if constexpr (A == kActBF16 && IG == 0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // columns 8 c + 4 h .. + 3 of the row
+          const int u[2] = {an[i][2 * h], an[i][2 * h + 1]};
+          __builtin_memcpy(
+              __builtin_assume_aligned(acts + m * L::PITCH + (c >> 2) * 64 + (c & 1) * 32 + h * 16 +
+                                           (c >> 1 & 1) * 8, 8), u, 8);
         }
       } else {
         __builtin_memcpy(__builtin_assume_aligned(acts + m * L::PITCH + 16 * c, 16), &an[i], 16);
@@ -416,8 +400,32 @@ __global__ __launch_bounds__(64 * W) void q4_rows_kernel(Q4Args p) {
   auto multiply = [&] {
     intx4 cv[NF];
 #pragma unroll
-    for (int j = 0; j < NF; ++j)
-      cv[j] = reinterpret_cast<const intx4*>(lds)[(16 * j + r) * UR + ((4 * wave + g) ^ r)];
+    for (int j = 0; j < NF; ++j) {
+      const unsigned char* at = lds + (16 * j + r) * L::CPITCH + 64 * wave;
+      if constexpr (IG == 2) {
+        cv[j] = reinterpret_cast<const intx4*>(at)[g];
+      } else if constexpr (IG == 1) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const intx2 c = reinterpret_cast<const intx2*>(at)[4 * k + g];
+          cv[j][2 * k] = c[0];
+          cv[j][2 * k + 1] = c[1];
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) cv[j][b] = reinterpret_cast<const int*>(at)[4 * b + g];
+      }
+    }
+    // the codes of the lane's octet in each instruction, four to a dword
+    const auto codes = [&](int j, int b) -> intx2 {
+      const intx4 v = cv[j];
+      if constexpr (IG == 0) {
+        return intx2{q4_low(v[b]), q4_high(v[b])};
+      } else {
+        const int p = IG == 2 ? b & 1 : b >> 1, high = IG == 2 ? b >> 1 : b & 1;
+        return q4_octet(v[2 * p], v[2 * p + 1], high);
+      }
+    };
     float4 dv[MV];
     if constexpr (A == kActQ8)
 #pragma unroll
@@ -437,16 +445,16 @@ __global__ __launch_bounds__(64 * W) void q4_rows_kernel(Q4Args p) {
         }
       }
       if constexpr (A == kActQ8) {
-        long ax;
-        __builtin_memcpy(&ax,
-                         __builtin_assume_aligned(
-                             acts + am * L::PITCH + 128 * wave + 32 * b + 8 * g, 8), 8);
+        const int* at =
+            reinterpret_cast<const int*>(acts + am * L::PITCH + 128 * wave + 32 * b) + g;
+        const long ax = (long)(unsigned)at[0] | ((long)at[4] << 32);
         const intx4 none{0, 0, 0, 0};
         const intx4 q =
             __builtin_amdgcn_mfma_i32_16x16x32_i8(ax, 0x0101010101010101L, none, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
-          const long cx = (long)(unsigned)q4_low(cv[j][b]) | ((long)q4_high(cv[j][b]) << 32);
+          const intx2 c = codes(j, b);
+          const long cx = (long)(unsigned)c[0] | ((long)c[1] << 32);
           const intx4 t = __builtin_amdgcn_mfma_i32_16x16x32_i8(ax, cx, none, 0, 0, 0);
           const int z = (int)sz[j].y;
 #pragma unroll
@@ -462,14 +470,17 @@ __global__ __launch_bounds__(64 * W) void q4_rows_kernel(Q4Args p) {
 #pragma unroll
         for (int l = 0; l < PL; ++l) {
           const int row = A == kActBF16 ? am : FEW ? 3 * am + min(r & 3, 2) : 3 * am + l;
+          const int octet = IG == 2   ? 4 * g + b
+                            : IG == 1 ? 8 * (b >> 1) + 4 * (g >> 1) + 2 * (b & 1) + (g & 1)
+                                      : 4 * b + g;
           __builtin_memcpy(&ax[l],
                            __builtin_assume_aligned(
-                               acts + row * L::PITCH + 256 * wave + 64 * b + 16 * g, 16), 16);
+                               acts + row * L::PITCH + 256 * wave + 16 * octet, 16), 16);
           ones = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ax[l], one, ones, 0, 0, 0);
         }
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
-          const bf16x8 cx = q4_to_bf16(cv[j][b]);
+          const bf16x8 cx = q4_to_bf16(codes(j, b));
 #pragma unroll
           for (int l = 0; l < PL; ++l)
             sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ax[l], cx, sum[j], 0, 0, 0);
@@ -603,8 +614,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
                       act_size<A>();
 #pragma unroll
   for (int i = 0; i < NB; ++i)
-    bp[i] = p.codes + (size_t)min(n0 + (int)(threadIdx.x + TH * i) / 4 % BN, p.N - 1) * SB * 64 +
-            (threadIdx.x & 3) * 16;
+    bp[i] = p.codes + (size_t)min(n0 + (int)(threadIdx.x + TH * i) / 4 % BN, p.N - 1) * KB * 16;
 #pragma unroll
   for (int i = 0; i < NS; ++i)
     sp[i] = (size_t)min(n0 + (int)(threadIdx.x + TH * i) / NG % BN, p.N - 1) * p.KG;
@@ -620,8 +630,9 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
     }
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      const int s = min(sb + (int)(threadIdx.x + TH * i) / 4 / BN, SB - 1);
-      bn[i] = *reinterpret_cast<const intx4*>(bp[i] + (unsigned)(s * 64));
+      const int at = threadIdx.x + TH * i;
+      const int k = min(4 * (sb + at / 4 / BN) + (at & 3), KB - 1);
+      bn[i] = *reinterpret_cast<const intx4*>(bp[i] + (unsigned)(k * 16));
     }
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
@@ -725,26 +736,40 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
     const float* sums = reinterpret_cast<const float*>(acts + L::ACTS);
     const float2* scales = reinterpret_cast<const float2*>(acts + L::ACTS + L::SUMS);
     constexpr int ROLL = GS == 0 ? 1 : NG;
+    // A lane half reads NO dwords, as many octets, at a time: whole blocks, every second one,
+    // or, where a group is one block, half of it, octets h and 2 + h.
+    constexpr int NO = GB > 1 ? 4 : 2, NU = 2 * GB / NO;
 #pragma unroll ROLL
     for (int k = 0; k < NG; ++k) {
       float2 sz[FN];
       bf16x8 bx[FN][2 * GB];
+      int c[FN][NU][NO];
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         const int n = (wn * FN + j) * 32 + r;
         sz[j] = scales[k * BN + n];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          int c[GB];  // an octet of each of the group's blocks
+        for (int u = 0; u < NU; ++u) {
+          const int first = NO * (GB > 1 ? 2 * u + h : h);  // of the group's dwords
           __builtin_memcpy(
-              c,
+              c[j][u],
               __builtin_assume_aligned(
-                  part + (n * 4 + ((2 * u + h) ^ ((n >> 2) & 3))) * 16 + k * GB * 4, 4 * GB),
-              4 * GB);
-#pragma unroll
-          for (int b = 0; b < GB; ++b) bx[j][2 * b + u] = q4_to_bf16(c[b]);
+                  part + (n * 4 + ((k * GB + (first >> 2)) ^ ((n >> 2) & 3))) * 16 +
+                      (first & 3) * 4, 4 * NO),
+              4 * NO);
         }
       }
+      // Left alone, the second read moves in among the products, which then wait for it: 500 x
+      // 7168 x 7168 in bf16 96 us, so 90.
+      if constexpr (NU > 1) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+#pragma unroll
+          for (int i = 0; i < NO; ++i)
+            bx[j][NO * u + i] =
+                q4_to_bf16(q4_octet(c[j][u][2 * i % NO], c[j][u][2 * i % NO + 1], i / (NO / 2)));
       // the tiles take turns, so that no product waits for the one before it
       floatx16 t[FM][FN];
 #pragma unroll
@@ -765,10 +790,12 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
         for (int i = 0; i < FM; ++i)
 #pragma unroll
           for (int b = 0; b < 2 * GB; ++b) {
-            const int m = (wm * FM + i) * 32 + r, unit = 4 * (k * GB + (b >> 1)) + 2 * (b & 1) + h;
+            const int m = (wm * FM + i) * 32 + r;
+            const int octet =
+                GB > 1 ? 4 * (k * GB + 2 * (b / NO) + h) + b % NO : 4 * k + 2 * b + h;
             __builtin_memcpy(&ax[i][b],
                              __builtin_assume_aligned(
-                                 acts + ((l * BM + m) * 16 + (unit ^ (m & 15))) * 16, 16), 16);
+                                 acts + ((l * BM + m) * 16 + (octet ^ (m & 15))) * 16, 16), 16);
           }
 #pragma unroll
         for (int b = 0; b < 2 * GB; ++b)

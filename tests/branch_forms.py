@@ -49,15 +49,14 @@ def norm_bwd(dz, dz_size, y, nw, eps):
 def byte_of(col):
     """Byte in a row of codes, and the half of it (0 low, 1 high), of each column."""
     col = np.asarray(col)
-    return (col // 128 * 64 + col % 32 // 8 * 16 + col % 128 // 32 * 4 + col % 4,
-            col % 8 // 4)
+    return col // 32 * 16 + col % 16, col % 32 // 16
 
 
 def pack(c):
-    """Codes [N, K] -> bytes [N, P/2]."""
+    """Codes [N, K] -> bytes [N, K/2]."""
     c = np.asarray(c, np.uint8)
     N, K = c.shape
-    out = np.zeros((N, -(-K // 128) * 64), np.uint8)
+    out = np.zeros((N, K // 2), np.uint8)
     at, half = byte_of(np.arange(K))
     for k in range(K):
         out[:, at[k]] |= c[:, k] << np.uint8(4 * half[k])
