@@ -901,8 +901,8 @@ def site_post_norm(x, f, nw, post, comb, eps: float = 1e-5, *, gate=None, gate_a
     """site_post of h = alpha * a(gate) * f / sqrt(mean f^2 + eps) * nw: the norm behind a
     branch, its gate and the residual scale, in the post mix.  x [T,S,H], f [T,H] (float32 or
     bfloat16), nw [H], post [T,S], comb [T,S,S]; gate [H] or [T,H] (float32 or bfloat16) or
-    None; gate_act None (a(gate) = gate), "sigmoid" or "silu".  Returns x' [T,S,H]; `out` may
-    supply it."""
+    None; gate_act None (a(gate) = gate), "sigmoid" or "silu", not read without a gate.  Returns
+    x' [T,S,H]; `out` may supply it."""
     import torch
     if stream is not None:
         return _on(stream, x.device, site_post_norm, x, f, nw, post, comb, eps, gate=gate,
@@ -912,9 +912,10 @@ def site_post_norm(x, f, nw, post, comb, eps: float = 1e-5, *, gate=None, gate_a
     T, S, H = x.shape
     f32 = torch.float32
     px = _gpu(x, "x", f32)
-    args = (px, *_typed(f, "f", (T, H)), _gpu(nw, "nw", f32, (H,)), *_gate(gate, gate_act, T, H),
-            float(alpha), _gpu(post, "post", f32, (T, S)), _gpu(comb, "comb", f32, (T, S, S)),
-            T, S, H, float(eps))
+    args = (px, *_typed(f, "f", (T, H)), _gpu(nw, "nw", f32, (H,)),
+            *_gate(gate, gate_act if gate is not None else None, T, H), float(alpha),
+            _gpu(post, "post", f32, (T, S)), _gpu(comb, "comb", f32, (T, S, S)), T, S, H,
+            float(eps))
     if out is None:
         out = x.new_empty((T, S, H))
         po = out.data_ptr()
@@ -946,7 +947,7 @@ def site_post_norm_bwd(g, x, f, nw, post, comb, eps: float = 1e-5, *, gate=None,
         f_bf16 = 0
     else:
         (pf, f_bf16), pfs, tf = _typed(f, "f", (T, H)), None, (f,)
-    how = _gate(gate, gate_act, T, H)
+    how = _gate(gate, gate_act if gate is not None else None, T, H)
     names = ("dx", "df", "dpost", "dcomb", "dnw")
     shapes = ((T, S, H), (T, H), (T, S), (T, S, S), (H,))
     if gate is not None:
