@@ -561,11 +561,12 @@ int mhc_site_post_norm_bwd(const float* g, const void* x, const unsigned char* x
  *   MHC_BF16 (rounded to nearest even).
  *   a [M][K], a_type   MHC_F32 or MHC_BF16 with a_scales NULL; or MHC_I8 with a_scales
  *     [M][K/32], value a * a_scales: the q and d of mhc_site_pre_zq8
- *   Products are exact and summed in fp32 in an order fixed by the shape (int8: exactly
- *   within 32 columns for M <= 16, else of a * a_scales rounded to fp32); a part of an fp32
- *   value that is under 2^-126 may count as zero.  A
- *   row of a with an infinity or a NaN gives a row that is not finite; other rows do not
- *   see it.
+ *   Products with the codes are exact and summed in fp32 in an order fixed by the shape
+ *   (int8: exactly within 32 columns for M <= 16, else of a * a_scales rounded to fp32); the
+ *   scale is applied to a group's sum, so that 15 times the sum of |a| over a group must
+ *   stay within fp32 (it does for |a| up to 2^117), also where the scale is small.  A value
+ *   of a, or a part of one in fp32, that is under 2^-126 may count as zero.  A row of a with
+ *   an infinity or a NaN gives a row that is not finite; other rows do not see it.
  *
  * N <= 2^24, K <= 2^20, M <= 2^20, M * N < 2^31 (MHC_EUNSUPPORTED); K % 32 == 0
  * (MHC_EALIGN); M = 0 does nothing.  Pointers are 16-byte aligned; outputs must not

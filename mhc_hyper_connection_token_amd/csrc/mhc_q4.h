@@ -37,4 +37,10 @@ __device__ __forceinline__ intx2 q4_octet(int a, int b, int high) {
 // scale 2^9 gives the integer, two to an instruction.
 __device__ __forceinline__ bf16x8 q4_to_bf16(intx2 c) { return f8_to_bf16(c[0], c[1], 512.f); }
 
+// ... and two of four codes as fp32, the same way: the lower two or the upper two.
+template <bool UPPER>
+__device__ __forceinline__ floatx2 q4_to_f32(int c) {
+  return __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, 512.f, UPPER);
+}
+
 }  // namespace mhc

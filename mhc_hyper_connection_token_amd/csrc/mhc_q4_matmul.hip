@@ -185,21 +185,17 @@ __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int
           }
           acc[i] = sv[i] * ((float)v * ad);
         } else {
-          // codes come as multiples of 2^-9 (mhc_q4.h): so does the zero point, and the
-          // sum is made up for it (a scale may be the type's largest)
-          float t = -(zv[i] * 0.001953125f) * as;
+          float t = -zv[i] * as;
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
             const int lo = q4_low(cv[i][d]), hi = q4_high(cv[i][d]);
-            const floatx2 c[4] = {__builtin_amdgcn_cvt_pk_f32_fp8(lo, false),
-                                  __builtin_amdgcn_cvt_pk_f32_fp8(lo, true),
-                                  __builtin_amdgcn_cvt_pk_f32_fp8(hi, false),
-                                  __builtin_amdgcn_cvt_pk_f32_fp8(hi, true)};
+            const floatx2 c[4] = {q4_to_f32<false>(lo), q4_to_f32<true>(lo), q4_to_f32<false>(hi),
+                                  q4_to_f32<true>(hi)};
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               t = fmaf(c[e >> 1][e & 1], av[16 * (e >> 2) + 4 * d + (e & 3)], t);
           }
-          acc[i] = sv[i] * (t * 512.f);
+          acc[i] = sv[i] * t;
         }
       }
 #pragma unroll
