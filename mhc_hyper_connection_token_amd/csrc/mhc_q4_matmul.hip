@@ -61,6 +61,12 @@ __device__ __forceinline__ void octet_values(const Octet<kActBF16>& o, float* v)
   }
 }
 
+// A product rounded by itself, also where it is subtracted from next.
+__device__ __forceinline__ float mul_rounded(float a, float b) {
+#pragma clang fp contract(off)
+  return a * b;
+}
+
 __device__ __forceinline__ void store_one(const Q4Args& p, size_t at, float v) {
   if (p.bf16_out)
     static_cast<__hip_bfloat16*>(p.out)[at] = __float2bfloat16(v);
@@ -671,7 +677,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void q4_tile_kernel(Q4Args p, in
         } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            v[e] = (float)((signed char)(an[i][e >> 2] >> (8 * (e & 3)))) * dn[i];
+            v[e] = mul_rounded((float)((signed char)(an[i][e >> 2] >> (8 * (e & 3)))), dn[i]);
         }
 #pragma unroll
         for (int e = 0; e < NV; ++e) total += v[e];
