@@ -167,7 +167,12 @@ __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int
     }
     if constexpr (A != kActQ8) {
 #pragma unroll
-      for (int e = 0; e < 32; ++e) as += av[e];
+      for (int d = 0; d < 4; ++d) {  // in the products' order
+        float u = av[4 * d];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) u += av[16 * (e >> 2) + 4 * d + (e & 3)];
+        as += u;
+      }
     }
     for (int it = 0; it < iters; ++it) {
       intx4 cv[R];
@@ -191,17 +196,21 @@ __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int
           }
           acc[i] = sv[i] * ((float)v * ad);
         } else {
-          float t = -zv[i] * as;
+          // Four chains, and the zero points last: one chain from minus zero point times sum on
+          // has twice the error, 8e-7 of the result at 488 x 128, groups of 64.
+          float u[4];
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
             const int lo = q4_low(cv[i][d]), hi = q4_high(cv[i][d]);
             const floatx2 c[4] = {q4_to_f32<false>(lo), q4_to_f32<true>(lo), q4_to_f32<false>(hi),
                                   q4_to_f32<true>(hi)};
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              t = fmaf(c[e >> 1][e & 1], av[16 * (e >> 2) + 4 * d + (e & 3)], t);
+            for (int e = 0; e < 8; ++e) {
+              const float v = av[16 * (e >> 2) + 4 * d + (e & 3)];
+              u[d] = e == 0 ? c[0][0] * v : fmaf(c[e >> 1][e & 1], v, u[d]);
+            }
           }
-          acc[i] = sv[i] * t;
+          acc[i] = sv[i] * fmaf(-zv[i], as, (u[0] + u[1]) + (u[2] + u[3]));
         }
       }
 #pragma unroll

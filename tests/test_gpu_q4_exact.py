@@ -100,3 +100,33 @@ def test_errors_are_independent_roundings(mhc, M, kind, group, zeros):
     rms = ((v * v) @ (size * size).t()).mean().sqrt()
     off = (got - v @ w.t()).square().mean().sqrt()
     assert off <= ULP * (n / 3) ** 0.5 * rms, (off / (ULP * rms)).item()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_one_row_of_one_sign(mhc, kind):
+    """Activations of one sign, as behind a relu: sum code * a and zero point * sum a are far
+    larger than their difference.  One row sums a block of 32 columns, and its activations, in
+    four chains of 8 and then the chains: the mean square of the error is at most that of
+    independent roundings, each half a step of its partial sum at most and 1/sqrt(3) of that in
+    the mean (the partial sums are taken in 64 bits here)."""
+    print(f"[case] one sign {kind}", flush=True)
+    g = np.random.default_rng(5)
+    N, K, off, sums = 2000, 32, 0.0, 0.0
+    for turn in range(40):
+        c = g.integers(0, 16, (N, K)).astype(np.uint8)
+        v = torch.from_numpy((0.5 + g.random(K)).astype(np.float32))
+        v = v.bfloat16() if kind == "bf16" else v
+        got = mhc.q4_matmul(v[None].cuda(), torch.from_numpy(bf.pack(c)).cuda(),
+                            torch.ones(N, 1, dtype=torch.bfloat16).cuda()).double().cpu()[0]
+        a = v.double().numpy()
+        want = (c.astype(np.float64) - 8) @ a
+        off += np.square(got.numpy() - want).mean()
+        # columns 4 d .. + 3 and 16 + 4 d .. + 3 are chain d
+        order = np.concatenate([np.r_[4 * d:4 * d + 4, 16 + 4 * d:20 + 4 * d] for d in range(4)])
+        for terms, by in ((c[:, order] * a[order], 1.0), (a[None, order], 8.0)):
+            p = np.cumsum(terms.reshape(-1, 4, 8), 2)
+            t = p[:, :, 7]
+            last = [t[:, 0] + t[:, 1], t[:, 2] + t[:, 3], t.sum(1)]
+            sums += by ** 2 * (np.square(p).sum((1, 2)).mean() + sum(np.square(x).mean() for x in last))
+        sums += np.square(want).mean()
+    assert (off / 40) ** 0.5 <= ULP * (sums / 40 / 3) ** 0.5, ((off / sums * 3) ** 0.5 / ULP)
