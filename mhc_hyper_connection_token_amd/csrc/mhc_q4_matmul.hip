@@ -281,7 +281,7 @@ __global__ __launch_bounds__(64 * W) void q4_rows_kernel(Q4Args p) {
   constexpr int UR = 4 * W, UA = 8 * W * act_size<A>();  // 16-byte units of a row, of codes and a
   constexpr int RA = FEW ? 4 : 16;
   constexpr int NS = (16 * NF * W * NG + NT - 1) / NT, NA = (RA * UA + NT - 1) / NT;
-  static_assert(NF * W * 16 * UR * 4 >= NF * MV * W * 64, "the sums fit where the codes were");
+  static_assert(L::CODES >= NF * MV * W * 64 * 4, "the sums fit where the codes were");
   extern __shared__ __align__(16) unsigned char lds[];
   float2* const scales = reinterpret_cast<float2*>(lds + L::CODES);
   unsigned char* const acts = lds + L::CODES + L::SCALES;
