@@ -495,7 +495,7 @@ int mhc_site_pre_bwd(const void* x, const unsigned char* x_scales, const float* 
  * Arguments:
  *   y [T][H] fp32; in the gradient fp32 with y_scales NULL, or the codes and scales of
  *     its 8-bit checkpoint (mhc_f8_encode)
- *   nw [H]; norm_eps > 0 and finite
+ *   nw [H]; norm_eps at least 2^-126 and finite (MHC_EINVAL)
  *   z, z_type and dz, dz_type   MHC_F32 or MHC_BF16 (z rounded to nearest even)
  *   x, post, comb, T, streams, hidden   as mhc_site_post; in the gradient x as in
  *     mhc_site_post_bwd

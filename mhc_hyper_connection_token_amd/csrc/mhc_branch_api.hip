@@ -1,5 +1,6 @@
 // mhc_branch_api.hip -- the C ABI of the norms around a branch, their gradients and the
 // 4-bit groups (declared in include/mhc.h): argument checks and kernel launches.
+#include <cfloat>
 #include <cmath>
 
 #include "mhc.h"
@@ -29,7 +30,8 @@ size_t type_size(int t) { return t == MHC_F32 ? 4 : 2; }
 
 int check_norm(int T, int streams, int hidden, float eps) {
   if (int rc = check_shape(T, streams, hidden)) return rc;
-  if (!(eps > 0.0f) || !std::isfinite(eps)) return MHC_EINVAL;
+  // (the reciprocal root takes numbers under the smallest normal one for zero)
+  if (!(eps >= FLT_MIN) || !std::isfinite(eps)) return MHC_EINVAL;
   return hidden > kMaxNormHidden ? MHC_EUNSUPPORTED : MHC_OK;
 }
 

@@ -32,3 +32,24 @@ def test_an_activation_is_not_read_without_a_gate(mhc, how):
     got = mhc.site_post_norm_bwd(g, x, f, nw, post, comb, gate_act=how)
     assert want[5] is None and got[5] is None
     assert all(map(torch.equal, got[:5], want[:5]))
+
+
+def test_rows_of_zeros_with_the_smallest_epsilon(mhc):
+    """A row without a square is a row of zeros, whatever the epsilon, and its gradient is the
+    incoming one times nw / sqrt(eps)."""
+    print("[case] zero rows", flush=True)
+    T, S, H = 6, 2, 260
+    r = _rand(2)
+    nw, post, comb, g = r(H), r(T, S), r(T, S, S), r(T, S, H)
+    y = torch.zeros(T, H, device="cuda")
+    x = r(T, S, H)
+    for eps in (2.0 ** -126, 1e-30, 1e-5):
+        assert not mhc.branch_norm(y, nw, eps).any()
+        dz = r(T, H)
+        dy, dnw = mhc.branch_norm_bwd(dz, y, nw, eps)
+        want = dz.double() * nw.double() / eps ** 0.5
+        assert ((dy.double() - want).abs() <= 1e-6 * want.abs()).all() and not dnw.any()
+        assert torch.equal(mhc.site_post_norm(x, y, nw, post, comb, eps),
+                           mhc.site_post(x, y, post, comb))
+        got = mhc.site_post_norm_bwd(g, x, y, nw, post, comb, eps)
+        assert all(torch.isfinite(t).all() for t in got[:5]) and not got[2].any() and not got[4].any()
