@@ -40,27 +40,25 @@ __global__ __launch_bounds__(64 * NW) void post_norm_bwd_kernel(PostNormBwd p, i
   float4 dw[Q], dg[Q];
 #pragma unroll
   for (int i = 0; i < Q; ++i) dw[i] = dg[i] = zero4();
-  // What of the next token is asked for while this one's sums are added up: the first EARLY
-  // quads of each thread, past the row's end its last ones.  us for 0, 1 and 2 of them: 4096
-  // tokens of 4 x 4096 159, 147 and 152 with an 8-bit state, 167, 177 and 169 in fp32; 8192
-  // of 4 x 512 56, 56 and 64.
-  constexpr int EARLY = X == kF32 && NW > 1 && S <= 4 ? 2 : 1;
-  float4 gn[EARLY][S];
-  Raw<X> xn[EARLY][S];
-  Raw<F> fn[EARLY];
-  Raw<gate_kind<GATE>()> an[EARLY];
+  // What of the next token is asked for while this one's sums are added up: the first quad of
+  // each thread, past the row's end its last one.  us for none, one and two of them: 4096 tokens
+  // of 4 x 4096 157, 147 and 151 with an 8-bit state and a bf16 gate, in fp32 186, 171 and 173
+  // with a gate, 176, 170 and 164 without; 1024 of 4 x 7168 in fp32 82, 81 and 105 without (two
+  // quads are kept in scratch there: 130 registers of some forms), 100, 122 and 144 with a gate a
+  // token; 8192 of 4 x 512 59, 56 and 60.
+  float4 gn[S];
+  Raw<X> xn[S];
+  Raw<F> fn;
+  Raw<gate_kind<GATE>()> an;
   auto fetch = [&](size_t t) {
+    const int q = min((int)threadIdx.x, HQ - 1);
 #pragma unroll
-    for (int i = 0; i < EARLY; ++i) {
-      const int q = min((int)threadIdx.x + NT * i, HQ - 1);
+    for (int k = 0; k < S; ++k) gn[k] = nt_load4(p.g + ((t * S + k) * HQ + q) * 4);
+    fn = load_raw<F>(p.f, p.f_scales, t, HQ, KB, q);
+    if constexpr (GATE != kNoGate)
+      an = load_raw<gate_kind<GATE>()>(p.gate, nullptr, p.gate_rows ? t : 0, HQ, 0, q);
 #pragma unroll
-      for (int k = 0; k < S; ++k) gn[i][k] = nt_load4(p.g + ((t * S + k) * HQ + q) * 4);
-      fn[i] = load_raw<F>(p.f, p.f_scales, t, HQ, KB, q);
-      if constexpr (GATE != kNoGate)
-        an[i] = load_raw<gate_kind<GATE>()>(p.gate, nullptr, p.gate_rows ? t : 0, HQ, 0, q);
-#pragma unroll
-      for (int j = 0; j < S; ++j) xn[i][j] = load_raw<X>(p.x, p.x_scales, t * S + j, HQ, KB, q);
-    }
+    for (int j = 0; j < S; ++j) xn[j] = load_raw<X>(p.x, p.x_scales, t * S + j, HQ, KB, q);
   };
   fetch(blockIdx.x);
   int at = 0;
@@ -84,13 +82,13 @@ __global__ __launch_bounds__(64 * NW) void post_norm_bwd_kernel(PostNormBwd p, i
       if (q >= HQ) continue;
       float4 gv[S];
       Raw<X> xr[S];
-      if (i < EARLY) {
-        fr[i] = fn[i < EARLY ? i : 0];
-        if constexpr (GATE != kNoGate) gr[i] = an[i < EARLY ? i : 0];
+      if (i == 0) {
+        fr[0] = fn;
+        if constexpr (GATE != kNoGate) gr[0] = an;
 #pragma unroll
         for (int k = 0; k < S; ++k) {
-          gv[k] = gn[i < EARLY ? i : 0][k];
-          xr[k] = xn[i < EARLY ? i : 0][k];
+          gv[k] = gn[k];
+          xr[k] = xn[k];
         }
       } else {
 #pragma unroll

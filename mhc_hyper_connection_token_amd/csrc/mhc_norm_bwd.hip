@@ -12,7 +12,7 @@
 // parts up, in an order fixed by the shape.  HBM-bound: branch_norm_bwd of 1001 x 7168 in fp32
 // 22 us (3.9 TB/s, the parts not counted), 4096 x 4096 in fp32 37 (5.4), from an 8-bit y and
 // a bf16 gradient 30 (3.9); site_post_norm_bwd of 4096 tokens of 4 x 4096 with an 8-bit state, a
-// bf16 branch and gate 146 us (5.5), in fp32 169 (5.6), 1024 of 8 x 7168 149 (4.1: the sums of
+// bf16 branch and gate 146 us (5.5), in fp32 171 (5.5), 1024 of 8 x 7168 149 (4.1: the sums of
 // eight streams take the registers that would hide the loads).
 #include "mhc_norm_bwd.h"
 
