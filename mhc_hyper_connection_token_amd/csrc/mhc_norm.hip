@@ -172,7 +172,11 @@ template <int S, int F, int GATE>
 void launch_post_norm_g(const PostNorm& p, int T, int HQ, float eps, hipStream_t st) {
   if (HQ <= 256)
     launch_post_norm_at<S, F, GATE, 256, 1, false>(p, T, HQ, eps, st);
-  else if (T <= 128)
+  else if (T <= (S > 4 || HQ <= 512 ? 64 : 24))
+    // several blocks a token while they are few, us so and with one block, bf16 branch and gate: 4
+    // streams of 4096 at 12, 24, 48 and 128 tokens 3.5 / 4.4, 4.9 / 4.9, 5.9 / 5.6, 7.8 / 6.6, of
+    // 2048 at 48 and 192 3.9 / 4.1, 5.9 / 5.4; 8 of 4096 at 32, 64 and 96 6.6 / 8.1, 7.9 / 8.9, 9.8
+    // / 9.5, of 7168 at 96 and 128 14.6 / 15.3, 17.7 / 16.1
     launch_post_norm_at<S, F, GATE, 256, 1, true>(p, T, HQ, eps, st);
   else if (HQ <= 1024)
     launch_post_norm_at<S, F, GATE, 512, 2, false>(p, T, HQ, eps, st);
