@@ -73,9 +73,11 @@ hipError_t launch_branch_norm(const float* y, const float* nw, int T, int H, flo
     launch_branch_norm_at<1, 1>(y, nw, T, HQ, eps, z, bf16, st);
   else if (HQ <= 256)
     launch_branch_norm_at<1, 4>(y, nw, T, HQ, eps, z, bf16, st);
-  else if (HQ <= 1024 && T >= 1024)
-    // more of a row in each thread, where tokens fill the chip: 4096 x 4096 to bf16 18.5 us,
-    // with four waves 20.3; one token 3.2 and 2.6
+  else if (HQ <= 1024 && T > 2048)
+    // more of a row in each thread, where the tokens' blocks of four waves no longer fit the chip
+    // together; us with two and four waves: 1024, 2048, 2304 and 4096 tokens of 4096 to bf16 7.8 /
+    // 6.8, 11.2 / 10.8, 12.1 / 12.8, 19.3 / 20.4, of 1028 3.7 / 3.5, 4.9 / 4.8, 5.2 / 5.6, 7.0 /
+    // 7.8; one token 3.2 / 2.6
     launch_branch_norm_at<2, 8>(y, nw, T, HQ, eps, z, bf16, st);
   else if (HQ <= 1024)
     launch_branch_norm_at<4, 4>(y, nw, T, HQ, eps, z, bf16, st);

@@ -34,6 +34,19 @@ def test_norm_gradient_of_bf16_and_an_fp32_row(mhc, T, H):
     _within(dnw, w_dnw, (T + RINV + 4) * ULP * size, "dnw")
 
 
+@pytest.mark.parametrize("T,H", [(2048, 1028), (2049, 1028), (2050, 4096), (2048, 4096)])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_norm_on_both_sides_of_its_rule(mhc, T, H, bf16):
+    """Up to 2048 tokens four waves hold a row, past it two."""
+    print(f"[case] branch_norm T={T} H={H} bf16={bf16}", flush=True)
+    r = _rand(T + H)
+    y, nw = r(T, H) * torch.exp(r(T, 1)), 1 + 0.2 * r(H)
+    y[T // 2] = 0
+    got = mhc.branch_norm(y.cuda(), nw.cuda(), EPS, dtype=torch.bfloat16 if bf16 else None)
+    want = bf.branch(y.double(), nw.double(), EPS64)
+    _within(got, want, want.abs() * ((RINV + 3) * ULP + (2.0 ** -8 * 1.01 if bf16 else 0)), "z")
+
+
 # A wave's rows, a block's up to 4096 and beyond; up to four streams and more; tokens that
 # follow one another in a block (more than 1024 short ones or 256 long ones) and that do not.
 SHAPES = [(9, 4, 260), (1100, 2, 132), (30, 6, 516), (7, 3, 1028), (270, 4, 1028), (6, 8, 2052),
@@ -46,7 +59,9 @@ def _gate_of(n):
     return ("channel", "token")[n % 2], (None, "sigmoid", "silu")[n // 2 % 3]
 
 
-@pytest.mark.parametrize("T,S,H", SHAPES + [(200, 1, 2052), (130, 7, 1028), (140, 4, 5000)])
+@pytest.mark.parametrize("T,S,H", SHAPES + [(200, 1, 2052), (130, 7, 1028), (140, 4, 5000),
+                                            (24, 4, 4096), (25, 4, 4096), (64, 8, 4100),
+                                            (65, 8, 4100), (64, 3, 2048), (65, 3, 2048)])
 @pytest.mark.parametrize("f_kind", ["f32", "bf16"])
 @pytest.mark.parametrize("gate_kind", GATES)
 def test_post_mix(mhc, T, S, H, f_kind, gate_kind):
