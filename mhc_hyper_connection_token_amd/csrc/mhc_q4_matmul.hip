@@ -900,6 +900,16 @@ void launch_q4_rows(const Q4Args& p, hipStream_t st) {
   hipLaunchKernelGGL((q4_rows_kernel<A, GS, FEW, NF, W>), dim3((p.N + 16 * NF - 1) / (16 * NF)),
                      dim3(64 * W), lds, st, p);
 }
+// Columns and waves of a block: one block of 16 columns a unit up to 4096, and long stages of
+// sixteen waves up to 8192; past that eight waves, two blocks a unit, and with fp32 planes, many
+// columns in bf16 or very many in int8 the activations staged for 64 columns instead of 32.  us at
+// K = 4096 in (16 columns, 16 waves) / (32, 16) / (32, 8) / (64, 8), fp32 past four rows in 8
+// waves all: 8 rows in bf16 4096 6.1 / 7.3 / 7.3 / 9.2, 8192 10.4 / 8.5 / 8.1 / 9.9, 12288 14.5 /
+// 13.8 / 11.0 / 10.6, 16384 18.5 / 15.1 / 12.1 / 11.6; 16 rows in bf16 8192 12.5 / 9.5 / 10.2 /
+// 11.0, 65536 - / 56 / 44 / 42; in fp32 8192 24.8 / 16.5 / 16.7 / 16.9, 12288 34.8 / 27.9 / 27.9 /
+// 17.5; in int8 16384 21.5 / 17.5 / 13.9 / 14.1, 65536 - / 58 / 42 / 49; 2 rows in bf16 8192 8.8 /
+// 7.5 / 6.9 / 8.9, 24576 21.3 / 17.8 / 15.0 / 17.5, in int8 16384 15.7 / 13.0 / 10.3 / 11.1, 65536
+// - / 41 / 30 / 28.
 template <int A, int GS, bool FEW>
 void launch_q4_few(const Q4Args& p, hipStream_t st) {
   constexpr int W = A == kActF32 && !FEW ? 8 : 16;  // 16 rows' planes of 16 superblocks: 197 KB
@@ -907,9 +917,9 @@ void launch_q4_few(const Q4Args& p, hipStream_t st) {
     launch_q4_rows<A, GS, FEW, 1, W>(p, st);
   else if (p.N <= 8192)
     launch_q4_rows<A, GS, FEW, 2, W>(p, st);
-  else if (p.N < 16384)
+  else if (A == kActQ8 ? !FEW || p.N < 28672 : FEW || (A == kActBF16 && p.N < 16384))
     launch_q4_rows<A, GS, FEW, 2, 8>(p, st);
-  else
+  else if constexpr (FEW == (A == kActQ8))
     launch_q4_rows<A, GS, FEW, 4, 8>(p, st);
 }
 template <int A, int GS, int R, int W>

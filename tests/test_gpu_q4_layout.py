@@ -73,3 +73,26 @@ def test_encode_and_decode(mhc, group, zeros):
         np.testing.assert_array_equal(kept[0].cpu().numpy(), _pack(c))
         assert (kept[1] == 1).all() and (not zeros or (kept[2] == 6).all())
         np.testing.assert_array_equal(mhc.q4_decode(*kept, cols=K).cpu().numpy(), w)
+
+
+@pytest.mark.parametrize("M", [2, 4, 5, 16])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "q8"])
+def test_product_of_many_columns(mhc, M, kind):
+    """On both sides of the numbers of columns where a block's shape changes."""
+    for N in (4096, 4097, 8192, 8193, 16383, 16384, 28671, 28672):
+        print(f"[case] columns M={M} N={N} {kind}", flush=True)
+        g = np.random.default_rng(M + N)
+        K, group = 96, 32
+        c = g.integers(0, 16, (N, K)).astype(np.uint8)
+        d = (2.0 ** g.integers(-2, 3, (N, K // group))).astype(np.float32)
+        z = g.integers(0, 16, (N, K // group)).astype(np.uint8)
+        a = g.integers(-3, 4, (M, K)).astype(np.float32)
+        t = torch.from_numpy(a).cuda()
+        if kind == "bf16":
+            t = t.bfloat16()
+        elif kind == "q8":
+            t = t.to(torch.int8), torch.ones(M, K // 32, device="cuda")
+        got = mhc.q4_matmul(t, torch.from_numpy(_pack(c)).cuda(),
+                            torch.from_numpy(d).bfloat16().cuda(), torch.from_numpy(z).cuda())
+        np.testing.assert_array_equal(got.double().cpu().numpy(),
+                                      a.astype(np.float64) @ _values(c, d, z, group).T)
