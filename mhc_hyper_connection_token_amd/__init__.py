@@ -1035,7 +1035,8 @@ def q4_encode(w, *, group: int = 128, zeros: bool = False, out=None, stream=None
     """4-bit groups of a weight w [N, K] (float32 or bfloat16; include/mhc.h, "4-bit groups"):
     (codes [N, K/2] uint8, scales [N, ceil(K/group)] bfloat16); with zeros=True a zero point
     for each group as well, uint8 like the scales.  group is 32, 64 or 128.  Byte j of 16 codes
-    holds column j of 32 in its low half and column 16 + j in its high half.  `out` may supply the tuple that the call returns."""
+    holds column j of 32 in its low half and column 16 + j in its high half.  `out` may supply
+    the tuple that the call returns."""
     import torch
     if not isinstance(w, torch.Tensor):
         raise TypeError("w must be a torch.Tensor")

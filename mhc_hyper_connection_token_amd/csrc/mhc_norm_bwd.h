@@ -176,6 +176,9 @@ void launch_post_norm_bwd_g(const PostNormBwd& p, int T, int HQ, int KB, float e
                             int n, float* gate_part, hipStream_t st) {
 #define MHC_NORM(W, Q) \
   post_norm_bwd_kernel<S, X, F, GATE, W, Q><<<n, 64 * W, 0, st>>>(p, T, HQ, KB, eps, part, gate_part)
+  // (Rows past 4096 still take more registers than there are in 14 of 18 forms at four streams,
+  // 2 to 50 of them, and in 5 at eight, 2 to 42; 1024 tokens of 4 x 7168 in fp32 with a gate a
+  // token 123 us, without a gate, which fits, 81.)
   if (HQ * 4 <= kOneWaveHidden)
     MHC_NORM(1, 4);
   else if constexpr (S > 4)  // the sums of many streams leave 512 threads too few registers:

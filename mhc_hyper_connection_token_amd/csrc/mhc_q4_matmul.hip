@@ -81,21 +81,26 @@ __device__ __forceinline__ void store_one(const Q4Args& p, size_t at, float v) {
 // them, the block's 16 bytes of each: R rows at a time, `iters` times, the next R on their
 // way.  A wave's 64 lanes cover 2048 columns; the block's W waves are KS slices of the depth
 // times W / KS runs of R * iters rows, whose sums meet in LDS.  us at 4096 x 4096, 16384 x 4096
-// and 28672 x 7168 (int8; bf16; bf16): 4.2, 9.3, 24.0 (4.5 TB/s); fp32 10.0 at the second, 10.4
-// with 64-column groups and zero points.
+// and 28672 x 7168 (int8; bf16; bf16): 4.2, 9.3, 24.4 (4.4 TB/s); fp32 9.3 at the second, 9.8
+// with 64-column groups and zero points.  What is left
+// above a plain read is the conversion and the products (2 instructions a weight) that the loads
+// do not hide, and the first loads' latency.  R = 2, 4, 8: 9.8, 10.3, 12.3 at 16384 x 4096 in bf16,
+// 8.5, 8.8, 8.9 in int8.
 constexpr int kVectorRows = 64;  // rows of a wave at most
 
 template <int A, int GS, bool ZEROS, int R, int W>
 __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int iters) {
   __shared__ float part[W][kVectorRows];
-  __shared__ floatx4 turn[A == kActF32 ? W : 1][A == kActF32 ? 64 * 5 : 1];
+  __shared__ floatx4 turn[A == kActF32 ? W : 1][A == kActF32 ? 64 * 9 : 1];  // (by slice)
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int KB = p.K / kQ4Block;
   const int slice = wave % KS, runs = W / KS, rows = R * iters;
   const int n0 = (blockIdx.x * runs + wave / KS) * rows;
   const size_t pitch = (size_t)KB * 16;
-  for (int k0 = slice * 64; k0 < KB; k0 += KS * 64) {
+  for (int b0 = 0; b0 < KB; b0 += KS * 64) {
+    const int k0 = b0 + slice * 64;
+    if (A != kActF32 && k0 >= KB) break;
     // lanes past the end read the last block, times zeros
     const int k = min(k0 + lane, KB - 1);
     const bool in = k0 + lane < KB;
@@ -121,28 +126,28 @@ __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int
     float av[32], ad = 0.f, as = 0.f;
     int qs = 0;
     if constexpr (A == kActF32) {
-      // asked for in whole half blocks, four lanes each, and turned about in LDS (a lane's own
-      // 128 bytes at a time are 64 lines a load: 4.9 -> 6.4 us at 4096 x 4096)
-      floatx4 v[2][4];
+      // The waves of a slice share its activations: each asks for a part of them, in whole
+      // blocks, and all of them lie in LDS then.  us at 4096 x 4096, 7168 x 7168 and 16384 x 4096
+      // so 5.1, 9.9 and 9.3; with a wave's own turned about in LDS 5.1, 10.6 and 9.9; with loads
+      // of a lane's own 128 bytes, 64 lines each, 6.4, 11.0 and 10.8.
+      const int run = wave / KS;
+      if (b0 > 0) __syncthreads();
+      floatx4 v[8];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int i = 0; i < 8; ++i)
+        if (i * runs < 8)
+          v[i] = reinterpret_cast<const floatx4*>(
+              p.a)[min(k0 + 8 * (i * runs + run) + (lane >> 3), KB - 1) * 8 + (lane & 7)];
+      if (k0 < KB) fetch(n0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[h][i] = reinterpret_cast<const floatx4*>(p.a)[min(k0 + 16 * i + (lane >> 2), KB - 1) * 8 +
-                                                         4 * h + (lane & 3)];
-      fetch(n0);
+      for (int i = 0; i < 8; ++i)
+        if (i * runs < 8) turn[slice][(8 * (i * runs + run) + (lane >> 3)) * 9 + (lane & 7)] = v[i];
+      __syncthreads();
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      for (int i = 0; i < 8; ++i) {
+        const floatx4 u = turn[slice][lane * 9 + i];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) turn[wave][(16 * i + (lane >> 2)) * 5 + (lane & 3)] = v[h][i];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const floatx4 u = turn[wave][lane * 5 + i];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) av[16 * h + 4 * i + e] = in ? u[e] : 0.f;
-        }
+        for (int e = 0; e < 4; ++e) av[4 * i + e] = in ? u[e] : 0.f;
       }
     } else {
       Octet<A> ao[4];
@@ -174,6 +179,7 @@ __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int
         as += u;
       }
     }
+    if (k0 >= KB) continue;  // (this wave, but for the barriers)
     for (int it = 0; it < iters; ++it) {
       intx4 cv[R];
       float sv[R], zv[R];
@@ -219,7 +225,7 @@ __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           float* to = &part[wave][R * it + i];
-          *to = k0 == slice * 64 ? acc[i] : *to + acc[i];
+          *to = b0 == 0 ? acc[i] : *to + acc[i];
         }
     }
   }
@@ -242,9 +248,9 @@ __global__ __launch_bounds__(64 * W) void q4_vector_kernel(Q4Args p, int KS, int
 // ahead on, in whole lines (a wave's load is 1 KB of one row).  Sixteen rows read straight
 // into the instructions' layout instead are sixteen lines a load, for the two bytes of a
 // scale as well, and every wave loads the activations again.
-// us at 2, 8 and 16 rows of 16384 x 4096: bf16 10.7 (3 rows), 11.7, 12.5; fp32 11.1, 15.3,
-// 18.4; int8 10.7, 13.2, 13.6; with the activations read by every wave 16.6 at 8 rows in
-// bf16.  What is left above the floor: two barriers a stage of 1024 columns, 700 clocks each.
+// us at 2, 8 and 16 rows of 16384 x 4096: bf16 10.1, 11.6, 12.5; fp32 11.0, 15.4, 18.6; int8
+// 10.2, 13.0, 14.0; with the activations read by every wave 16.6 at 8 rows in bf16.  What is
+// left above the floor: two barriers a stage of 1024 columns, 700 clocks each.
 // A row, of codes and of activations, is 16 bytes longer than it needs, so that sixteen rows
 // read at one place meet all banks.
 // Which four octets (mhc_q4.h) an instruction sums: of a superblock's sixteen, lane group g
@@ -559,9 +565,11 @@ __global__ __launch_bounds__(64 * W) void q4_rows_kernel(Q4Args p) {
 // The 16-byte units of a row are placed so that sixteen rows read at one unit meet all banks.
 // What bounds it: a stage of a 128 x 128 tile in bf16 takes 4000 clocks of its unit, of which
 // the matrix instructions fill 1030, the vector ones (staging and sums 700, conversion to bf16
-// and scaling the rest) 1680 and LDS 1240; two waves a SIMD, all its registers allow, leave a
-// third of the time to waits.  Memory is not it: with two stages on their way instead of one
-// 97 and 98 us at 333 x 7168 x 7168.
+// and scaling the rest) 1680 and LDS 1240; two waves a SIMD leave a third of the time to waits.
+// Its 85 KB of LDS keep it to one block a unit (150 registers would allow three waves), the 96 x
+// 128 tile's 137 KB and 248 registers as well.  fp32 and int8 multiply three planes, whose
+// tiles of more than 32 rows have one buffer only. Memory is not it: with two stages on their way
+// instead of one 97 and 98 us at 333 x 7168 x 7168 (then with tiles of 32 x 128).
 template <int A, int GS, int FM, int FN, int WM, int WN, int KG>
 struct TileLayout {
   static constexpr int PL = A == kActBF16 ? 1 : 3, NG = 4 >> GS;
@@ -940,14 +948,17 @@ void launch_q4_vector(const Q4Args& p, hipStream_t st) {
                        iters);
 }
 // Tiles by the rounds of 256 blocks they take: the smallest that need one, with several groups
-// of waves on each; us in 32 x 64 / 32 x 128 / 64 x 128 / 128 x 128: 48 x 7168 x 7168 26 / 35 /
-// 50 / 83, 64 x 16384 x 4096 30 / 23 / 32 / 49, 100 x 7168 x 7168 46 / 35 / 51 / 88, 128 x
-// 16384 x 4096 56 / 41 / 34 / 52, 512 x 4096 x 4096 56 / 39 / 33 / 52.  Past one round a tile's
-// cost goes with its size, nearly, and small ones waste less of the last round: 32 x 128, 96 x
-// 128 and 128 x 128 take 96, 75 and 96 us at 333 x 7168 x 7168, 121, 123 and 105 at 512 x 16384 x
-// 4096, 46, 44 and 52 at 288 x 9000 x 4096.  In fp32 (three planes of 96 rows do not fit twice)
-// 181, 238 and 190 at the first; the two ends 187 and 157 at 512 x 8192 x 4096, groups of 32.
-// Where the rule is off: 384 x 8192 x 4096, groups of 64, 70 instead of 65.
+// of waves on each; us in bf16 in 32 x 64 / 32 x 128 / 64 x 128 / 128 x 128: 48 x 7168 x 7168 25
+// / 35 / 48 / 82, 64 x 16384 x 4096 29 / 23 / 30 / 49, 100 x 7168 x 7168 44 / 34 / 49 / 87, 128 x
+// 16384 x 4096 54 / 34 / 32 / 52, 512 x 4096 x 4096 53 / 34 / 32 / 52; in fp32 and int8 at 64 x
+// 16384 x 4096 58 / 41 / 64 / 106 and 49 / 35 / 57 / 107, at 128 x 16384 x 4096 108 / 73 / 67 /
+// 109 and 91 / 67 / 62 / 107. Past one round a tile's cost goes with its size, nearly, and small
+// ones waste less of the last round: in bf16 32 x 128, 96 x 128 and 128 x 128 take 78, 69 and 89
+// us at 333 x 7168 x 7168 (groups of 64: 95, 82, 108), 99, 130 and 90 at 500 rows, 118, 121 and
+// 105 at 512 x 16384 x 4096, 47, 42 and 51 at 288 x 9000 x 4096, 64, 54 and 65 at 384 x 8192 x
+// 4096 in groups of 64. In fp32 (three planes of 96 rows do not fit twice) and int8 the two ends
+// are 181, 190 and 149, 185 at the first, 241, 192 and 201, 187 at 500 rows, 104, 110 and 88, 109
+// at 288 x 9000 x 4096.
 template <int A, int GS>
 void launch_q4_tiles(const Q4Args& p, hipStream_t st) {
   auto blocks = [&](long bm, long bn) {
